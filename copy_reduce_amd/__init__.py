@@ -1,7 +1,9 @@
 """copy_reduce_amd: the MI355X (gfx950) transfer hot path behind a C ABI.
 
     libtb.so (include/tb.h)      hand-written HIP kernels + host checks
+                                 (include/tb_cache.h: the paged key/value cache)
     copy_reduce_amd._tb          ctypes binding, same names as the C calls
+    copy_reduce_amd._tb_cache    the same for tb_cache.h
     copy_reduce_amd.torch_api    torch-tensor conveniences (device memory and
                                  streams only; every step runs in libtb)
 
@@ -15,4 +17,7 @@ from ._tb import (  # noqa: F401
     tb_reduce_copy, tb_ring_create, tb_ring_destroy, tb_ring_poll, tb_ring_submit, tb_ring_wait, tb_rotate_sources,
     tb_shutdown, tb_slice_stride, tb_spin_gate_arm, tb_spin_gate_release, tb_spin_gate_status, tb_status_string,
     tb_time_next_launch, tb_batched_set_max_workgroups,
+)
+from ._tb_cache import (  # noqa: F401
+    TB_CACHE_BUSY, TB_CACHE_RANGE, TB_CACHE_SHARED, TB_CACHE_SHORT, TB_CACHE_TWICE, TB_MAX_POOLS,
 )

@@ -17,7 +17,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtb.so")
 ARCH = "gfx950"
 
-SOURCES = ["tb_host.cpp", "tb_gen.cpp", "tb_ring.cpp", "tb_kernels.hip"]
+SOURCES = ["tb_host.cpp", "tb_gen.cpp", "tb_ring.cpp", "tb_kernels.hip",
+           "tb_cache.cpp", "tb_cache_kernels.hip", "tb_attention.hip"]
 # The measuring instruments of bench.py --roofs: a library of their own.
 ROOFS_SOURCES = ["tb_roofs.hip"]
 ROOFS_LIB = os.path.join(PKG, "libtb_roofs.so")

@@ -78,6 +78,22 @@ int device_info(DeviceInfo *out) {
     return TB_OK;
 }
 
+}  // namespace
+
+namespace tbh {
+
+int cu_count_of_device(int *out) {
+    DeviceInfo info;
+    const int rc = device_info(&info);
+    if (rc == TB_OK)
+        *out = info.cu_count;
+    return rc;
+}
+
+}  // namespace tbh
+
+namespace {
+
 // Batched-copy scratch, one per (device, stream), zeroed once at allocation,
 // with the epoch of the last launch made on it.  Launches on one scratch must
 // reach their stream in epoch order (each clears what the next one uses), so

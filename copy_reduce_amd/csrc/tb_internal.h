@@ -149,6 +149,9 @@ namespace tbh {
 // Record `what` and e's text for tb_last_hip_error(); returns TB_ERR_HIP.
 int hip_fail(hipError_t e, const char *what);
 
+// Compute units of the current device (TB_OK, or the error to return).
+int cu_count_of_device(int *out);
+
 // The TB_BC_* mode last set by tb_batched_set_mode.
 int batched_mode();
 

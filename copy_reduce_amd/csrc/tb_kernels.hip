@@ -6,11 +6,11 @@
 #include <atomic>
 #include <mutex>
 
-#include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "tb_internal.h"
+#include "tb_launch.h"
 
 namespace tbk {
 
@@ -430,37 +430,9 @@ int reduce_grid(uint64_t nfloats, int nsrc, bool vector_path, int cu_count) {
     return (int)(g > 0 ? g : 1);
 }
 
-// Events the next launch made by this host thread records as part of the
-// launch itself (set by tb_time_next_launch; consumed by that launch).
-static thread_local hipEvent_t t_next_start = nullptr;
-static thread_local hipEvent_t t_next_stop = nullptr;
-
 void set_next_launch_events(hipEvent_t start, hipEvent_t stop) {
     t_next_start = start;
     t_next_stop = stop;
-}
-
-// Every kernel of the library is launched here.  With events (the timing hook,
-// or `done` from the caller), the launch carries them as its own start / stop
-// events, so no separate event command sits between kernels.  A launch has
-// one stop event: when `done` takes it (a ring slot's completion event) and
-// the timing hook also set one, the hook's is recorded right after the launch
-// as a command of its own, so it too fires when the kernel has completed.
-template <typename... KArgs, typename... Args>
-static hipError_t launch(void (*kernel)(KArgs...), int grid, int block, hipStream_t s, hipEvent_t done,
-                         Args... args) {
-    const hipEvent_t start = t_next_start;
-    const hipEvent_t hook_stop = t_next_stop;
-    const hipEvent_t stop = done != nullptr ? done : hook_stop;
-    t_next_start = t_next_stop = nullptr;
-    if (start != nullptr || stop != nullptr)
-        hipExtLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, start, stop, 0u, args...);
-    else
-        hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && done != nullptr && hook_stop != nullptr)
-        e = hipEventRecord(hook_stop, s);
-    return e;
 }
 
 template <int N>

@@ -7,13 +7,18 @@ host memory and streams; every step of the path runs in libtb.
     make_desc        (src_off, dst_off, bytes) offsets -> device tb_copy_desc array
     batched_copy     tb_batched_copy on a device descriptor tensor
     DescRing         tb_ring_* (descriptor-slot ring) over host descriptor arrays
+    PagedCache       a paged key/value cache: tb_page_* over tensors
+    tree_attention   tb_tree_attention of drafted tokens over a PagedCache
 """
-from typing import List, Optional, Sequence
+import ctypes
+import math
+from contextlib import nullcontext
+from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
 
-from . import _tb
+from . import _tb, _tb_cache
 
 
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -140,3 +145,232 @@ class DescRing:
 
     def __exit__(self, *exc):
         self.close()
+
+
+_NO_CONTEXT = nullcontext()
+
+
+def _list_arg(t: torch.Tensor, n: Optional[int], device: torch.device, what: str) -> int:
+    """Address of an int32 index list on the cache's device."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 1
+            or not t.is_contiguous() or (n is not None and t.shape[0] != n)):
+        raise ValueError(f"{what} must be a contiguous one-dimensional int32 tensor on {device}"
+                         + ("" if n is None else f" of {n} entries"))
+    return t.data_ptr()
+
+
+class PagedCache:
+    """A paged key/value cache over tensors (include/tb_cache.h).
+
+    pools        a tensor [npools, num_pages, ...] or a sequence of tensors
+                 [num_pages, ...]: keys of layer l in pool 2 l, values in 2 l + 1.
+                 A page is [page_tokens, heads, head_dim] (layout "token") or
+                 [heads, page_tokens, head_dim] (layout "head"), contiguous.
+    max_seqs     rows of the table, each of max_pages pages
+    state        an int32 tensor of state_words() words with a state to go on
+                 from; by default a new one, empty
+
+    table, lens, refs, free_list and counts are views of `state`, on the device:
+    copying `state` keeps the whole bookkeeping.  Index lists are contiguous
+    int32 tensors on the cache's device; a negative entry is padding.  Every
+    call only enqueues on the current stream of the cache's device, or on `stream`;
+    the caller orders calls on one cache.  What a listed entry asked for and
+    could not have shows in counts[1] (TB_CACHE_* bits, see flags())."""
+
+    def __init__(self, pools: Union[torch.Tensor, Sequence[torch.Tensor]], page_tokens: int, max_seqs: int,
+                 max_pages: int, layout: str = "token", state: Optional[torch.Tensor] = None):
+        if layout not in ("token", "head"):
+            raise ValueError("layout must be 'token' or 'head'")
+        pools = list(pools)   # of a tensor: its pools
+        if not 1 <= len(pools) <= _tb_cache.TB_MAX_POOLS:
+            raise ValueError(f"a cache has 1 to {_tb_cache.TB_MAX_POOLS} pools")
+        p0 = pools[0]
+        for p in pools:
+            if (not p.is_cuda or p.device != p0.device or p.dtype != p0.dtype or p.shape != p0.shape
+                    or p.stride() != p0.stride()):
+                raise ValueError("pools must be CUDA tensors of one device, type, shape and stride")
+        if p0.dim() != 4 or p0.shape[1 if layout == "token" else 2] != page_tokens or not p0[:1].is_contiguous():
+            raise ValueError("a pool is [num_pages, page_tokens, heads, head_dim] (layout 'token') or "
+                             "[num_pages, heads, page_tokens, head_dim] (layout 'head'), pages contiguous")
+        self.pools, self.layout, self.page_tokens = pools, layout, page_tokens
+        self.num_pages, self.head_dim = p0.shape[0], p0.shape[3]
+        self.heads = p0.shape[2 if layout == "token" else 1]
+        self.max_seqs, self.max_pages = max_seqs, max_pages
+        self.device, self.dtype = p0.device, p0.dtype
+        page = page_tokens * self.heads * self.head_dim
+        words = self.state_words(self.num_pages, max_seqs, max_pages)
+        fresh = state is None
+        if fresh:
+            state = torch.empty(words, dtype=torch.int32, device=self.device)
+            state[:max_seqs * max_pages] = 0
+        elif (state.dtype != torch.int32 or state.device != self.device or state.dim() != 1
+              or not state.is_contiguous() or state.shape[0] != words):
+            raise ValueError(f"state must be a contiguous int32 tensor of {words} words on {self.device}")
+        self.state = state
+        cuts = [max_seqs * max_pages, max_seqs, self.num_pages, self.num_pages, 4]
+        table, self.lens, self.refs, self.free_list, self.counts = torch.split(state, cuts)
+        self.table = table.view(max_seqs, max_pages)
+        self._scratch = torch.zeros(_tb_cache.tb_cache_scratch_bytes(self.num_pages, max_seqs), dtype=torch.uint8,
+                                    device=self.device)
+        self._pool_ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
+        c = _tb_cache.tb_cache()
+        c.pools = ctypes.addressof(self._pool_ptrs)
+        c.npools, c.num_pages, c.page_tokens, c.heads = len(pools), self.num_pages, page_tokens, self.heads
+        c.layout = _tb_cache.TB_CACHE_TOKEN_MAJOR if layout == "token" else _tb_cache.TB_CACHE_HEAD_MAJOR
+        size = p0.element_size()
+        c.head_bytes = self.head_dim * size
+        c.page_stride = (p0.stride(0) if self.num_pages > 1 else page) * size
+        c.max_seqs, c.max_pages = max_seqs, max_pages
+        c.table, c.lens, c.refs = self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr()
+        c.free_list, c.counts = self.free_list.data_ptr(), self.counts.data_ptr()
+        c.scratch = self._scratch.data_ptr()
+        self._c = c
+        if fresh:
+            with self._there():
+                _tb_cache.tb_cache_init(c, self._stream(None))
+
+    @staticmethod
+    def state_words(num_pages: int, max_seqs: int, max_pages: int) -> int:
+        return max_seqs * max_pages + max_seqs + 2 * num_pages + 4
+
+    def _there(self):
+        """The cache's device as the current one, for the length of a call."""
+        return (_NO_CONTEXT if torch.cuda.current_device() == self.device.index
+                else torch.cuda.device(self.device))
+
+    def _stream(self, stream: Optional[torch.cuda.Stream]) -> int:
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if s.device != self.device:
+            raise ValueError(f"the stream must be one of {self.device}")
+        return int(s.cuda_stream)
+
+    def flags(self, clear: bool = False) -> int:
+        """The TB_CACHE_* bits raised so far (waits for the device)."""
+        bits = int(self.counts[1])
+        if clear:
+            self.counts[1] = 0
+        return bits
+
+    def copy_pages(self, dst_pages: torch.Tensor, src_pages: torch.Tensor, src: Optional["PagedCache"] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Copy src's pages src_pages (of this cache by default) to dst_pages, in every pool."""
+        src = self if src is None else src
+        if src.device != self.device or src.dtype != self.dtype:
+            raise ValueError("both caches must be of one device and type")
+        d = _list_arg(dst_pages, None, self.device, "dst_pages")
+        s = _list_arg(src_pages, dst_pages.shape[0], self.device, "src_pages")
+        with self._there():
+            _tb_cache.tb_page_copy(self._c, src._c, d, s, dst_pages.shape[0], self._stream(stream))
+
+    def append(self, rows: torch.Tensor, seqs: torch.Tensor, positions: torch.Tensor,
+               index: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Write rows[:, index[i]] ([npools, n, heads, head_dim]) to position positions[i] of sequence seqs[i]."""
+        if (rows.dtype != self.dtype or rows.device != self.device or rows.dim() != 4
+                or rows.shape[0] != len(self.pools) or rows.shape[2:] != (self.heads, self.head_dim)
+                or rows.stride(3) != 1 or (self.heads > 1 and rows.stride(2) != self.head_dim)):
+            raise ValueError("rows must be [npools, n, heads, head_dim] of the cache's type and device, "
+                             "each token contiguous")
+        n = seqs.shape[0]
+        q, p = _list_arg(seqs, None, self.device, "seqs"), _list_arg(positions, n, self.device, "positions")
+        x = 0 if index is None else _list_arg(index, n, self.device, "index")
+        if index is None and rows.shape[1] < n:
+            raise ValueError("rows must hold a row for each entry")
+        size = rows.element_size()
+        step = rows.stride(1) if rows.shape[1] > 1 else self.heads * self.head_dim
+        with self._there():
+            _tb_cache.tb_page_append(self._c, rows.data_ptr(), rows.shape[1], step * size, rows.stride(0) * size, q, p,
+                                     x, n, self._stream(stream))
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Make the empty sequences `children` copies of `parents`, sharing their full pages."""
+        p = _list_arg(parents, None, self.device, "parents")
+        c = _list_arg(children, parents.shape[0], self.device, "children")
+        with self._there():
+            _tb_cache.tb_page_fork(self._c, p, c, parents.shape[0], self._stream(stream))
+
+    def resize(self, seqs: torch.Tensor, lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Give the sequences `seqs` the lengths `lens`, 0 freeing one: releases pages, then takes new ones."""
+        q = _list_arg(seqs, None, self.device, "seqs")
+        n = _list_arg(lens, seqs.shape[0], self.device, "lens")
+        with self._there():
+            _tb_cache.tb_page_resize(self._c, q, n, seqs.shape[0], self._stream(stream))
+
+    def free(self, seqs: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Free whole sequences."""
+        with torch.cuda.stream(stream) if stream is not None else _NO_CONTEXT:
+            zero = torch.zeros_like(seqs)
+        self.resize(seqs, zero, stream)
+
+    def compact(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Move the pages in use to the lowest numbers."""
+        with self._there():
+            _tb_cache.tb_page_compact(self._c, self._stream(stream))
+
+
+_ATTN_TYPES = {torch.bfloat16: _tb_cache.TB_BF16, torch.float16: _tb_cache.TB_FP16}
+
+
+def tree_attention_workspace(q: torch.Tensor, cache: PagedCache) -> torch.Tensor:
+    """Workspace for tree_attention calls with queries of q's shape over `cache`, whatever the lengths.
+    One serves any number of calls that follow each other; calls that can overlap need one each."""
+    a = _tb_cache.tb_tree_attn()
+    a.batch, a.nodes, a.heads_q, a.head_dim = q.shape
+    with cache._there():
+        n = _tb_cache.tb_tree_attention_workspace(a, cache._c)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedCache, layer: int,
+                   seqs: torch.Tensor, mask: Optional[torch.Tensor] = None, nodes: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted tokens over the cache's context of `layer` and over each other.
+
+    q [batch, nodes, heads_q, head_dim]; k, v [batch, nodes, heads, head_dim] of the drafted tokens, which are
+    not in the cache.  seqs [batch]: the sequences' rows in the cache.  mask int64 [batch, nodes, ceil(nodes /
+    64)]: bit u % 64 of word u / 64 lets a node see node u (default: node t sees u <= t, so that one node is
+    ordinary decoding).  nodes int32 [batch]: how many of the nodes are real (default: all).  scale: 1 /
+    sqrt(head_dim) by default.  Returns (out, lse): out as q, lse float32 [batch, nodes, heads_q], the natural
+    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf."""
+    dtype, dev = q.dtype, cache.device
+    if dtype not in _ATTN_TYPES or cache.dtype != dtype:
+        raise ValueError("q and the cache must be both bfloat16 or both float16")
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, nodes, heads_q, head_dim]")
+    b, t, hq, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("q's head_dim must be the cache's")
+    if not 0 <= layer < len(cache.pools) // 2:
+        raise ValueError("the cache has no such layer")
+    kv_shape = (b, t, cache.heads, d)
+    for x, shape, name in ((q, q.shape, "q"), (k, kv_shape, "k"), (v, kv_shape, "v")):
+        if x.dtype != dtype or x.device != dev or x.shape != shape or x.stride(3) != 1:
+            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {dev}, head_dim contiguous")
+    sq = _list_arg(seqs, b, dev, "seqs")
+    if mask is not None and (mask.dtype != torch.int64 or mask.device != dev or mask.shape != (b, t, (t + 63) // 64)
+                             or not mask.is_contiguous()):
+        raise ValueError(f"mask must be a contiguous int64 tensor of shape {(b, t, (t + 63) // 64)} on {dev}")
+    tn = None if nodes is None else _list_arg(nodes, b, dev, "nodes")
+    with cache._there():
+        sh = cache._stream(stream)
+        with torch.cuda.stream(stream) if stream is not None else _NO_CONTEXT:
+            if out is None:
+                out = torch.empty(q.shape, dtype=dtype, device=dev)
+            elif out.dtype != dtype or out.device != dev or out.shape != q.shape or out.stride(3) != 1:
+                raise ValueError("out must have q's type, shape and device, head_dim contiguous")
+            if lse is None:
+                lse = torch.empty((b, t, hq), dtype=torch.float32, device=dev)
+            elif lse.dtype != torch.float32 or lse.device != dev or lse.shape != (b, t, hq) or not lse.is_contiguous():
+                raise ValueError("lse must be a contiguous float32 tensor [batch, nodes, heads_q]")
+            if workspace is None:
+                workspace = tree_attention_workspace(q, cache)
+            elif workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        a = _tb_cache.tb_tree_attn(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), q.stride()[:3],
+            k.stride()[:3], v.stride()[:3], out.stride()[:3], sq, None if mask is None else mask.data_ptr(), tn,
+            b, t, hq, d, _ATTN_TYPES[dtype], 2 * layer, 2 * layer + 1, 1 / math.sqrt(d) if scale is None else scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        _tb_cache.tb_tree_attention(a, cache._c, sh)
+    return out, lse
