@@ -1,7 +1,25 @@
-// tb_attention.hip -- gfx950 kernel of the attention of drafted tokens over the
+// tb_attention.hip -- gfx950 kernels of the attention of drafted tokens over the
 // paged cache.
-#include <hip/hip_bf16.h>
-#include <hip/hip_fp16.h>
+//
+// The M = nodes * (heads_q / heads) rows of one sequence that read one
+// key/value head share each of its keys, so a key costs M multiply-adds a
+// byte: up to some 200 rows the cache's bytes decide, beyond that the
+// products.  Either way every key and value goes from memory straight into the
+// registers of the one wave (or, for many rows, the few waves) that multiplies it.
+//
+// A wave owns R = 16 NT rows and walks over tiles of 32 keys with a running
+// maximum and sum.  Both products run on 16x16x32 matrix instructions and are
+// taken transposed, rows along the columns:
+//   S' = K Q'   a lane (n = lane % 16, g = lane / 16) then holds, of row n, the
+//               scores of keys 4g .. 4g+3 and 16+4g .. 16+4g+3,
+//   O' = V' P'  which are just the k-places that lane has to supply of P', so
+//               that the probabilities never leave their lane.  V' wants, for
+//               one element of the head, the values of those eight keys in one
+//               register quad: each lane loads D/16 neighbouring elements of
+//               its eight keys and pairs them up by byte permutes.  The order
+//               in which elements meet the instruction's rows is free: place n
+//               of instruction j is element n D/16 + j.
+// The statistics of row n are in the lanes with that n, as is its column of O'.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -11,116 +29,701 @@
 
 namespace tbk {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(1))) u32x4 gu32x4;
+typedef __attribute__((address_space(1))) f32x4 gf32x4;
+
+constexpr int kWaves = 4;              // waves of a workgroup
+constexpr int kTile = 32;              // keys of a tile
+constexpr uint32_t kListPages = 2048;  // page numbers of a chunk kept in LDS
+constexpr uint32_t kMinChunk = 128;    // fewest tokens a workgroup is given
+
 struct AttnArgs {
-    tb_tree_attn a;
+    const uint8_t *q, *k, *v;
+    uint8_t *out;
+    float *lse;
+    uint64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];   // bytes
+    const int32_t *seqs;
+    const uint32_t *mask;              // 32 nodes a word
+    const int32_t *tree_nodes;
     const uint8_t *k_cache, *v_cache;
     const int32_t *table, *lens;
-    uint64_t page_stride, token_step, head_step;
-    uint32_t num_pages, page_tokens, max_seqs, max_pages, heads;
+    uint32_t batch, nodes, heads_q, heads, group, rows;   // rows: nodes * group
+    uint32_t page_stride, token_step, head_step;          // bytes
+    uint32_t num_pages, page_tokens, max_seqs, max_pages;
+    uint32_t div_mul, div_shift;       // token / page_tokens = token * div_mul >> div_shift
+    uint32_t row_blocks;               // workgroups that share a head's rows
+    uint32_t budget;                   // chunks that all sequences together are cut into, one more each
+    float scale, scale2;               // |scale| log2 e; 1 for scale 0, see load_q
+    int32_t sign;                      // of scale
+    int32_t *split_base, *split_count; // [batch] workspace
+    float *part_ml;                    // [slots][rows][2]
+    float *part_o;                     // [slots][rows][D]
 };
 
-__device__ __forceinline__ float to_float(__hip_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ void from_float(float v, __hip_bfloat16 *o) { *o = __float2bfloat16(v); }
-__device__ __forceinline__ void from_float(float v, __half *o) { *o = __float2half(v); }
+template <typename T>
+struct Mfma;
+template <>
+struct Mfma<__bf16> {
+    typedef bf16x8 V;
+    static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static constexpr uint32_t kExp = 0x7f80;   // exponent bits, all set where a value is not finite
+};
+template <>
+struct Mfma<_Float16> {
+    typedef f16x8 V;
+    static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static constexpr uint32_t kExp = 0x7c00;
+};
 
-// One wave a row (sequence, node, query head): one key after the other with a
-// running maximum and sum, each lane holding ceil(D / 64) of the elements.
-template <typename T, int D>
-__global__ __launch_bounds__(64) void tree_attention_kernel(AttnArgs g) {
-    constexpr int R = (D + 63) / 64;
-    const uint32_t lane = threadIdx.x, h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-    const uint32_t kvh = h / (g.a.heads_q / g.heads);
-    const int32_t seq = g.a.seqs[b];
-    const bool there = seq >= 0 && (uint32_t)seq < g.max_seqs;
-    int32_t nodes = there ? (int32_t)g.a.nodes : 0, ctx = 0;
-    if (there) {
-        if (g.a.tree_nodes != nullptr)
-            nodes = min(max(g.a.tree_nodes[b], 0), nodes);
-        ctx = min(max(g.lens[seq], 0), (int32_t)(g.max_pages * g.page_tokens));
+// N dwords at 4-byte alignment or better, as 16-byte loads and one rest.
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t *r, uint64_t at) {
+    typedef __attribute__((address_space(1))) u32x2 gu32x2;
+    typedef uint32_t u32x3a __attribute__((ext_vector_type(3), aligned(4)));
+    typedef __attribute__((address_space(1))) u32x3a gu32x3;
+    if constexpr (N >= 4) {
+        const u32x4 x = *(const gu32x4 *)at;
+        r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+        if constexpr (N > 4)
+            load_dwords<N - 4>(r + 4, at + 16);
+    } else if constexpr (N == 3) {
+        const u32x3a x = *(const gu32x3 *)at;
+        r[0] = x.x, r[1] = x.y, r[2] = x.z;
+    } else {
+        static_assert(N == 2, "dwords");
+        const u32x2 x = *(const gu32x2 *)at;
+        r[0] = x.x, r[1] = x.y;
     }
-    if ((int32_t)t >= nodes)
-        ctx = 0, nodes = 0;
-    const T *qp = (const T *)g.a.q + b * g.a.q_stride[0] + t * g.a.q_stride[1] + h * g.a.q_stride[2];
-    float q[R], o[R];
-#pragma unroll
-    for (int r = 0; r < R; r++) {
-        q[r] = lane + 64 * r < D ? to_float(qp[lane + 64 * r]) : 0.f;
-        o[r] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const uint32_t words = (g.a.nodes + 63) / 64;
-    for (int32_t j = 0; j < ctx + nodes; j++) {
-        const T *kp, *vp;
-        if (j < ctx) {
-            uint32_t page = (uint32_t)g.table[(uint64_t)seq * g.max_pages + j / g.page_tokens];
-            page = page < g.num_pages ? page : 0;
-            const uint64_t at = page * g.page_stride + (j % g.page_tokens) * g.token_step + kvh * g.head_step;
-            kp = (const T *)(g.k_cache + at);
-            vp = (const T *)(g.v_cache + at);
-        } else {
-            const uint32_t u = j - ctx;
-            const bool sees = g.a.mask == nullptr ? u <= t
-                                                  : (g.a.mask[((uint64_t)b * g.a.nodes + t) * words + u / 64] >> (u % 64)) & 1;
-            if (!sees)
-                continue;
-            kp = (const T *)g.a.k + b * g.a.k_stride[0] + u * g.a.k_stride[1] + kvh * g.a.k_stride[2];
-            vp = (const T *)g.a.v + b * g.a.v_stride[0] + u * g.a.v_stride[1] + kvh * g.a.v_stride[2];
-        }
-        float x = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; r++)
-            if (lane + 64 * r < D)
-                x += q[r] * to_float(kp[lane + 64 * r]);
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1)
-            x += __shfl_xor(x, d);
-        x *= g.a.scale;
-        const float top = fmaxf(m, x), base = top == -INFINITY ? 0.f : top;
-        const float keep = expf(m - base), p = expf(x - base);
-        m = top;
-        l = l * keep + p;
-#pragma unroll
-        for (int r = 0; r < R; r++)
-            if (lane + 64 * r < D)
-                o[r] = o[r] * keep + p * to_float(vp[lane + 64 * r]);
-    }
-    T *op = (T *)g.a.out + b * g.a.out_stride[0] + t * g.a.out_stride[1] + h * g.a.out_stride[2];
-#pragma unroll
-    for (int r = 0; r < R; r++)
-        if (lane + 64 * r < D)
-            from_float(l == 0.f ? 0.f : o[r] / l, &op[lane + 64 * r]);
-    if (g.a.lse != nullptr && lane == 0)
-        g.a.lse[((uint64_t)b * g.a.nodes + t) * g.a.heads_q + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-uint64_t tree_attention_workspace(const tb_tree_attn &, uint32_t, int) { return 16; }
+__device__ __forceinline__ float lanes_max(float x) {   // over the lanes with the same lane % 16
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float lanes_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
 
-hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, hipStream_t stream) {
+// What a workgroup works on.
+struct Work {
+    int32_t batch;   // -1: nothing
+    int32_t split;
+    int32_t splits;
+    int32_t slot;    // number of the split among all
+    int32_t chunk;   // tokens of a split
+    int32_t seq;
+    int32_t context;
+};
+
+__device__ __forceinline__ int32_t context_of(const AttnArgs &g, uint32_t b, int32_t *seq) {
+    const int32_t q = g.seqs[b];
+    *seq = (uint32_t)q < g.max_seqs ? q : -1;
+    if (*seq < 0)
+        return 0;
+    const int32_t n = g.lens[q], most = (int32_t)(g.max_pages * g.page_tokens);
+    return n < 0 ? 0 : (n < most ? n : most);
+}
+
+// Cuts the contexts into chunks of equal length, as many as `budget` and one
+// more a sequence at most, and finds chunk number `want`.  Every workgroup does
+// the whole of it (a few loads and two sums), so nothing has to be planned
+// before the launch and the lengths stay on the device.
+__device__ __forceinline__ void find_work(const AttnArgs &g, int32_t want, Work *out, uint64_t *lds) {
+    const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int32_t seq = -1, ctx = 0;
+    uint64_t total = 0;
+    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * kWaves) {
+        ctx = b0 + t < g.batch ? context_of(g, b0 + t, &seq) : 0;
+        total += (uint32_t)ctx;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        total += __shfl_xor(total, d);
+    if (lane == 0)
+        lds[wave] = total;
+    if (t == 0)
+        out->batch = -1;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWaves; w++)
+        total += lds[w];
+    uint64_t chunk = (total + g.budget - 1) / g.budget;
+    chunk = chunk < kMinChunk ? kMinChunk : (chunk + kMinChunk - 1) / kMinChunk * kMinChunk;
+    uint32_t before = 0;
+    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * kWaves) {
+        if (g.batch > 64 * kWaves)
+            ctx = b0 + t < g.batch ? context_of(g, b0 + t, &seq) : 0;
+        const uint32_t n = b0 + t >= g.batch ? 0 : (ctx == 0 ? 1 : (uint32_t)(((uint32_t)ctx + chunk - 1) / chunk));
+        uint32_t x = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t y = __shfl_up(x, d);
+            if (lane >= (uint32_t)d)
+                x += y;
+        }
+        __syncthreads();
+        if (lane == 63)
+            lds[wave] = x;
+        __syncthreads();
+        uint32_t base = before + x - n;
+        for (uint32_t w = 0; w < kWaves; w++) {
+            base += w < wave ? (uint32_t)lds[w] : 0;
+            before += (uint32_t)lds[w];
+        }
+        if ((uint32_t)want >= base && (uint32_t)want < base + n) {
+            out->batch = (int32_t)(b0 + t);
+            out->split = want - (int32_t)base;
+            out->splits = (int32_t)n;
+            out->slot = want;
+            out->chunk = (int32_t)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
+            out->seq = seq;
+            out->context = ctx;
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, int D, int NT, int WM>
+__global__ __launch_bounds__(64 * kWaves) void tree_attention_kernel(AttnArgs g) {
+    typedef typename Mfma<T>::V V8;
+    constexpr int WK = kWaves / WM;        // waves that share rows and divide the keys
+    constexpr int KS = D / 32;             // steps of the first product
+    constexpr int DJ = D / 16;             // instructions of the second one, elements a lane loads of a value
+    constexpr int R = 16 * NT;             // rows of a wave
+    constexpr int kRegs = NT * DJ * 4;     // accumulators
+    __shared__ Work work;
+    __shared__ uint64_t sums[kWaves];
+    __shared__ uint32_t list[kListPages];
+    __shared__ float merge[WK > 1 ? WM * (WK / 2) * 64 * (kRegs + 2 * NT) : 1];
+
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t n = lane & 15, q4 = lane >> 4;
+    const uint32_t wm = wave % WM, wk = wave / WM;
+
+    // The row blocks of one head's chunk run on one XCD, one after the other: they read the same keys.
+    uint32_t unit = blockIdx.x, block = 0;
+    if (g.row_blocks > 1) {
+        const uint32_t at = blockIdx.x >> 3;
+        block = at % g.row_blocks;
+        unit = at / g.row_blocks * 8 + (blockIdx.x & 7);
+    }
+    const uint32_t head = unit % g.heads;
+    find_work(g, (int32_t)(unit / g.heads), &work, sums);
+    if (work.batch < 0)
+        return;
+    const Work w = work;
+    const uint32_t b = (uint32_t)w.batch;
+    int32_t nodes = w.seq < 0 ? 0 : (int32_t)g.nodes;
+    if (w.seq >= 0 && g.tree_nodes != nullptr) {
+        const int32_t x = g.tree_nodes[b];
+        nodes = x < 0 ? 0 : (x < nodes ? x : nodes);
+    }
+    if (block == 0 && head == 0 && w.split == 0 && threadIdx.x == 0) {
+        g.split_base[b] = w.slot;
+        g.split_count[b] = w.splits;
+    }
+    const uint32_t c0 = (uint32_t)w.split * (uint32_t)w.chunk;
+    const uint32_t c1 = min(c0 + (uint32_t)w.chunk, (uint32_t)w.context);
+    const bool last = w.split + 1 == w.splits;
+
+    // the chunk's page numbers
+    const auto page_of = [&](uint32_t token) { return (uint32_t)(((uint64_t)token * g.div_mul) >> g.div_shift); };
+    const int32_t *row_table = g.table + (uint64_t)(w.seq < 0 ? 0 : w.seq) * g.max_pages;
+    const uint32_t p0 = page_of(c0), pages = c1 > c0 ? page_of(c1 - 1) - p0 + 1 : 0;
+    const bool listed = pages <= kListPages;
+    if (listed)
+        for (uint32_t i = threadIdx.x; i < pages; i += 64 * kWaves) {
+            const uint32_t p = (uint32_t)row_table[p0 + i];
+            list[i] = p < g.num_pages ? p : 0;
+        }
+
+    // this wave's rows: row r is node r / group of query head head * group + r % group
+    const uint32_t row0 = (block * WM + wm) * R;
+    V8 q[NT][KS];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        const uint32_t r = row0 + t * 16 + n;
+        const uint32_t node = r / g.group, h = head * g.group + r % g.group;
+        const uint64_t at = reinterpret_cast<uint64_t>(g.q) + b * g.q_stride[0] + node * g.q_stride[1] + h * g.q_stride[2] + q4 * 16;
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            u32x4 x = {0, 0, 0, 0};
+            if (r < g.rows && g.sign != 0)
+                x = *(const gu32x4 *)(at + s * 64);
+            if (g.sign < 0)   // a negative scale: the sign goes to q, exactly
+                x ^= 0x80008000u;
+            q[t][s] = __builtin_bit_cast(V8, x);
+        }
+    }
+    __syncthreads();
+
+    f32x4 o[NT][DJ];
+    float m[NT], l[NT];   // l: this lane's keys only
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        m[t] = -INFINITY;
+        l[t] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DJ; j++)
+            o[t][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+
+    uint32_t kr[2][KS][4], vr[8][DJ / 2];
+
+    // byte offset of a context token's head in its pool
+    const auto offset_of = [&](uint32_t token) {
+        const uint32_t p = page_of(token), in_page = token - p * g.page_tokens;
+        uint32_t page;
+        if (listed) {
+            page = list[p - p0];
+        } else {
+            page = (uint32_t)row_table[p];
+            page = page < g.num_pages ? page : 0;
+        }
+        return (uint64_t)page * g.page_stride + in_page * g.token_step + head * g.head_step;
+    };
+    const auto load_k = [&](uint64_t base, uint64_t off0, uint64_t off1) {
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            load_dwords<4>(kr[0][s], base + off0 + s * 64 + q4 * 16);
+            load_dwords<4>(kr[1][s], base + off1 + s * 64 + q4 * 16);
+        }
+    };
+    const auto load_ctx_k = [&](uint32_t first) {   // tokens first .. first + 31, those past the chunk its last one
+        const uint32_t t0 = min(first + n, c1 - 1), t1 = min(first + 16 + n, c1 - 1);
+        load_k(reinterpret_cast<uint64_t>(g.k_cache), offset_of(t0), offset_of(t1));
+    };
+    const auto load_ctx_v = [&](uint32_t first) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t token = min(first + (i < 4 ? 0 : 12) + 4 * q4 + i, c1 - 1);
+            load_dwords<DJ / 2>(vr[i], reinterpret_cast<uint64_t>(g.v_cache) + offset_of(token) + n * (2 * DJ));
+        }
+    };
+
+    // One tile: scores, statistics, second product.  keep(t, i): whether row
+    // t * 16 + n sees the lane's i-th key; `some`: whether any row does not see all.
+    // after_k() runs once the keys are no longer needed.
+    const auto tile = [&](bool some, auto keep, auto after_k) {
+        f32x4 s[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+            s[t][0] = s[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; k++)
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+                const u32x4 x = {kr[z][k][0], kr[z][k][1], kr[z][k][2], kr[z][k][3]};
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    s[t][z] = Mfma<T>::mul(__builtin_bit_cast(V8, x), q[t][k], s[t][z]);
+            }
+        after_k();
+        V8 p[NT];
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x[i] = s[t][i / 4][i % 4];
+            if (some) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    x[i] = keep(t, i) ? x[i] : -INFINITY;
+            }
+            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            top = fmaxf(lanes_max(top), m[t]);
+            const float base = top == -INFINITY ? 0.f : top * g.scale2;
+            if (__any(top > m[t])) {
+                // the row's first keys: m = -inf, the factor 0 meets sums that are 0
+                const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -base));
+                l[t] *= fade;
+#pragma unroll
+                for (int j = 0; j < DJ; j++)
+                    o[t][j] *= fade;
+                m[t] = top;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], g.scale2, -base));
+                l[t] += e;
+                // rounded to the element type: what the matrix instruction takes; the sum above keeps all bits
+                p[t][i] = (T)e;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < DJ; j++) {
+            u32x4 x;
+#pragma unroll
+            for (int i = 0; i < 4; i++)   // elements j of keys 2i and 2i + 1
+                x[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j / 2], vr[2 * i][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+                o[t][j] = Mfma<T>::mul(__builtin_bit_cast(V8, x), p[t], o[t][j]);
+        }
+    };
+
+    // the chunk of the context
+    if (c1 > c0 + wk * kTile) {
+        load_ctx_k(c0 + wk * kTile);
+        load_ctx_v(c0 + wk * kTile);
+    }
+    for (uint32_t first = c0 + wk * kTile; first < c1; first += WK * kTile) {
+        const uint32_t next = first + WK * kTile;
+        const bool some = first + kTile > c1;
+        if (some) {
+            // values of keys past the end meet weights of 0 and have to be finite: 0
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int j = 0; j < DJ / 2; j++)
+                    vr[i][j] = first + (i < 4 ? 0 : 12) + 4 * q4 + i < c1 ? vr[i][j] : 0;
+        }
+        tile(some, [&](int, int i) { return first + (i < 4 ? 0 : 12) + 4 * q4 + i < c1; },
+             [&] {
+                 if (next < c1)
+                     load_ctx_k(next);
+             });
+        if (next < c1)
+            load_ctx_v(next);
+    }
+
+    // the drafted nodes, with the sequence's last chunk
+    if (last) {
+        const uint32_t words = (g.nodes + 63) / 64 * 2, count = (uint32_t)nodes;
+        for (uint32_t first = wk * kTile; first < count; first += WK * kTile) {
+            const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + b * g.k_stride[0] + head * g.k_stride[2];
+            const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + b * g.v_stride[0] + head * g.v_stride[2];
+            load_k(kb, min(first + n, count - 1) * g.k_stride[1], min(first + 16 + n, count - 1) * g.k_stride[1]);
+            uint32_t wild = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint32_t u = first + (i < 4 ? 0 : 12) + 4 * q4 + i;
+                load_dwords<DJ / 2>(vr[i], vb + min(u, count - 1) * g.v_stride[1] + n * (2 * DJ));
+#pragma unroll
+                for (int j = 0; j < DJ / 2; j++) {
+                    uint32_t x = u < count ? vr[i][j] : 0;
+                    // A value that is not finite would turn a weight of 0 into NaN: here it counts as 0,
+                    // and rows that do see it get it added below.
+                    const uint32_t lo = (x & Mfma<T>::kExp) == Mfma<T>::kExp, hi = (x >> 16 & Mfma<T>::kExp) == Mfma<T>::kExp;
+                    x &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+                    wild |= lo | hi;
+                    vr[i][j] = x;
+                }
+            }
+            uint32_t bits[NT];
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                const uint32_t r = min(row0 + t * 16 + n, g.rows - 1), node = r / g.group;
+                if (g.mask != nullptr)
+                    bits[t] = g.mask[((uint64_t)b * g.nodes + node) * words + first / 32];
+                else
+                    bits[t] = node < first ? 0u : (node >= first + 31 ? 0xffffffffu : (2u << (node - first)) - 1);
+                if (count < first + 32)
+                    bits[t] &= (1u << (count - first)) - 1;
+            }
+            tile(true, [&](int t, int i) { return (bits[t] >> ((i < 4 ? 0 : 12) + 4 * q4 + i) & 1) != 0; }, [] {});
+            if (__any(wild)) {
+                for (uint32_t u = first; u < min(first + 32, count); u++) {
+                    const T *row = reinterpret_cast<const T *>(vb + u * g.v_stride[1]);
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        const bool sees = bits[t] >> (u - first) & 1;
+#pragma unroll
+                        for (int j = 0; j < DJ; j++)
+#pragma unroll
+                            for (int r = 0; r < 4; r++) {
+                                const float x = (float)row[(4 * q4 + r) * DJ + j];
+                                if (sees && !(fabsf(x) < INFINITY))
+                                    o[t][j][r] += x;   // any weight of it gives the same
+                            }
+                    }
+                }
+            }
+        }
+    }
+
+    // the waves that divided the keys
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+        l[t] = lanes_sum(l[t]);
+#pragma unroll
+    for (int half = WK / 2; half > 0; half /= 2) {
+        if (wk >= (uint32_t)half && wk < (uint32_t)(2 * half)) {
+            float *at = merge + ((wk - half) * WM + wm) * 64 * (kRegs + 2 * NT) + lane;
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                at[t * 128] = m[t];
+                at[t * 128 + 64] = l[t];
+#pragma unroll
+                for (int j = 0; j < DJ; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        at[64 * (2 * NT + (t * DJ + j) * 4 + r)] = o[t][j][r];
+            }
+        }
+        __syncthreads();
+        if (wk < (uint32_t)half) {
+            const float *at = merge + (wk * WM + wm) * 64 * (kRegs + 2 * NT) + lane;
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                const float m2 = at[t * 128], top = fmaxf(m[t], m2), base = top == -INFINITY ? 0.f : top * g.scale2;
+                const float f1 = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -base));
+                const float f2 = __builtin_amdgcn_exp2f(__builtin_fmaf(m2, g.scale2, -base));
+                m[t] = top;
+                l[t] = l[t] * f1 + at[t * 128 + 64] * f2;
+#pragma unroll
+                for (int j = 0; j < DJ; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        o[t][j][r] = o[t][j][r] * f1 + at[64 * (2 * NT + (t * DJ + j) * 4 + r)] * f2;
+            }
+        }
+        __syncthreads();
+    }
+    if (wk != 0)
+        return;
+
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        const uint32_t r = row0 + t * 16 + n;
+        if (r >= g.rows)
+            continue;
+        const uint32_t node = r / g.group, h = head * g.group + r % g.group;
+        if (w.splits > 1) {
+            const uint64_t at = ((uint64_t)w.slot * g.heads + head) * g.rows + r;
+            if (q4 == 0) {
+                g.part_ml[2 * at] = m[t];
+                g.part_ml[2 * at + 1] = l[t];
+            }
+            gf32x4 *to = (gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (at * D + 4 * q4 * DJ) * 4);
+#pragma unroll
+            for (int i = 0; i < DJ; i++) {
+                f32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    x[e] = o[t][(4 * i + e) % DJ][(4 * i + e) / DJ];
+                to[i] = x;
+            }
+            continue;
+        }
+        const bool empty = l[t] == 0.f || (int32_t)node >= nodes;
+        const float inv = empty ? 0.f : 1.f / l[t];
+        gu32x4 *to = (gu32x4 *)(reinterpret_cast<uint64_t>(g.out) + b * g.out_stride[0] + node * g.out_stride[1] +
+                                h * g.out_stride[2] + 4 * q4 * DJ * 2);
+#pragma unroll
+        for (int i = 0; i < DJ / 2; i++) {
+            V8 x;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                x[e] = (T)(empty ? 0.f : o[t][(8 * i + e) % DJ][(8 * i + e) / DJ] * inv);
+            to[i] = __builtin_bit_cast(u32x4, x);
+        }
+        if (g.lse != nullptr && q4 == 0)
+            g.lse[((uint64_t)b * g.nodes + node) * g.heads_q + h] = empty ? -INFINITY : m[t] * g.scale + logf(l[t]);
+    }
+}
+
+// Joins the chunks of sequences that have several: one wave a row.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
+    const uint32_t lane = threadIdx.x & 63;
+    const uint64_t at = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const uint32_t r = (uint32_t)(at % g.rows), head = (uint32_t)(at / g.rows % g.heads);
+    const uint64_t b = at / g.rows / g.heads;
+    if (b >= g.batch)
+        return;
+    const int32_t splits = g.split_count[b];
+    if (splits <= 1)
+        return;
+    const uint64_t first = (uint64_t)g.split_base[b];
+    float m = -INFINITY;
+    for (int32_t s = lane; s < splits; s += 64)
+        m = fmaxf(m, g.part_ml[2 * (((first + s) * g.heads + head) * g.rows + r)]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        m = fmaxf(m, __shfl_xor(m, d));
+    const float base = m == -INFINITY ? 0.f : m * g.scale2;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    for (int32_t s = 0; s < splits; s++) {
+        const uint64_t k = ((first + s) * g.heads + head) * g.rows + r;
+        const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(g.part_ml[2 * k], g.scale2, -base));
+        l += f * g.part_ml[2 * k + 1];
+        if (lane * 4 < D) {
+            const f32x4 x = *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + lane * 4) * 4);
+            o += x * f;
+        }
+    }
+    const uint32_t node = r / g.group, h = head * g.group + r % g.group;
+    int32_t nodes = (int32_t)g.nodes;
+    if (g.tree_nodes != nullptr)
+        nodes = g.tree_nodes[b];
+    const bool empty = l == 0.f || (int32_t)node >= nodes;
+    if (lane * 4 < D) {
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        t4 x;
+        for (int e = 0; e < 4; e++)
+            x[e] = (T)(empty ? 0.f : o[e] / l);
+        *reinterpret_cast<t4 *>(g.out + b * g.out_stride[0] + node * g.out_stride[1] + h * g.out_stride[2] + lane * 8) = x;
+    }
+    if (g.lse != nullptr && lane == 0)
+        g.lse[(b * g.nodes + node) * g.heads_q + h] = empty ? -INFINITY : m * g.scale + logf(l);
+}
+
+// ---- host ----------------------------------------------------------------------
+
+// Rows of a wave: 16 NT, and how many of the workgroup's waves hold rows of their own.
+struct Shape {
+    int nt, wm;
+};
+static Shape shape_of(uint32_t rows, uint32_t head_dim) {
+    if (rows <= 16)
+        return {1, 1};
+    if (rows <= 32)
+        return {2, 1};
+    if (head_dim > 128)
+        return {2, rows <= 64 ? 2 : 4};
+    return {4, rows <= 64 ? 1 : (rows <= 128 ? 2 : 4)};
+}
+
+struct Plan {
+    Shape shape;
+    uint32_t rows, row_blocks, budget;
+    uint64_t slots;
+};
+static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count) {
+    Plan p;
+    p.rows = a.nodes * (a.heads_q / heads);
+    p.shape = shape_of(p.rows, a.head_dim);
+    const uint32_t per_wg = 16 * p.shape.nt * p.shape.wm;
+    p.row_blocks = (p.rows + per_wg - 1) / per_wg;
+    const uint32_t target = (uint32_t)cu_count * (p.shape.nt == 1 ? 3 : (p.shape.nt == 2 ? 2 : 1));
+    p.budget = target / (heads * p.row_blocks);
+    if (p.budget < 1)
+        p.budget = 1;
+    p.slots = (uint64_t)p.budget + a.batch;
+    return p;
+}
+
+static uint64_t round16(uint64_t n) { return (n + 15) / 16 * 16; }
+
+uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count) {
+    const Plan p = plan_of(a, heads, cu_count);
+    const uint64_t rows = p.slots * heads * p.rows;
+    return round16(8ull * a.batch) + round16(8 * rows) + 4 * rows * a.head_dim;
+}
+
+template <typename T, int D, int NT, int WM>
+static hipError_t launch_shape(const AttnArgs &g, uint32_t grid, hipStream_t stream) {
+    LaunchSeq seq;
+    hipError_t e = launch(tree_attention_kernel<T, D, NT, WM>, grid, 64 * kWaves, stream, nullptr, g);
+    if (e != hipSuccess)
+        return e;
+    seq.last();
+    const uint64_t rows = (uint64_t)g.batch * g.heads * g.rows;
+    return launch(tree_combine_kernel<T, D>, (uint32_t)((rows + 3) / 4), 256, stream, nullptr, g);
+}
+
+template <typename T, int D>
+static hipError_t launch_dim(const AttnArgs &g, Shape s, uint32_t grid, hipStream_t stream) {
+    if (s.nt == 1)
+        return launch_shape<T, D, 1, 1>(g, grid, stream);
+    if constexpr (D > 128) {
+        if (s.wm == 1)
+            return launch_shape<T, D, 2, 1>(g, grid, stream);
+        return s.wm == 2 ? launch_shape<T, D, 2, 2>(g, grid, stream) : launch_shape<T, D, 2, 4>(g, grid, stream);
+    } else {
+        if (s.nt == 2)
+            return launch_shape<T, D, 2, 1>(g, grid, stream);
+        if (s.wm == 1)
+            return launch_shape<T, D, 4, 1>(g, grid, stream);
+        return s.wm == 2 ? launch_shape<T, D, 4, 2>(g, grid, stream) : launch_shape<T, D, 4, 4>(g, grid, stream);
+    }
+}
+
+template <typename T>
+static hipError_t launch_type(const AttnArgs &g, uint32_t dim, Shape s, uint32_t grid, hipStream_t stream) {
+    switch (dim) {
+    case 64: return launch_dim<T, 64>(g, s, grid, stream);
+    case 96: return launch_dim<T, 96>(g, s, grid, stream);
+    case 128: return launch_dim<T, 128>(g, s, grid, stream);
+    case 256: return launch_dim<T, 256>(g, s, grid, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream) {
+    const Plan p = plan_of(a, c.heads, cu_count);
     AttnArgs g;
-    g.a = a;
+    g.q = static_cast<const uint8_t *>(a.q);
+    g.k = static_cast<const uint8_t *>(a.k);
+    g.v = static_cast<const uint8_t *>(a.v);
+    g.out = static_cast<uint8_t *>(a.out);
+    g.lse = a.lse;
+    for (int k = 0; k < 3; k++) {
+        g.q_stride[k] = 2 * a.q_stride[k];
+        g.k_stride[k] = 2 * a.k_stride[k];
+        g.v_stride[k] = 2 * a.v_stride[k];
+        g.out_stride[k] = 2 * a.out_stride[k];
+    }
+    g.seqs = a.seqs;
+    g.mask = reinterpret_cast<const uint32_t *>(a.mask);
+    g.tree_nodes = a.tree_nodes;
     g.k_cache = static_cast<const uint8_t *>(c.pools[a.k_pool]);
     g.v_cache = static_cast<const uint8_t *>(c.pools[a.v_pool]);
     g.table = c.table;
     g.lens = c.lens;
-    g.page_stride = c.page_stride;
+    g.batch = a.batch;
+    g.nodes = a.nodes;
+    g.heads_q = a.heads_q;
+    g.heads = c.heads;
+    g.group = a.heads_q / c.heads;
+    g.rows = p.rows;
     const bool token_major = c.layout == TB_CACHE_TOKEN_MAJOR;
-    g.token_step = token_major ? (uint64_t)c.heads * c.head_bytes : c.head_bytes;
-    g.head_step = token_major ? c.head_bytes : (uint64_t)c.page_tokens * c.head_bytes;
+    g.page_stride = (uint32_t)c.page_stride;
+    g.token_step = token_major ? c.heads * c.head_bytes : c.head_bytes;
+    g.head_step = token_major ? c.head_bytes : c.page_tokens * c.head_bytes;
     g.num_pages = c.num_pages;
     g.page_tokens = c.page_tokens;
     g.max_seqs = c.max_seqs;
     g.max_pages = c.max_pages;
-    g.heads = c.heads;
-    const dim3 grid(a.heads_q, a.nodes, a.batch);
-    const bool bf = a.dtype == TB_BF16;
-    switch (a.head_dim) {
-    case 64: return launch(bf ? tree_attention_kernel<__hip_bfloat16, 64> : tree_attention_kernel<__half, 64>, grid, 64, stream, nullptr, g);
-    case 96: return launch(bf ? tree_attention_kernel<__hip_bfloat16, 96> : tree_attention_kernel<__half, 96>, grid, 64, stream, nullptr, g);
-    case 128: return launch(bf ? tree_attention_kernel<__hip_bfloat16, 128> : tree_attention_kernel<__half, 128>, grid, 64, stream, nullptr, g);
-    case 256: return launch(bf ? tree_attention_kernel<__hip_bfloat16, 256> : tree_attention_kernel<__half, 256>, grid, 64, stream, nullptr, g);
-    default: return hipErrorInvalidValue;
-    }
+    // x / d for x < 2^31: with 2^(s-1) < d <= 2^s and f = ceil(2^(31+s) / d) < 2^32, x f / 2^(31+s)
+    // exceeds x / d by less than x / 2^(31+s) <= 1 / d, too little to reach the next whole number
+    uint32_t s = 0;
+    while ((1u << s) < c.page_tokens)
+        s++;
+    g.div_shift = 31 + s;
+    g.div_mul = (uint32_t)(((1ull << (31 + s)) + c.page_tokens - 1) / c.page_tokens);
+    g.row_blocks = p.row_blocks;
+    g.budget = p.budget;
+    g.sign = a.scale > 0.f ? 1 : (a.scale < 0.f ? -1 : 0);
+    // scale 0: q is taken as 0, and any positive scale will do
+    g.scale = g.sign == 0 ? 1.f : fabsf(a.scale);
+    g.scale2 = (float)((double)g.scale * 1.4426950408889634);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    const uint64_t rows = p.slots * c.heads * p.rows;
+    g.split_base = reinterpret_cast<int32_t *>(ws);
+    g.split_count = g.split_base + a.batch;
+    g.part_ml = reinterpret_cast<float *>(ws + round16(8ull * a.batch));
+    g.part_o = reinterpret_cast<float *>(ws + round16(8ull * a.batch) + round16(8 * rows));
+    const uint64_t units = p.slots * c.heads;
+    const uint64_t grid = p.row_blocks > 1 ? (units + 7) / 8 * 8 * p.row_blocks : units;
+    if (grid > (1u << 30))
+        return hipErrorInvalidValue;
+    return a.dtype == TB_BF16 ? launch_type<__bf16>(g, a.head_dim, p.shape, (uint32_t)grid, stream)
+                              : launch_type<_Float16>(g, a.head_dim, p.shape, (uint32_t)grid, stream);
 }
 
 }  // namespace tbk

@@ -251,7 +251,7 @@ int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;
     if (!aligned(c->pools[a->k_pool], 16) || !aligned(c->pools[a->v_pool], 16) || c->page_stride % 16 != 0 ||
-        a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
+        c->page_stride >= (1ull << 32) || a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
         !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
         !list_ok(a->seqs) || !aligned(a->mask, 8) || !aligned(a->tree_nodes, 4))
         return TB_ERR_INVALID;
@@ -269,13 +269,13 @@ int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     }
     if (a->workspace == nullptr || !aligned(a->workspace, 16))
         return TB_ERR_INVALID;
-    uint64_t need = 0;
-    const int rc = tb_tree_attention_workspace(a, c, &need);
+    int cus = 0;
+    const int rc = tbh::cu_count_of_device(&cus);
     if (rc != TB_OK)
         return rc;
-    if (a->workspace_bytes < need)
+    if (a->workspace_bytes < tbk::tree_attention_workspace(args, c->heads, cus))
         return TB_ERR_INVALID;
-    const hipError_t e = tbk::launch_tree_attention(args, *c, static_cast<hipStream_t>(stream));
+    const hipError_t e = tbk::launch_tree_attention(args, *c, cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? TB_OK : hip_fail(e, "tree attention launch");
 }
 

@@ -118,7 +118,7 @@ hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t
 hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream);
 hipError_t launch_compact_apply(const CacheState &s, hipStream_t stream);
 
-hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, hipStream_t stream);
+hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream);
 uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count);
 
 }  // namespace tbk
