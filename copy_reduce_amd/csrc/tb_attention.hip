@@ -37,10 +37,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(1))) u32x4 gu32x4;
 typedef __attribute__((address_space(1))) f32x4 gf32x4;
+typedef __attribute__((address_space(1))) void gvoid;
+typedef __attribute__((address_space(3))) void svoid;
 
 constexpr int kTile = 32;              // keys of a tile
 constexpr uint32_t kListPages = 2048;  // page numbers of a chunk kept in LDS
-constexpr uint32_t kMinChunk = 128;    // fewest tokens a workgroup is given
 // A row's maximum is let stand until a score exceeds it by this much (in powers of
 // two): weights then stay below 2^8, well inside every type here, and after the
 // first tiles the accumulators are hardly ever scaled again.
@@ -57,11 +58,11 @@ struct AttnArgs {
     const uint8_t *k_cache, *v_cache;
     const int32_t *table, *lens;
     uint32_t batch, nodes, heads_q, heads, group, rows;   // rows: nodes * group
-    uint32_t page_stride, token_step, head_step;          // bytes
+    uint32_t page_step, token_step, head_step;            // in pieces of 16 bytes, see Keys
     uint32_t num_pages, page_tokens, max_seqs, max_pages;
     uint32_t div_mul, div_shift;       // token / page_tokens = token * div_mul >> div_shift
     uint32_t row_blocks;               // workgroups that share a head's rows
-    uint32_t budget;                   // chunks that all sequences together are cut into, one more each
+    uint32_t budget;                   // shares that a head's stream of keys is cut into
     float scale, scale2;               // |scale| log2 e; 1 for scale 0, see load_q
     int32_t sign;                      // of scale
     int32_t *split_base, *split_count; // [batch] workspace
@@ -88,6 +89,11 @@ struct Mfma<_Float16> {
     static constexpr uint32_t kExp = 0x7c00;
 };
 
+// Cache policy of the keys and values: nontemporal, each is read by one workgroup (or by few, at
+// the same time).  Against plain loads: 64 sequences of up to 8,191 tokens 209 us against 216, trees of 64
+// nodes over up to 16,383 tokens 215 against 220.
+constexpr int kStream = 2;
+
 // N dwords at 4-byte alignment or better, as 16-byte loads and one rest.
 template <int N>
 __device__ __forceinline__ void load_dwords(uint32_t *r, uint64_t at) {
@@ -95,7 +101,7 @@ __device__ __forceinline__ void load_dwords(uint32_t *r, uint64_t at) {
     typedef uint32_t u32x3a __attribute__((ext_vector_type(3), aligned(4)));
     typedef __attribute__((address_space(1))) u32x3a gu32x3;
     if constexpr (N >= 4) {
-        const u32x4 x = *(const gu32x4 *)at;
+        const u32x4 x = __builtin_nontemporal_load((const gu32x4 *)at);
         r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
         if constexpr (N > 4)
             load_dwords<N - 4>(r + 4, at + 16);
@@ -109,6 +115,9 @@ __device__ __forceinline__ void load_dwords(uint32_t *r, uint64_t at) {
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
 // Over the lanes with the same lane % 16.
 __device__ __forceinline__ float lanes_max(float x) {
     u32x2 y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -121,38 +130,64 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// What a workgroup works on.
-struct Work {
-    int32_t batch;   // -1: nothing
-    int32_t split;
-    int32_t splits;
-    int32_t slot;    // number of the split among all
-    int32_t chunk;   // tokens of a split
-    int32_t seq;
-    int32_t context;
-};
-
-__device__ __forceinline__ int32_t context_of(const AttnArgs &g, uint32_t b, int32_t *seq) {
-    const int32_t q = g.seqs[b];
-    *seq = (uint32_t)q < g.max_seqs ? q : -1;
-    if (*seq < 0)
-        return 0;
-    const int32_t n = g.lens[q], most = (int32_t)(g.max_pages * g.page_tokens);
-    return n < 0 ? 0 : (n < most ? n : most);
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return (uint64_t)uniform((uint32_t)(x >> 32)) << 32 | uniform((uint32_t)x);
 }
 
-// Cuts the contexts into chunks of equal length, as many as `budget` and one
-// more a sequence at most, and finds chunk number `want`.  Every workgroup does
-// the whole of it (a few loads and two sums), so nothing has to be planned
-// before the launch and the lengths stay on the device.
-template <int kWaves>
-__device__ __forceinline__ void find_work(const AttnArgs &g, int32_t want, Work *out, uint64_t *lds) {
+// x again, as a value the compiler knows nothing about: what follows from it is
+// computed where it is used and not kept in registers across the loop over parts.
+__device__ __forceinline__ uint32_t anew(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Context of sequence b of the batch, its row and its drafted nodes.
+struct Sequence {
+    int32_t row;   // -1: none
+    uint32_t context, nodes;
+};
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs &g, uint32_t b) {
+    Sequence s = {-1, 0, 0};
+    const int32_t q = g.seqs[b];
+    if ((uint32_t)q >= g.max_seqs)
+        return s;
+    s.row = q;
+    const int32_t n = g.lens[q], most = (int32_t)(g.max_pages * g.page_tokens);
+    s.context = (uint32_t)(n < 0 ? 0 : (n < most ? n : most));
+    s.nodes = g.nodes;
+    if (g.tree_nodes != nullptr) {
+        const int32_t x = g.tree_nodes[b];
+        s.nodes = x < 0 ? 0 : min((uint32_t)x, g.nodes);
+    }
+    return s;
+}
+
+// The batch's keys as one stream: each sequence's context and nodes, rounded up to kUnit
+// keys, and one unit more for what a sequence costs by itself, one after the other.  It is cut into equal shares,
+// one for each of the workgroups that a head's rows have, so that they all end together
+// however the lengths differ.  A share may cover parts of several sequences.
+// Every workgroup finds its place by itself (a few loads and a sum over the
+// batch): nothing is planned before the launch and the lengths stay on the device.
+constexpr uint32_t kUnit = 128;
+__device__ __forceinline__ uint32_t weight_of(const Sequence &s) {
+    return ((s.context + s.nodes + kUnit - 1) / kUnit + 1) * kUnit;
+}
+
+struct Place {
+    uint64_t start;   // of sequence `batch` in the stream
+    uint64_t share;
+    uint32_t batch;   // the sequence in which the share begins; g.batch: no share
+};
+
+template <int WAVES>
+__device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds) {
     const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    int32_t seq = -1, ctx = 0;
-    uint64_t total = 0;
-    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * kWaves) {
-        ctx = b0 + t < g.batch ? context_of(g, b0 + t, &seq) : 0;
-        total += (uint32_t)ctx;
+    uint64_t total = 0, w = 0;
+    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {
+        w = b0 + t < g.batch ? weight_of(sequence_of(g, b0 + t)) : 0;
+        total += w;
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
@@ -160,22 +195,22 @@ __device__ __forceinline__ void find_work(const AttnArgs &g, int32_t want, Work 
     if (lane == 0)
         lds[wave] = total;
     if (t == 0)
-        out->batch = -1;
+        out->batch = g.batch;
     __syncthreads();
     total = 0;
-    for (int w = 0; w < kWaves; w++)
-        total += lds[w];
-    uint64_t chunk = (total + g.budget - 1) / g.budget;
-    chunk = chunk < kMinChunk ? kMinChunk : (chunk + kMinChunk - 1) / kMinChunk * kMinChunk;
-    uint32_t before = 0;
-    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * kWaves) {
-        if (g.batch > 64 * kWaves)
-            ctx = b0 + t < g.batch ? context_of(g, b0 + t, &seq) : 0;
-        const uint32_t n = b0 + t >= g.batch ? 0 : (ctx == 0 ? 1 : (uint32_t)(((uint32_t)ctx + chunk - 1) / chunk));
-        uint32_t x = n;
+    for (int k = 0; k < WAVES; k++)
+        total += lds[k];
+    const uint64_t units = total / kUnit;
+    const uint64_t share = (units <= 0xffffffffu ? ((uint32_t)units + g.budget - 1) / g.budget : (units + g.budget - 1) / g.budget) * kUnit;
+    const uint64_t begin = mine * share;
+    uint64_t before = 0;
+    for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {
+        if (g.batch > 64 * WAVES)
+            w = b0 + t < g.batch ? weight_of(sequence_of(g, b0 + t)) : 0;
+        uint64_t x = w;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t y = __shfl_up(x, d);
+            const uint64_t y = __shfl_up(x, d);
             if (lane >= (uint32_t)d)
                 x += y;
         }
@@ -183,71 +218,90 @@ __device__ __forceinline__ void find_work(const AttnArgs &g, int32_t want, Work 
         if (lane == 63)
             lds[wave] = x;
         __syncthreads();
-        uint32_t base = before + x - n;
-        for (uint32_t w = 0; w < kWaves; w++) {
-            base += w < wave ? (uint32_t)lds[w] : 0;
-            before += (uint32_t)lds[w];
+        uint64_t start = before + x - w;
+        for (uint32_t k = 0; k < WAVES; k++) {
+            start += k < wave ? lds[k] : 0;
+            before += lds[k];
         }
-        if ((uint32_t)want >= base && (uint32_t)want < base + n) {
-            out->batch = (int32_t)(b0 + t);
-            out->split = want - (int32_t)base;
-            out->splits = (int32_t)n;
-            out->slot = want;
-            out->chunk = (int32_t)(chunk < 0x7fffffff ? chunk : 0x7fffffff);
-            out->seq = seq;
-            out->context = ctx;
+        if (begin >= start && begin < start + w) {
+            out->batch = b0 + t;
+            out->start = start;
+            out->share = share;
         }
     }
     __syncthreads();
 }
 
-// Where a workgroup's keys are: its chunk [c0, c1) of the context, the drafted
-// nodes if `last`, and the pages of the chunk.
-template <int kWaves>
+// What a workgroup does of one sequence: the part [c0, c1) of its context and, if
+// `last`, its nodes.  Shares of one sequence are joined afterwards, from slot
+// (workgroup + sequence), unless there is only one.
+struct Part {
+    Sequence seq;
+    uint32_t b, c0, c1, slot, splits;
+    uint64_t end;       // of the sequence in the stream
+    bool first, last;
+
+    __device__ __forceinline__ Part(const AttnArgs &g, const Place &at, uint32_t mine) : b(at.batch) {
+        const Sequence s = sequence_of(g, b);
+        seq.row = uniform(s.row);
+        seq.context = uniform(s.context);
+        seq.nodes = uniform(s.nodes);
+        end = at.start + weight_of(seq);
+        const uint64_t begin = mine * at.share;
+        const uint64_t lo = begin > at.start ? begin - at.start : 0;
+        const uint64_t hi = min(begin + at.share, end) - at.start;
+        c0 = (uint32_t)min(lo, (uint64_t)seq.context);
+        c1 = (uint32_t)min(hi, (uint64_t)seq.context);
+        last = at.start + hi == end;
+        first = begin <= at.start;
+        if (first && last) {
+            splits = 1;
+        } else {
+            const uint64_t u = at.share / kUnit, a = at.start / kUnit, z = end / kUnit - 1;
+            splits = uniform(z <= 0xffffffffu ? (uint32_t)z / (uint32_t)u - (uint32_t)a / (uint32_t)u + 1 : (uint32_t)(z / u - a / u + 1));
+        }
+        slot = mine + b;
+    }
+};
+
+// Where the part's keys are.
+template <int WAVES>
 struct Keys {
     const AttnArgs &g;
-    const Work w;
-    uint32_t b, head, c0, c1, count, p0;
-    bool last, listed;
+    uint32_t b, head, count, p0;
+    bool listed;
     const int32_t *row_table;
     const uint32_t *list;
 
-    __device__ __forceinline__ Keys(const AttnArgs &g_, const Work &w_, uint32_t head_, uint32_t *lds)
-        : g(g_), w(w_), b((uint32_t)w_.batch), head(head_), list(lds) {
-        int32_t nodes = w.seq < 0 ? 0 : (int32_t)g.nodes;
-        if (w.seq >= 0 && g.tree_nodes != nullptr) {
-            const int32_t x = g.tree_nodes[b];
-            nodes = x < 0 ? 0 : (x < nodes ? x : nodes);
-        }
-        count = (uint32_t)nodes;
-        c0 = (uint32_t)w.split * (uint32_t)w.chunk;
-        c1 = min(c0 + (uint32_t)w.chunk, (uint32_t)w.context);
-        last = w.split + 1 == w.splits;
-        row_table = g.table + (uint64_t)(w.seq < 0 ? 0 : w.seq) * g.max_pages;
-        p0 = page_of(c0);
-        const uint32_t pages = c1 > c0 ? page_of(c1 - 1) - p0 + 1 : 0;
+    // Places in a pool count pieces of 16 bytes: 32 bits reach 64 GiB, and the address costs one instruction.
+    __device__ __forceinline__ Keys(const AttnArgs &g_, const Part &part, uint32_t head_, uint32_t *lds)
+        : g(g_), b(part.b), head(head_), count(part.seq.nodes), list(lds) {
+        row_table = g.table + (uint64_t)max(part.seq.row, 0) * g.max_pages;
+        p0 = page_of(part.c0);
+        const uint32_t pages = part.c1 > part.c0 ? page_of(part.c1 - 1) - p0 + 1 : 0;
         listed = pages <= kListPages;
         if (listed)
-            for (uint32_t i = threadIdx.x; i < pages; i += 64 * kWaves) {
+            for (uint32_t i = threadIdx.x; i < pages; i += 64 * WAVES) {
                 const uint32_t p = (uint32_t)row_table[p0 + i];
-                lds[i] = p < g.num_pages ? p : 0;
+                lds[i] = (p < g.num_pages ? p : 0) * g.page_step;
             }
     }
     __device__ __forceinline__ uint32_t page_of(uint32_t token) const {
         return (uint32_t)(((uint64_t)token * g.div_mul) >> g.div_shift);
     }
-    // Byte offset of a context token's head in its pool.
-    __device__ __forceinline__ uint64_t offset_of(uint32_t token) const {
+    // Place of a context token's head in its pool.
+    __device__ __forceinline__ uint32_t place_of(uint32_t token) const {
         const uint32_t p = page_of(token), in_page = token - p * g.page_tokens;
-        uint32_t page;
+        uint32_t at;
         if (listed) {
-            page = list[p - p0];
+            at = list[p - p0];
         } else {
-            page = (uint32_t)row_table[p];
-            page = page < g.num_pages ? page : 0;
+            const uint32_t page = (uint32_t)row_table[p];
+            at = (page < g.num_pages ? page : 0) * g.page_step;
         }
-        return (uint64_t)page * g.page_stride + in_page * g.token_step + head * g.head_step;
+        return at + in_page * g.token_step + head * g.head_step;
     }
+    __device__ __forceinline__ uint64_t offset_of(uint32_t token) const { return (uint64_t)place_of(token) * 16; }
     // Bits of the nodes first .. first + 31 that row r sees.
     __device__ __forceinline__ uint32_t seen(uint32_t r, uint32_t first) const {
         const uint32_t words = (g.nodes + 63) / 64 * 2, node = min(r, g.rows - 1) / g.group;
@@ -277,15 +331,17 @@ struct Rows {
     typedef typename Mfma<T>::V V8;
     static constexpr int KS = D / 32;   // steps of the first product
     static constexpr int DJ = D / 16;   // instructions of the second one
+    static constexpr int GJ = DJ % 4 == 0 ? 4 : 2;   // of them, whose operands are had together
     static constexpr int kRegs = NT * DJ * 4;
     static constexpr int kMergeFloats = 64 * (kRegs + 2 * NT);   // of one wave, see join()
     V8 q[NT][KS];
     f32x4 o[NT][DJ];
-    float m[NT], l[NT];                 // l: this lane's keys only, until close()
+    float m[NT], l[NT];                 // l: this lane's keys only, until join()
+    float base[NT];                     // of the exponents: m scaled, 0 while m is -inf
 
     // Row r is node r / group of query head head * group + r % group.
-    __device__ __forceinline__ void open(const AttnArgs &g, uint32_t b, uint32_t head, uint32_t row0) {
-        const uint32_t lane = threadIdx.x & 63, n = lane & 15, q4 = lane >> 4;
+    __device__ __forceinline__ void open(const AttnArgs &g, uint32_t b, uint32_t head, uint32_t row0, uint32_t lane) {
+        const uint32_t n = lane & 15, q4 = lane >> 4;
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const uint32_t r = row0 + t * 16 + n, node = r / g.group, h = head * g.group + r % g.group;
@@ -301,72 +357,91 @@ struct Rows {
                 q[t][s] = __builtin_bit_cast(V8, x);
             }
             m[t] = -INFINITY;
-            l[t] = 0.f;
+            l[t] = base[t] = 0.f;
 #pragma unroll
             for (int j = 0; j < DJ; j++)
                 o[t][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
         }
     }
 
-    // One tile of keys.  key(z, k): step k's operand for keys 16 z .. 16 z + 15; value(j):
-    // instruction j's operand; keep(t, i): whether row t * 16 + n sees the lane's
-    // i-th key, asked only if `some` row may not see all.  between() runs once
-    // the keys are no longer needed.
-    template <typename Key, typename Value, typename Keep, typename Between>
-    __device__ __forceinline__ void tile(const AttnArgs &g, bool some, Key key, Value value, Keep keep, Between between) {
-        f32x4 s[NT][2];
+    // Raises the maxima to what the lanes saw, and scales what has been summed up.
+    __device__ __forceinline__ void raise_maxima(const AttnArgs &g, const float *tops) {
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const float top = fmaxf(lanes_max(tops[t]), m[t]);
+            base[t] = top == -INFINITY ? 0.f : top * g.scale2;
+            // a row's first keys: m = -inf, the factor 0 meets sums that are 0
+            const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -base[t]));
+            m[t] = top;
+            l[t] *= fade;
+#pragma unroll
+            for (int j = 0; j < DJ; j++)
+                o[t][j] *= fade;
+        }
+    }
+
+    // A tile is worked on in two halves, scores() and apply().  Where scores() says so, the
+    // maxima have to be raised in between, which is rare.
+    //
+    // keys(k, x): x[2 e + z] becomes step k + e's operand for keys 16 z .. 16 z + 15, e and z 0 and 1;
+    // keep(t, i): whether row t * 16 + n sees the lane's i-th key, asked only if `some` row may not see all.
+    template <typename Keys2, typename Keep>
+    __device__ __forceinline__ bool scores(const AttnArgs &g, bool some, Keys2 keys, Keep keep, f32x4 (&s)[NT][2], float (&tops)[NT]) {
 #pragma unroll
         for (int t = 0; t < NT; t++)
             s[t][0] = s[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < KS; k++)
+        for (int k = 0; k < KS; k += 2) {
+            V8 x[4];
+            keys(k, x);
 #pragma unroll
-            for (int z = 0; z < 2; z++) {
-                const V8 x = key(z, k);
+            for (int e = 0; e < 2 && k + e < KS; e++)
 #pragma unroll
-                for (int t = 0; t < NT; t++)
-                    s[t][z] = Mfma<T>::mul(x, q[t][k], s[t][z]);
-            }
-        between();
-        V8 p[NT];
+                for (int z = 0; z < 2; z++)
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-            float x[8];
+                    for (int t = 0; t < NT; t++)
+                        s[t][z] = Mfma<T>::mul(x[2 * e + z], q[t][k + e], s[t][z]);
+        }
+        if (some) {
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                x[i] = s[t][i / 4][i % 4];
-            if (some) {
+            for (int t = 0; t < NT; t++)
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    x[i] = keep(t, i) ? x[i] : -INFINITY;
-            }
-            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            if (__any(top * g.scale2 > __builtin_fmaf(m[t], g.scale2, kSlack))) {
-                top = fmaxf(lanes_max(top), m[t]);
-                const float base = top == -INFINITY ? 0.f : top * g.scale2;
-                // a row's first keys: m = -inf, the factor 0 meets sums that are 0
-                const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -base));
-                l[t] *= fade;
+                    s[t][i / 4][i % 4] = keep(t, i) ? s[t][i / 4][i % 4] : -INFINITY;
+        }
+        bool above = false;
 #pragma unroll
-                for (int j = 0; j < DJ; j++)
-                    o[t][j] *= fade;
-                m[t] = top;
-            }
-            const float base = m[t] == -INFINITY ? 0.f : m[t] * g.scale2;
+        for (int t = 0; t < NT; t++) {
+            // a NaN among the scores stays one: the row is NaN then, whatever its maximum
+            tops[t] = max3(max3(s[t][0][0], s[t][0][1], s[t][0][2]), max3(s[t][0][3], s[t][1][0], s[t][1][1]),
+                           __builtin_elementwise_maximum(s[t][1][2], s[t][1][3]));
+            above |= tops[t] * g.scale2 > __builtin_fmaf(m[t], g.scale2, kSlack);
+        }
+        return __any(above);
+    }
+
+    // values(j, x): x[0 .. GJ - 1] become the operands of the second product's instructions j on.
+    template <typename Values>
+    __device__ __forceinline__ void apply(const AttnArgs &g, const f32x4 (&s)[NT][2], Values values) {
+        V8 p[NT];
+#pragma unroll
+        for (int t = 0; t < NT; t++)
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], g.scale2, -base));
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i / 4][i % 4], g.scale2, -base[t]));
                 l[t] += e;
                 // rounded to the element type, which is what the matrix instruction takes; the sum keeps all bits
                 p[t][i] = (T)e;
             }
-        }
 #pragma unroll
-        for (int j = 0; j < DJ; j++) {
-            const V8 x = value(j);
+        for (int j = 0; j < DJ; j += GJ) {
+            V8 x[GJ];
+            values(j, x);
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-                o[t][j] = Mfma<T>::mul(x, p[t], o[t][j]);
+            for (int e = 0; e < GJ; e++)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    o[t][j + e] = Mfma<T>::mul(x[e], p[t], o[t][j + e]);
         }
     }
 
@@ -397,8 +472,8 @@ struct Rows {
     // Joins the WK waves (wave = wk * WM + wm) that divided the keys of the same rows; the
     // result is in those with wk = 0.  lds: WM * WK / 2 * kMergeFloats floats.
     template <int WM, int WK>
-    __device__ __forceinline__ void join(const AttnArgs &g, float *lds) {
-        const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % WM, wk = wave / WM;
+    __device__ __forceinline__ void join(const AttnArgs &g, float *lds, uint32_t wave, uint32_t lane) {
+        const uint32_t wm = wave % WM, wk = wave / WM;
 #pragma unroll
         for (int t = 0; t < NT; t++)
             l[t] = lanes_sum(l[t]);
@@ -442,11 +517,10 @@ struct Rows {
     // Each lane holds, of row n, runs of RUN neighbouring elements: run i begins at element
     // begin(i), and its element e is value(t, i, e).
     template <int RUN, typename Begin, typename Value>
-    __device__ __forceinline__ void close(const AttnArgs &g, const Work &w, uint32_t head, uint32_t row0, uint32_t count,
-                                          Begin begin, Value value) {
+    __device__ __forceinline__ void close(const AttnArgs &g, const Part &w, uint32_t head, uint32_t row0, uint32_t lane, Begin begin, Value value) {
         constexpr int kRuns = 4 * DJ / RUN;
         typedef T tv __attribute__((ext_vector_type(RUN)));
-        const uint32_t lane = threadIdx.x & 63, n = lane & 15, q4 = lane >> 4;
+        const uint32_t n = lane & 15, q4 = lane >> 4;
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const uint32_t r = row0 + t * 16 + n;
@@ -468,9 +542,9 @@ struct Rows {
                 }
                 continue;
             }
-            const bool empty = l[t] == 0.f || node >= count;
+            const bool empty = l[t] == 0.f || node >= w.seq.nodes;
             const float inv = empty ? 0.f : 1.f / l[t];
-            const uint64_t to = reinterpret_cast<uint64_t>(g.out) + (uint32_t)w.batch * g.out_stride[0] +
+            const uint64_t to = reinterpret_cast<uint64_t>(g.out) + w.b * g.out_stride[0] +
                                 node * g.out_stride[1] + h * g.out_stride[2];
 #pragma unroll
             for (int i = 0; i < kRuns; i++) {
@@ -482,49 +556,52 @@ struct Rows {
                 *(gtv *)(to + begin(i) * 2) = x;
             }
             if (g.lse != nullptr && q4 == 0)
-                g.lse[((uint64_t)(uint32_t)w.batch * g.nodes + node) * g.heads_q + h] =
+                g.lse[((uint64_t)w.b * g.nodes + node) * g.heads_q + h] =
                     empty ? -INFINITY : m[t] * g.scale + logf(l[t]);
         }
     }
 };
 
 // The combine kernel's way into the slots.
-__device__ __forceinline__ void note_splits(const AttnArgs &g, const Work &w, uint32_t head, uint32_t block) {
-    if (block == 0 && head == 0 && w.split == 0 && threadIdx.x == 0) {
-        g.split_base[w.batch] = w.slot;
-        g.split_count[w.batch] = w.splits;
+__device__ __forceinline__ void note_splits(const AttnArgs &g, const Part &w, uint32_t head, uint32_t block) {
+    if (block == 0 && head == 0 && w.first && threadIdx.x == 0) {
+        g.split_base[w.b] = (int32_t)w.slot;
+        g.split_count[w.b] = (int32_t)w.splits;
     }
 }
 
 // ---- few rows ------------------------------------------------------------------
 //
-// Up to 32 rows (16 NT): the cache's bytes decide.  Each of the four waves
+// Up to 16 rows: the cache's bytes decide.  Each of the four waves
 // takes every fourth tile and reads its keys and values straight into the registers
 // from which they are multiplied; the next tile's keys are on their way during the
 // second product, its values during the first.
 constexpr int kWaves = 4;
 
-template <typename T, int D, int NT>
-__global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void tree_attention_kernel(AttnArgs g) {
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void tree_attention_kernel(AttnArgs g) {
+    constexpr int NT = 1;
     typedef Rows<T, D, NT> R;
     typedef typename R::V8 V8;
     constexpr int KS = R::KS, DJ = R::DJ;
-    __shared__ Work work;
+    __shared__ Place place;
     __shared__ uint64_t sums[kWaves];
     __shared__ uint32_t list[kListPages];
     __shared__ float merge[kWaves / 2 * R::kMergeFloats];
 
-    const uint32_t lane = threadIdx.x & 63, wk = threadIdx.x >> 6, n = lane & 15, q4 = lane >> 4;
-    const uint32_t head = blockIdx.x % g.heads;
-    find_work<kWaves>(g, (int32_t)(blockIdx.x / g.heads), &work, sums);
-    if (work.batch < 0)
-        return;
-    const Work w = work;
+    const uint32_t wk = uniform(threadIdx.x >> 6), mine = blockIdx.x / g.heads, head = blockIdx.x % g.heads;
+    find_place<kWaves>(g, mine, &place, sums);
+    Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
+#pragma unroll 1
+    for (; at.batch < g.batch && at.start < (mine + 1) * at.share; at.batch++) {
+    const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
+    const Part w(g, at, mine);
+    at.start = w.end;
     note_splits(g, w, head, 0);
     const Keys<kWaves> keys(g, w, head, list);
-    const uint32_t c0 = keys.c0, c1 = keys.c1;
+    const uint32_t c0 = w.c0, c1 = w.c1;
     R rows;
-    rows.open(g, keys.b, head, 0);
+    rows.open(g, keys.b, head, 0, lane);
     __syncthreads();
 
     uint32_t kr[2][KS][4], vr[8][DJ / 2];
@@ -546,16 +623,24 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void tree_attention_
             load_dwords<DJ / 2>(vr[i], reinterpret_cast<uint64_t>(g.v_cache) + n * (2 * DJ) +
                                            keys.offset_of(min(first + key_of(q4, i), c1 - 1)));
     };
-    const auto key = [&](int z, int k) {
-        return __builtin_bit_cast(V8, (u32x4){kr[z][k][0], kr[z][k][1], kr[z][k][2], kr[z][k][3]});
-    };
-    // element j of the lane's D/16 elements of keys 2i and 2i + 1 side by side
-    const auto value = [&](int j) {
-        u32x4 x;
+    const auto key = [&](int k, V8 *x) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            x[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j / 2], vr[2 * i][j / 2], j % 2 == 0 ? 0x05040100u : 0x07060302u);
-        return __builtin_bit_cast(V8, x);
+        for (int i = 0; i < 4 && k + i / 2 < KS; i++) {
+            const uint32_t *r = kr[i % 2][k + i / 2];
+            x[i] = __builtin_bit_cast(V8, (u32x4){r[0], r[1], r[2], r[3]});
+        }
+    };
+    // element j + e of the lane's D/16 elements of keys 2i and 2i + 1 side by side
+    const auto values = [&](int j, V8 *x) {
+#pragma unroll
+        for (int e = 0; e < R::GJ; e++) {
+            u32x4 y;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                y[i] = __builtin_amdgcn_perm(vr[2 * i + 1][(j + e) / 2], vr[2 * i][(j + e) / 2],
+                                             (j + e) % 2 == 0 ? 0x05040100u : 0x07060302u);
+            x[e] = __builtin_bit_cast(V8, y);
+        }
     };
 
     // the chunk of the context
@@ -563,28 +648,32 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void tree_attention_
         load_ctx_k(c0 + wk * kTile);
         load_ctx_v(c0 + wk * kTile);
     }
+    f32x4 score[NT][2];
+    float tops[NT];
+#pragma unroll 1
     for (uint32_t first = c0 + wk * kTile; first < c1; first += kWaves * kTile) {
         const uint32_t next = first + kWaves * kTile;
         const bool some = first + kTile > c1;
+        const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; }, score, tops);
+        if (next < c1)
+            load_ctx_k(next);
         if (some) {
             // values of keys past the end meet weights of 0 and have to be finite: 0
 #pragma unroll
             for (int i = 0; i < 8; i++)
 #pragma unroll
                 for (int j = 0; j < DJ / 2; j++)
-                    vr[i][j] = first + key_of(q4, i) < c1 ? vr[i][j] : 0;
+                    vr[i][j] = key_of(q4, i) < c1 - first ? vr[i][j] : 0;
         }
-        rows.tile(g, some, key, value, [&](int, int i) { return first + key_of(q4, i) < c1; },
-                  [&] {
-                      if (next < c1)
-                          load_ctx_k(next);
-                  });
+        if (raise)
+            rows.raise_maxima(g, tops);
+        rows.apply(g, score, values);
         if (next < c1)
             load_ctx_v(next);
     }
 
     // the drafted nodes, with the sequence's last chunk
-    if (keys.last) {
+    if (w.last) {
         const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
         const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
         const uint32_t count = keys.count;
@@ -605,181 +694,306 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void tree_attention_
 #pragma unroll
             for (int t = 0; t < NT; t++)
                 bits[t] = keys.seen(t * 16 + n, first);
-            rows.tile(g, true, key, value, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, [] {});
+            if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, score, tops))
+                rows.raise_maxima(g, tops);
+            rows.apply(g, score, values);
             if (__any(wild))
                 rows.add_wild(g, vb, first, min(first + kTile, count), bits,
                               [&](int j, int r) { return (4 * q4 + r) * DJ + j; });
         }
     }
 
-    rows.template join<1, kWaves>(g, merge);
+    rows.template join<1, kWaves>(g, merge, wk, lane);
     if (wk == 0)
         rows.template close<2 * DJ % 8 == 0 ? 8 : 4>(
-            g, w, head, 0, keys.count, [&](int i) { return 4 * q4 * DJ + i * (2 * DJ % 8 == 0 ? 8 : 4); },
+            g, w, head, 0, lane, [&](int i) { return 4 * q4 * DJ + i * (2 * DJ % 8 == 0 ? 8 : 4); },
             [&](int t, int i, int e) {
                 const int k = i * (2 * DJ % 8 == 0 ? 8 : 4) + e;
                 return rows.o[t][k % DJ][k / DJ];
             });
+    }   // join() left the LDS free
 }
 
 // ---- many rows -----------------------------------------------------------------
 //
 // More rows than one wave can hold: eight waves share the keys and values of a
 // workgroup's steps through LDS, WM of them with rows of their own, 8 / WM
-// dividing the step's tiles.  A step of kStep keys is copied from memory to
-// registers while the one before is worked on, and from there to the other of
-// two LDS buffers.  A key's 16-byte pieces are stored at places
+// dividing the step's tiles.  A step of kStep keys comes from memory to one of two
+// LDS buffers while the step before is worked on in the other.  A key's 16-byte pieces are stored at places
 // piece ^ (key % 16), so that neither product's reads, one a column of
 // pieces and one a transposing read of four keys, meet in the banks.
 constexpr int kSharedWaves = 8;
 constexpr int shared_nt(int head_dim) { return head_dim <= 128 ? 2 : 1; }
-constexpr int shared_step(int head_dim) { return head_dim <= 128 ? 128 : 64; }
+// Keys of a step: a tile at least for each wave that divides them, whole pieces for each thread.
+constexpr int shared_step(int head_dim, int wm) { return head_dim < 128 || wm == 2 ? 128 : 64; }
+
+// Place of a piece in its key's row of D / 8. The first product reads one piece of sixteen keys at
+// once, the second two neighbouring pieces of eight: with these places both meet every bank once
+// (for 96 elements nearly so), where plain rows would meet the same few.
+template <int D>
+__device__ __forceinline__ uint32_t place_of_piece(uint32_t key, uint32_t piece) {
+    if constexpr (D >= 128)
+        return piece ^ ((key & 7) << 1 | (key >> 3 & 1));
+    else if constexpr (D == 64)
+        return piece ^ ((key >> 1 & 3) << 1 | (key >> 3 & 1));
+    else
+        return (piece + (key >> 2 & 3)) % (D / 8);
+}
+// The piece at a place: the way back.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at_place(uint32_t key, uint32_t place) {
+    if constexpr (D == 96)
+        return (place + D / 8 - (key >> 2 & 3)) % (D / 8);
+    else
+        return place_of_piece<D>(key, place);
+}
 
 template <typename T, int D, int WM>
 __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_kernel(AttnArgs g) {
-    constexpr int NT = shared_nt(D), kStep = shared_step(D), WK = kSharedWaves / WM;
+    constexpr int NT = shared_nt(D), kStep = shared_step(D, WM), WK = kSharedWaves / WM;
     constexpr int kThreads = 64 * kSharedWaves, kPieces = D / 8, kEach = kStep * kPieces / kThreads;
     static_assert(kStep * kPieces % kThreads == 0 && kStep % (WK * kTile) == 0, "step");
     typedef Rows<T, D, NT> R;
     typedef typename R::V8 V8;
     constexpr int kBuffer = kStep * D * 2;   // bytes of a step's keys, or values
-    constexpr int kSwizzle = kPieces >= 16 ? 15 : (kPieces == 8 ? 7 : 0);   // 12 pieces: their rows differ in banks by themselves
-    union Lds {
-        uint8_t data[2][2][kBuffer];         // [buffer][keys, values]
-        float merge[WK > 1 ? WM * WK / 2 * R::kMergeFloats : 1];
-    };
-    __shared__ __attribute__((aligned(16))) Lds lds;
-    __shared__ Work work;
+    constexpr int kMerge = WK > 1 ? WM * WK / 2 * R::kMergeFloats * 4 : 0;
+    // two buffers, keys before values
+    __shared__ __attribute__((aligned(16))) uint8_t data[4 * kBuffer > kMerge ? 4 * kBuffer : kMerge];
+    __shared__ Place place;
     __shared__ uint64_t sums[kSharedWaves];
     __shared__ uint32_t list[kListPages];
-    __shared__ uint32_t wild_step[2];        // by buffer: the last step with values that are not finite, plus 1
+    __shared__ uint32_t wild_step;           // the last step of nodes with values that are not finite, plus 1
 
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q4 = lane >> 4;
-    const uint32_t wm = wave % WM, wk = wave / WM;
-    // The row blocks of one head's chunk run on one XCD, one after the other: they read the same keys.
+    const uint32_t wave = uniform(threadIdx.x >> 6), wm = wave % WM, wk = wave / WM;
+    // The row blocks of one head's share run on one XCD, one after the other: they read the same keys.
     uint32_t unit = blockIdx.x, block = 0;
     if (g.row_blocks > 1) {
         const uint32_t at = blockIdx.x >> 3;
         block = at % g.row_blocks;
         unit = at / g.row_blocks * 8 + (blockIdx.x & 7);
     }
-    const uint32_t head = unit % g.heads;
-    find_work<kSharedWaves>(g, (int32_t)(unit / g.heads), &work, sums);
-    if (work.batch < 0)
+    const uint32_t mine = unit / g.heads, head = unit % g.heads;
+    if (mine >= g.budget)
         return;
-    const Work w = work;
+    find_place<kSharedWaves>(g, mine, &place, sums);
+    Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
+#pragma unroll 1
+    for (; at.batch < g.batch && at.start < (mine + 1) * at.share; at.batch++) {
+    const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
+    const Part w(g, at, mine);
+    at.start = w.end;
     note_splits(g, w, head, block);
     const Keys<kSharedWaves> keys(g, w, head, list);
-    const uint32_t c0 = keys.c0, c1 = keys.c1, count = keys.count;
+    const uint32_t c0 = w.c0, c1 = w.c1, count = w.seq.nodes;
     const uint32_t row0 = (block * WM + wm) * 16 * NT;
     R rows;
-    rows.open(g, keys.b, head, row0);
-    if (threadIdx.x < 2)
-        wild_step[threadIdx.x] = 0;
+    rows.open(g, keys.b, head, row0, lane);
+    if (threadIdx.x == 0)
+        wild_step = 0;
     __syncthreads();
 
-    const uint32_t steps_ctx = c1 > c0 ? (c1 - c0 + kStep - 1) / kStep : 0;
-    const uint32_t steps = steps_ctx + (keys.last ? (count + kStep - 1) / kStep : 0);
-    const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
-    const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
-
-    u32x4 sk[kEach], sv[kEach];
-    const auto fetch = [&](uint32_t step) {
-        const bool ctx = step < steps_ctx;
-        const uint32_t first = ctx ? c0 + step * kStep : (step - steps_ctx) * kStep, end = ctx ? c1 : count;
+    // This thread's pieces of a step: place at % kPieces of key at / kPieces, at = i * kThreads + thread.
+    // Each wave's loads go straight to LDS, 64 places in a row.
+    const uint64_t pools_apart = reinterpret_cast<uint64_t>(g.v_cache) - reinterpret_cast<uint64_t>(g.k_cache);
+    // The key of each piece as its page in the list and its place in the page, carried from step to step.
+    const uint32_t head_at = head * g.head_step, page_end = g.page_tokens * g.token_step;
+    const uint32_t pages_on = keys.page_of(kStep), places_on = (kStep - pages_on * g.page_tokens) * g.token_step;
+    uint32_t in_list[kEach], in_page[kEach];
 #pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const uint32_t at = i * kThreads + threadIdx.x, key = at / kPieces, piece = at % kPieces;
-            const uint32_t k = min(first + key, end - 1);
-            uint64_t ka, va;
-            if (ctx) {
-                const uint64_t off = keys.offset_of(k) + piece * 16;
-                ka = reinterpret_cast<uint64_t>(g.k_cache) + off;
-                va = reinterpret_cast<uint64_t>(g.v_cache) + off;
-            } else {
-                ka = kb + k * g.k_stride[1] + piece * 16;
-                va = vb + k * g.v_stride[1] + piece * 16;
-            }
-            sk[i] = *(const gu32x4 *)ka;
-            sv[i] = *(const gu32x4 *)va;
-        }
-    };
-    const auto put = [&](uint32_t step) {
-        const bool ctx = step < steps_ctx;
-        const uint32_t first = ctx ? c0 + step * kStep : (step - steps_ctx) * kStep, end = ctx ? c1 : count;
-        uint32_t wild = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const uint32_t at = i * kThreads + threadIdx.x, key = at / kPieces, piece = at % kPieces;
-            const uint32_t to = (key * kPieces + (piece ^ (key & kSwizzle))) * 16;
-            // values of keys past the end, and (until add_wild) those that are not finite, count as 0
-            u32x4 v = first + key < end ? sv[i] : (u32x4){0, 0, 0, 0};
-            if (!ctx)
-                for (int e = 0; e < 4; e++)
-                    v[e] = tamed<T>(v[e], &wild);
-            *reinterpret_cast<u32x4 *>(lds.data[step & 1][0] + to) = sk[i];
-            *reinterpret_cast<u32x4 *>(lds.data[step & 1][1] + to) = v;
-        }
-        if (wild)
-            wild_step[step & 1] = step + 1;
-    };
-
-    if (steps > 0) {
-        fetch(0);
-        put(0);
+    for (int i = 0; i < kEach; i++) {
+        const uint32_t token = c0 + (i * kThreads + thread) / kPieces, p = keys.page_of(token);
+        in_list[i] = p - keys.p0;
+        in_page[i] = (token - p * g.page_tokens) * g.token_step;
     }
-    __syncthreads();
-    for (uint32_t step = 0; step < steps; step++) {
-        if (step + 1 < steps)
-            fetch(step + 1);
-        const bool ctx = step < steps_ctx;
-        const uint32_t first = ctx ? c0 + step * kStep : (step - steps_ctx) * kStep, end = ctx ? c1 : count;
-        const bool wild = wild_step[step & 1] == step + 1;
-#pragma unroll 1
-        for (uint32_t tile = wk; tile < kStep / kTile; tile += WK) {
-            const uint32_t t0 = first + tile * kTile;
-            if (t0 >= end)
-                break;
-            const uint8_t *kp = lds.data[step & 1][0] + tile * kTile * D * 2, *vp = lds.data[step & 1][1] + tile * kTile * D * 2;
-            const auto key = [&](int z, int k) {
-                const uint32_t row = z * 16 + n;
-                return *reinterpret_cast<const V8 *>(kp + (row * kPieces + ((k * 4 + q4) ^ (row & kSwizzle))) * 16);
-            };
-            // elements 16 j .. 16 j + 15 of the lane group's eight keys, transposed on the way: two reads of four keys
-            const auto value = [&](int j) {
-                typedef short s16x4 __attribute__((ext_vector_type(4)));
-                typedef __attribute__((address_space(3))) s16x4 ls16x4;
-                s16x4 half[2];
+    // Called for the part's steps in turn.
+    const auto fetch = [&](uint8_t *to, uint32_t first) {
+        uint32_t place[kEach];
+        const bool whole = keys.listed && first + kStep <= c1;
+        if (whole) {
 #pragma unroll
-                for (int z = 0; z < 2; z++) {
-                    const uint32_t row = z * 16 + 4 * q4 + n / 4, piece = 2 * j + (n % 4) / 2;
-                    half[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (ls16x4 *)(vp + (row * kPieces + (piece ^ (row & kSwizzle))) * 16 + (n & 1) * 8));
-                }
-                return __builtin_bit_cast(V8, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
-            };
-            if (ctx) {
-                rows.tile(g, t0 + kTile > c1, key, value, [&](int, int i) { return t0 + key_of(q4, i) < c1; }, [] {});
-            } else {
-                uint32_t bits[NT];
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-                    bits[t] = keys.seen(row0 + t * 16 + n, t0);
-                rows.tile(g, true, key, value, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, [] {});
-                if (wild)
-                    rows.add_wild(g, vb, t0, min(t0 + kTile, count), bits,
-                                  [&](int j, int r) { return 16 * j + 4 * q4 + r; });
+            for (int i = 0; i < kEach; i++) {
+                place[i] = list[in_list[i]] + in_page[i] + head_at;
+                const uint32_t next = in_page[i] + places_on;
+                const bool over = next >= page_end;
+                in_page[i] = over ? next - page_end : next;
+                in_list[i] += over ? pages_on + 1 : pages_on;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; i++)
+                place[i] = keys.place_of(min(first + (i * kThreads + thread) / kPieces, c1 - 1));
         }
-        if (step + 1 < steps)
-            put(step + 1);
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const uint32_t at = i * kThreads + thread, key = at / kPieces, piece = piece_at_place<D>(key, at % kPieces);
+            const uint64_t from = reinterpret_cast<uint64_t>(g.k_cache) + (uint64_t)(place[i] + piece) * 16;
+            uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
+            __builtin_amdgcn_global_load_lds((const gvoid *)from, (svoid *)there, 16, 0, kStream);
+            __builtin_amdgcn_global_load_lds((const gvoid *)(from + pools_apart), (svoid *)(there + kBuffer), 16, 0, kStream);
+        }
+    };
+    // Waits for the step's loads; values of keys past the end meet weights of 0 and have to be finite: 0.
+    const auto arrived = [&](uint8_t *to, uint32_t left) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (left < kStep) {
+            for (uint32_t at = left * kPieces + thread; at < kStep * kPieces; at += kThreads)
+                *reinterpret_cast<u32x4 *>(to + kBuffer + at * 16) = (u32x4){0, 0, 0, 0};
+            __syncthreads();
+        }
+    };
+
+    // Where this lane reads in a tile.  The reads are in assembly, each group with its own wait: the compiler
+    // does not see that they have nothing to do with the loads on their way to the other buffer, and
+    // would wait for those as well.
+    const uint32_t data_at = (uint32_t)(uintptr_t)(svoid *)data;
+    uint32_t key_at[R::KS], value_at[R::DJ];
+#pragma unroll
+    for (int k = 0; k < R::KS; k++)
+        key_at[k] = (n * kPieces + place_of_piece<D>(n, k * 4 + q4)) * 16;
+#pragma unroll
+    for (int j = 0; j < R::DJ; j++) {
+        const uint32_t row = 4 * q4 + n / 4;
+        value_at[j] = kBuffer + (row * kPieces + place_of_piece<D>(row, 2 * j + (n % 4) / 2)) * 16 + (n & 1) * 8;
+    }
+    uint32_t tile_at = 0;   // of the tile in LDS
+    const auto key = [&](int k, V8 *x) {
+        u32x4 y[4];
+        if (k + 1 < R::KS)
+            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\t"
+                         "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+                         : "v"(tile_at + key_at[k]), "v"(tile_at + key_at[k + 1 < R::KS ? k + 1 : k]), "n"(16 * D * 2)
+                         : "memory");
+        else
+            asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(y[0]), "=&v"(y[1])
+                         : "v"(tile_at + key_at[k]), "n"(16 * D * 2)
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < 4 && k + i / 2 < R::KS; i++)
+            x[i] = __builtin_bit_cast(V8, y[i]);
+    };
+    // Elements 16 j .. 16 j + 15 of the lane group's eight keys, transposed on the way: two reads of four keys.
+    const auto values = [&](int j, V8 *x) {
+        u32x2 y[2 * R::GJ];
+        if constexpr (R::GJ == 4)
+            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7])
+                         : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "v"(tile_at + value_at[j + R::GJ - 2]),
+                           "v"(tile_at + value_at[j + R::GJ - 1]), "n"(16 * D * 2)
+                         : "memory");
+        else
+            asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                         "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+                         : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "n"(16 * D * 2)
+                         : "memory");
+#pragma unroll
+        for (int e = 0; e < R::GJ; e++)
+            x[e] = __builtin_bit_cast(V8, (u32x4){y[2 * e].x, y[2 * e].y, y[2 * e + 1].x, y[2 * e + 1].y});
+    };
+    f32x4 score[NT][2];
+    float tops[NT];
+
+    // The part of the context.  Every wave does kTurns tiles of each step, also of the last one, where keys past
+    // the end are masked.  The scores of a tile are had at the end of the turn before its
+    // own, so that the loop has one way out, at its end, for the end and for maxima that have
+    // to be raised alike: with a branch or a break inside, the compiler moves all accumulators in
+    // every turn.  (After the last tile the scores of it are had once more, for nothing.)
+    constexpr uint32_t kTurns = kStep / kTile / WK, kTileBytes = kTile * D * 2;
+    if (c0 < c1) {
+        fetch(data, c0);
+        arrived(data, c1 - c0);
+        if (c0 + kStep < c1)
+            fetch(data + 2 * kBuffer, c0 + kStep);
+        uint32_t first = c0, turn = 0, buffer = 0;
+        const auto look = [&] {
+            tile_at = uniform(data_at + buffer * 2 * kBuffer + (turn * WK + wk) * kTileBytes);
+            const uint32_t t0 = first + (turn * WK + wk) * kTile;
+            return rows.scores(g, t0 + kTile > c1, key, [&](int, int i) { return t0 + key_of(q4, i) < c1; }, score, tops);
+        };
+        bool raise = look();
+        bool more = true;
+        do {
+            if (raise)
+                rows.raise_maxima(g, tops);
+            do {
+                rows.apply(g, score, values);
+                turn++;
+                if (turn == kTurns) {
+                    more = first + kStep < c1;
+                    if (more) {
+                        turn = 0;
+                        buffer ^= 1;
+                        first += kStep;
+                        arrived(data + buffer * 2 * kBuffer, c1 - first);
+                        if (first + kStep < c1)
+                            fetch(data + (buffer ^ 1) * 2 * kBuffer, first + kStep);
+                    } else {
+                        turn = kTurns - 1;
+                    }
+                }
+                raise = look();
+            } while (more && !raise);
+        } while (more);
         __syncthreads();
     }
 
-    rows.template join<WM, WK>(g, lds.merge);
+    // the drafted nodes, with the sequence's last chunk
+    const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
+    const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+#pragma unroll 1
+    for (uint32_t first = 0; w.last && first < count; first += kStep) {
+        uint32_t wild = 0;
+#pragma unroll 1
+        for (uint32_t at = thread; at < kStep * kPieces; at += kThreads) {
+            const uint32_t key = at / kPieces, piece = at % kPieces;
+            const uint32_t u = min(first + key, count - 1), to = (key * kPieces + place_of_piece<D>(key, piece)) * 16;
+            *reinterpret_cast<u32x4 *>(data + to) = *(const gu32x4 *)(kb + u * g.k_stride[1] + piece * 16);
+            // A value that is not finite would turn a weight of 0 into NaN: here it counts
+            // as 0, and the rows that do see it get it added afterwards.
+            u32x4 x = {0, 0, 0, 0};
+            if (first + key < count)
+                x = *(const gu32x4 *)(vb + u * g.v_stride[1] + piece * 16);
+            for (int e = 0; e < 4; e++)
+                x[e] = tamed<T>(x[e], &wild);
+            *reinterpret_cast<u32x4 *>(data + kBuffer + to) = x;
+        }
+        if (wild)
+            wild_step = first + 1;
+        __syncthreads();
+        const bool any_wild = wild_step == first + 1;
+#pragma unroll 1
+        for (uint32_t turn = 0; turn < kTurns; turn++) {
+            const uint32_t tile = turn * WK + wk, t0 = first + tile * kTile;
+            if (t0 >= count)
+                break;
+            tile_at = uniform(data_at + tile * kTileBytes);
+            uint32_t bits[NT];
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+                bits[t] = keys.seen(row0 + t * 16 + n, t0);
+            if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, score, tops))
+                rows.raise_maxima(g, tops);
+            rows.apply(g, score, values);
+            if (any_wild)
+                rows.add_wild(g, vb, t0, min(t0 + kTile, count), bits, [&](int j, int r) { return 16 * j + 4 * q4 + r; });
+        }
+        __syncthreads();
+    }
+
+    rows.template join<WM, WK>(g, reinterpret_cast<float *>(data), wave, lane);
     if (wk == 0)
-        rows.template close<4>(g, w, head, row0, count, [&](int i) { return 16 * i + 4 * q4; },
+        rows.template close<4>(g, w, head, row0, lane, [&](int i) { return 16 * i + 4 * q4; },
                                [&](int t, int i, int e) { return rows.o[t][i][e]; });
+    __syncthreads();   // before the next part fills the LDS
+    }
 }
 
 // Joins the chunks of sequences that have several: one wave a row.
@@ -794,31 +1008,56 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
     const int32_t splits = g.split_count[b];
     if (splits <= 1)
         return;
-    const uint64_t first = (uint64_t)g.split_base[b];
-    float m = -INFINITY;
-    for (int32_t s = lane; s < splits; s += 64)
-        m = fmaxf(m, g.part_ml[2 * (((first + s) * g.heads + head) * g.rows + r)]);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-        m = fmaxf(m, __shfl_xor(m, d));
-    const float base = m == -INFINITY ? 0.f : m * g.scale2;
+    const uint64_t first = (uint64_t)g.split_base[b], step = (uint64_t)g.heads * g.rows;
+    const uint64_t slot0 = first * step + (uint64_t)head * g.rows + r;
+    // 64 / kLanes groups of lanes take every so many-th split, kLanes * 4 elements each
+    constexpr uint32_t kLanes = D <= 64 ? 16 : (D <= 128 ? 32 : 64), kGroups = 64 / kLanes;
+    const uint32_t part = lane / kLanes, at4 = lane % kLanes * 4;
+    float m = -INFINITY, l = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int32_t s = 0; s < splits; s++) {
-        const uint64_t k = ((first + s) * g.heads + head) * g.rows + r;
-        const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(g.part_ml[2 * k], g.scale2, -base));
-        l += f * g.part_ml[2 * k + 1];
-        if (lane * 4 < D) {
-            const f32x4 x = *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + lane * 4) * 4);
-            o += x * f;
+    for (int32_t s0 = 0; s0 < splits; s0 += 64) {   // lane s has split s0 + s's maximum and sum
+        const bool there = s0 + (int32_t)lane < splits;
+        float ms = -INFINITY, ls = 0.f;
+        if (there) {
+            const uint64_t k = slot0 + (uint64_t)(s0 + lane) * step;
+            ms = g.part_ml[2 * k];
+            ls = g.part_ml[2 * k + 1];
+        }
+        float top = fmaxf(ms, m);
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor(top, d));
+        const float base = top == -INFINITY ? 0.f : top * g.scale2;
+        const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m, g.scale2, -base));
+        const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(ms, g.scale2, -base));
+        m = top;
+        o *= fade;
+        float sum = f * ls;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            sum += __shfl_xor(sum, d);
+        l = l * fade + sum;
+        const int32_t n = splits - s0 < 64 ? splits - s0 : 64;
+        for (int32_t i = 0; i < n; i += kGroups) {   // every lane in every turn: all supply their f
+            const int32_t s = i + (int32_t)part;
+            const float fs = __shfl(f, s < 64 ? s : 63);
+            if (s < n && at4 < D) {
+                const uint64_t k = slot0 + (uint64_t)(s0 + s) * step;
+                o += *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + at4) * 4) * fs;
+            }
         }
     }
+#pragma unroll
+    for (uint32_t d = kLanes; d < 64; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            o[e] += __shfl_xor(o[e], (int)d);
     const uint32_t node = r / g.group, h = head * g.group + r % g.group;
     int32_t nodes = (int32_t)g.nodes;
     if (g.tree_nodes != nullptr)
         nodes = g.tree_nodes[b];
     const bool empty = l == 0.f || (int32_t)node >= nodes;
-    if (lane * 4 < D) {
+    if (part == 0 && at4 < D) {
         typedef T t4 __attribute__((ext_vector_type(4)));
         t4 x;
         for (int e = 0; e < 4; e++)
@@ -834,17 +1073,24 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
 // Which kernel, how many of its waves hold rows of their own, and the rows of a workgroup.
 struct Shape {
     bool shared;
-    int nt, wm;
+    int wm;
     uint32_t rows;
 };
 static Shape shape_of(uint32_t rows, uint32_t head_dim) {
-    if (rows <= 16 || (rows <= 32 && head_dim <= 128))
-        return {false, rows <= 16 ? 1 : 2, 1, rows <= 16 ? 16u : 32u};
+    if (rows <= 16)
+        return {false, 1, 16};
     const uint32_t each = 16 * shared_nt((int)head_dim);
     int wm = head_dim <= 128 ? 2 : 4;
     while (wm < kSharedWaves && wm * each < rows)
         wm *= 2;
-    return {true, 0, wm, wm * each};
+    return {true, wm, wm * each};
+}
+
+// Workgroups of the kernel that a CU holds, by the registers they are built with.
+static uint32_t resident(const Shape &s, uint32_t head_dim) {
+    if (s.shared)
+        return 1;
+    return head_dim == 64 ? 3 : (head_dim <= 128 ? 2 : 1);
 }
 
 struct Plan {
@@ -857,10 +1103,20 @@ static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count) {
     p.rows = a.nodes * (a.heads_q / heads);
     p.shape = shape_of(p.rows, a.head_dim);
     p.row_blocks = (p.rows + p.shape.rows - 1) / p.shape.rows;
-    const uint32_t target = (uint32_t)cu_count * (p.shape.shared ? 2 : (p.shape.nt == 1 ? 3 : 2));
-    p.budget = target / (heads * p.row_blocks);
-    if (p.budget < 1)
-        p.budget = 1;
+    // Shares a head's stream is cut into: as many as run at once, or, where heads and row
+    // blocks leave CUs idle that way, the number up to four rounds that leaves the fewest.
+    const uint64_t each = (uint64_t)heads * p.row_blocks, room = (uint64_t)cu_count * resident(p.shape, a.head_dim);
+    const uint64_t most = 4 * room / each > 1 ? 4 * room / each : 1, least = room / each > 1 ? room / each : 1;
+    uint64_t best = least;
+    double best_use = 0;
+    for (uint64_t n = least; n <= most; n++) {
+        const double use = (double)(n * each) / (double)((n * each + room - 1) / room * room);
+        if (use > best_use + 0.04) {
+            best = n;
+            best_use = use;
+        }
+    }
+    p.budget = (uint32_t)best;
     p.slots = (uint64_t)p.budget + a.batch;
     return p;
 }
@@ -878,12 +1134,7 @@ static hipError_t launch_dim(const AttnArgs &g, Shape s, uint32_t grid, hipStrea
     LaunchSeq seq;
     hipError_t e;
     if (!s.shared) {
-        if (s.nt == 1)
-            e = launch(tree_attention_kernel<T, D, 1>, grid, 64 * kWaves, stream, nullptr, g);
-        else if constexpr (D <= 128)
-            e = launch(tree_attention_kernel<T, D, 2>, grid, 64 * kWaves, stream, nullptr, g);
-        else
-            e = hipErrorInvalidValue;
+        e = launch(tree_attention_kernel<T, D>, grid, 64 * kWaves, stream, nullptr, g);
     } else if (s.wm == 8) {
         e = launch(tree_attention_shared_kernel<T, D, 8>, grid, 64 * kSharedWaves, stream, nullptr, g);
     } else if (s.wm == 4) {
@@ -940,9 +1191,9 @@ hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int c
     g.group = a.heads_q / c.heads;
     g.rows = p.rows;
     const bool token_major = c.layout == TB_CACHE_TOKEN_MAJOR;
-    g.page_stride = (uint32_t)c.page_stride;
-    g.token_step = token_major ? c.heads * c.head_bytes : c.head_bytes;
-    g.head_step = token_major ? c.head_bytes : c.page_tokens * c.head_bytes;
+    g.page_step = (uint32_t)(c.page_stride / 16);
+    g.token_step = (token_major ? c.heads * c.head_bytes : c.head_bytes) / 16;
+    g.head_step = (token_major ? c.head_bytes : c.page_tokens * c.head_bytes) / 16;
     g.num_pages = c.num_pages;
     g.page_tokens = c.page_tokens;
     g.max_seqs = c.max_seqs;
@@ -966,7 +1217,7 @@ hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int c
     g.split_count = g.split_base + a.batch;
     g.part_ml = reinterpret_cast<float *>(ws + round16(8ull * a.batch));
     g.part_o = reinterpret_cast<float *>(ws + round16(8ull * a.batch) + round16(8 * rows));
-    const uint64_t units = p.slots * c.heads;
+    const uint64_t units = (uint64_t)p.budget * c.heads;
     const uint64_t grid = p.row_blocks > 1 ? (units + 7) / 8 * 8 * p.row_blocks : units;
     if (grid > (1u << 30))
         return hipErrorInvalidValue;

@@ -251,7 +251,7 @@ int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;
     if (!aligned(c->pools[a->k_pool], 16) || !aligned(c->pools[a->v_pool], 16) || c->page_stride % 16 != 0 ||
-        c->page_stride >= (1ull << 32) || a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
+        c->page_stride * c->num_pages > TB_ATTN_MAX_POOL || a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
         !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
         !list_ok(a->seqs) || !aligned(a->mask, 8) || !aligned(a->tree_nodes, 4))
         return TB_ERR_INVALID;

@@ -148,6 +148,9 @@ int tb_page_resize(const tb_cache *cache, const int32_t *seqs, const int32_t *le
  */
 int tb_page_compact(const tb_cache *cache, void *stream);
 
+/* Largest pool that tb_tree_attention reads: page_stride * num_pages. */
+#define TB_ATTN_MAX_POOL (1ull << 36)
+
 /* Element types of tb_tree_attention. */
 enum { TB_BF16 = 0, TB_FP16 = 1 };
 
