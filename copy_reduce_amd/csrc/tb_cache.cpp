@@ -76,31 +76,38 @@ bool vectors_fit(const tb_cache *c) {
     return true;
 }
 
-// Copy the pairs' pages in every pool, in launches of kPoolsPerLaunch pools.
-// `by_head`: the used tokens of a head-major page are a stretch a head.
-hipError_t copy_pages(const tb_cache *dst, const tb_cache *src, const tbk::PagePairs &pairs, hipStream_t stream) {
+// Calls launch_one(pools, npools, shape, fit, last) for the pools of both caches, kPoolsPerLaunch at a time (once,
+// with none, for caches without pools).  `parts`: the used tokens of a head-major page are a stretch a head.
+template <typename Launch>
+hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launch launch_one) {
     tbk::PageShape g;
     g.src_stride = src->page_stride;
     g.dst_stride = dst->page_stride;
     g.src_pages = src->num_pages;
     g.dst_pages = dst->num_pages;
     g.page_tokens = dst->page_tokens;
-    const bool parts = pairs.tokens != nullptr && dst->layout == TB_CACHE_HEAD_MAJOR;
+    parts = parts && dst->layout == TB_CACHE_HEAD_MAJOR;
     g.runs = parts ? dst->heads : 1;
     g.token_bytes = (uint32_t)(parts ? dst->head_bytes : token_bytes(dst));
     const bool fit = vectors_fit(dst) && vectors_fit(src);
-    for (uint32_t p0 = 0; p0 < dst->npools; p0 += tbk::kPoolsPerLaunch) {
+    if (dst->npools == 0) {   // what rides along with the copy has to run all the same; no page is in range
+        g.src_pages = g.dst_pages = 0;
+        const tbk::Pools none = {};
+        return launch_one(none, 1, g, true, true);
+    }
+    uint32_t p0 = 0;
+    do {
         const uint32_t n = dst->npools - p0 < tbk::kPoolsPerLaunch ? dst->npools - p0 : tbk::kPoolsPerLaunch;
         tbk::Pools pools;
-        memset(&pools, 0, sizeof(pools));
         for (uint32_t p = 0; p < n; p++) {
             pools.src[p] = reinterpret_cast<uintptr_t>(src->pools[p0 + p]);
             pools.dst[p] = reinterpret_cast<uintptr_t>(dst->pools[p0 + p]);
         }
-        const hipError_t e = tbk::launch_page_copy(pools, n, g, pairs, fit, stream);
+        p0 += n;
+        const hipError_t e = launch_one(pools, n, g, fit, p0 == dst->npools);
         if (e != hipSuccess)
             return e;
-    }
+    } while (p0 < dst->npools);
     return hipSuccess;
 }
 
@@ -133,7 +140,12 @@ int tb_page_copy(const tb_cache *dst, const tb_cache *src, const int32_t *dst_pa
     if (!list_ok(dst_pages) || !list_ok(src_pages))
         return TB_ERR_INVALID;
     tbk::PagePairs pairs = {src_pages, dst_pages, nullptr, nullptr, n};
-    const hipError_t e = copy_pages(dst, src, pairs, static_cast<hipStream_t>(stream));
+    tbk::LaunchSeq seq;
+    const hipError_t e = for_pools(dst, src, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+        if (last)
+            seq.last();
+        return tbk::launch_page_copy(pools, np, g, pairs, fit, static_cast<hipStream_t>(stream));
+    });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page copy launch");
 }
 
@@ -192,11 +204,15 @@ int tb_page_fork(const tb_cache *cache, const int32_t *parents, const int32_t *c
         return TB_ERR_INVALID;
     const tbk::CacheState s = state_of(cache);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    hipError_t e = tbk::launch_fork_tables(s, parents, children, n, st);
-    if (e == hipSuccess) {
-        tbk::PagePairs pairs = {s.w.from, s.w.to, s.w.aux, nullptr, n};
-        e = copy_pages(cache, cache, pairs, st);
-    }
+    tbk::LaunchSeq seq;
+    hipError_t e = tbk::launch_fork_plan(s, parents, children, n, st);
+    const tbk::PagePairs pairs = {s.w.from, s.w.to, s.w.aux, nullptr, n};
+    if (e == hipSuccess)
+        e = for_pools(cache, cache, true, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+            if (last)
+                seq.last();
+            return tbk::launch_fork_copy(pools, np, g, pairs, fit, s, parents, children, n, last, st);
+        });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page fork launch");
 }
 
@@ -218,13 +234,13 @@ int tb_page_compact(const tb_cache *cache, void *stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     tbk::LaunchSeq seq;
     hipError_t e = tbk::launch_compact_plan(s, st);
-    if (e == hipSuccess && cache->num_pages > 1) {
-        tbk::PagePairs pairs = {s.w.from, s.w.to, nullptr, s.w.pairs, cache->num_pages / 2};
-        e = copy_pages(cache, cache, pairs, st);
-    }
-    seq.last();
+    const tbk::PagePairs pairs = {s.w.from, s.w.to, nullptr, s.w.pairs, cache->num_pages / 2};
     if (e == hipSuccess)
-        e = tbk::launch_compact_apply(s, st);
+        e = for_pools(cache, cache, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+            if (last)
+                seq.last();
+            return tbk::launch_compact_copy(pools, np, g, pairs, fit, s, last, st);
+        });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page compact launch");
 }
 

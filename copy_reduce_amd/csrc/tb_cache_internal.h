@@ -24,11 +24,12 @@ struct Scratch32 {
     int32_t *claim;    // [max_seqs]
     uint32_t *chunk;   // [2 * chunks] free pages below / used pages above the border, by chunk
     uint32_t *pairs;   // [1] pages that the compaction moves
+    uint32_t *top;     // [1] free pages before a resize
 };
 
 inline uint64_t scratch_words(uint32_t num_pages, uint32_t max_seqs, uint32_t *base, Scratch32 *out) {
     const uint64_t p = num_pages, s = max_seqs, most = p > s ? p : s;
-    const uint64_t sizes[8] = {(p + 31) / 32, most, most, p, s, s, 2 * ((p + kScanChunk - 1) / kScanChunk), 1};
+    const uint64_t sizes[8] = {(p + 31) / 32, most, most, p, s, s, 2 * ((p + kScanChunk - 1) / kScanChunk), 2};
     uint64_t at[9] = {0};
     for (int k = 0; k < 8; k++)
         at[k + 1] = (at[k] + sizes[k] + 3) / 4 * 4;   // 16-byte steps
@@ -41,6 +42,7 @@ inline uint64_t scratch_words(uint32_t num_pages, uint32_t max_seqs, uint32_t *b
         out->claim = reinterpret_cast<int32_t *>(base + at[5]);
         out->chunk = base + at[6];
         out->pairs = base + at[7];
+        out->top = base + at[7] + 1;
     }
     return at[8];
 }
@@ -109,14 +111,18 @@ hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape
                             bool aligned16, hipStream_t stream);
 hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a,
                          bool aligned16, hipStream_t stream);
-hipError_t launch_fork_tables(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
-                              hipStream_t stream);
+// A fork: its plan, then its pages (pairs over the plan) and, with the launch that has `rows`, its rows.
+hipError_t launch_fork_plan(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
+                            hipStream_t stream);
+hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
+                            bool aligned16, const CacheState &s, const int32_t *parents, const int32_t *children,
+                            uint32_t n, bool rows, hipStream_t stream);
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream);
-// The compaction's plan, then its tables; pages are copied between the two by
-// launch_page_copy.
+// A compaction: its plan, then its pages and, with the launch that has `apply`, its tables.
 hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream);
-hipError_t launch_compact_apply(const CacheState &s, hipStream_t stream);
+hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
+                               bool aligned16, const CacheState &s, bool apply, hipStream_t stream);
 
 hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream);
 uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count);

@@ -87,12 +87,43 @@ hipError_t launch_cache_init(const CacheState &s, hipStream_t stream) {
 
 // ---- page copy -----------------------------------------------------------------
 
-// One workgroup copies up to kCopyBlock bytes of one run of one page in one pool: x is
-// the place in the page, y the pool, z the pair (strided).
-constexpr uint32_t kCopyBlock = 256 * 16 * 4;
+// Raw buffer resource over [base, base + bytes): accesses outside are not made (the hardware checks).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_over(uint64_t base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
+}
 
-template <int E>
-__global__ __launch_bounds__(256) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks) {
+// What the bookkeeping still has to do while a fork's or a compaction's pages are copied: it goes
+// by the same plan and touches nothing that the copy does, so it rides along in the same launch.
+enum { kAlone = 0, kWithFork = 1, kWithCompact = 2 };
+struct Rider {
+    CacheState s;
+    const int32_t *parents, *children;
+    uint32_t n;
+};
+__device__ void fork_rows(const Rider &r, uint32_t block, uint32_t blocks);
+__device__ void compact_apply(const Rider &r, uint32_t block, uint32_t blocks);
+
+// One workgroup copies TH * U * 16 bytes of one run of one page in one pool: x is the place
+// in the page, y the pool, z the pair (strided).  The bytes are only moved, so HBM bounds it: whole pages with
+// one load in flight a thread, streaming past the caches (nt; nt sc0 sc1 for the stores), 400 pages of
+// 16 KiB in 64 pools in 147 us, 5.7 TB/s, against 162 us with four loads a thread, 153 us with one-wave
+// workgroups and 165 us through the caches.  A fork's partly used pages (the tokens before the
+// end only) go in small workgroups, of which those behind the end do nothing, and are loaded
+// through the caches, several children reading one page: 192 such pages of 32 KiB in 32 pools in 24 us;
+// nt loads 46 us for the whole call against 34.
+template <int E, int TH, int U, int LD, int ST, int WITH>
+__global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks, Rider rider) {
+    constexpr uint32_t kBlock = TH * 16 * U;
+    if constexpr (WITH != kAlone) {
+        if (blockIdx.x == blocks * g.runs) {
+            const uint32_t block = blockIdx.z * gridDim.y + blockIdx.y, all = gridDim.y * gridDim.z;
+            if constexpr (WITH == kWithFork)
+                fork_rows(rider, block, all);
+            else
+                compact_apply(rider, block, all);
+            return;
+        }
+    }
     const uint32_t run = blockIdx.x / blocks, block = blockIdx.x % blocks;
     const uint64_t run_step = (uint64_t)g.page_tokens * g.token_bytes;
     const uint64_t src0 = pools.src[blockIdx.y], dst0 = pools.dst[blockIdx.y];
@@ -106,32 +137,51 @@ __global__ __launch_bounds__(256) void page_copy_kernel(Pools pools, PageShape g
             const int32_t t = pairs.tokens[i];
             bytes = t > 0 ? (uint64_t)((uint32_t)t % g.page_tokens) * g.token_bytes : 0;
         }
-        const uint64_t src = src0 + a * g.src_stride + run * run_step, dst = dst0 + b * g.dst_stride + run * run_step;
+        const uint64_t begin = (uint64_t)block * kBlock;
+        if (begin >= bytes)
+            continue;
+        const uint32_t left = (uint32_t)(bytes - begin < kBlock ? bytes - begin : kBlock);
+        const uint64_t at = run * run_step + begin;
+        const uint64_t src = src0 + a * g.src_stride + at, dst = dst0 + b * g.dst_stride + at;
         if constexpr (E == 16) {
-            u32x4 v[4];
-            const uint64_t at = (uint64_t)block * kCopyBlock + threadIdx.x * 16;
+            const __amdgpu_buffer_rsrc_t in = buffer_over(src, left), out = buffer_over(dst, left);
+            u32x4 v[U];
 #pragma unroll
-            for (int u = 0; u < 4; u++)
-                if (at + u * 4096 < bytes)
-                    v[u] = *(const gu32x4 *)(src + at + u * 4096);
+            for (int u = 0; u < U; u++)
+                v[u] = __builtin_amdgcn_raw_buffer_load_b128(in, threadIdx.x * 16, u * TH * 16, LD);
 #pragma unroll
-            for (int u = 0; u < 4; u++)
-                if (at + u * 4096 < bytes)
-                    *(gu32x4 *)(dst + at + u * 4096) = v[u];
+            for (int u = 0; u < U; u++)
+                __builtin_amdgcn_raw_buffer_store_b128(v[u], out, threadIdx.x * 16, u * TH * 16, ST);
         } else {
-            for (uint64_t at = (uint64_t)block * kCopyBlock + threadIdx.x; at < bytes && at < (uint64_t)(block + 1) * kCopyBlock; at += 256)
-                *(gu8 *)(dst + at) = *(const gu8 *)(src + at);
+            for (uint32_t k = threadIdx.x; k < left; k += TH)
+                *(gu8 *)(dst + k) = *(const gu8 *)(src + k);
         }
     }
 }
 
+template <int E, int TH, int U, int LD, int ST, int WITH>
+static hipError_t launch_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
+                              const Rider &rider, hipStream_t stream) {
+    const uint64_t run = (uint64_t)g.page_tokens * g.token_bytes, block = TH * 16 * U;
+    const uint32_t blocks = (uint32_t)((run + block - 1) / block);
+    uint64_t z = pairs.n;
+    if (pairs.n_dev != nullptr) {
+        // The device knows the number: enough workgroups to fill it some times over, each for several
+        // pairs (a workgroup for each that there could be took 216 us where this takes 178).
+        const uint64_t each = (uint64_t)blocks * g.runs * npools, want = (8192 + each - 1) / each;
+        z = z < want ? z : want;
+    }
+    z = z < 65535 ? z : 65535;
+    const dim3 grid(blocks * g.runs + (WITH != kAlone), npools, (uint32_t)(z > 0 ? z : 1));
+    return launch(page_copy_kernel<E, TH, U, LD, ST, WITH>, grid, TH, stream, nullptr, pools, g, pairs, blocks, rider);
+}
+
 hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
                             bool aligned16, hipStream_t stream) {
-    const uint64_t run = (uint64_t)g.page_tokens * g.token_bytes;
-    const uint32_t blocks = (uint32_t)((run + kCopyBlock - 1) / kCopyBlock);
-    const dim3 grid(blocks * g.runs, npools, pairs.n < 65535 ? pairs.n : 65535);
-    return launch(aligned16 ? page_copy_kernel<16> : page_copy_kernel<1>, grid, 256, stream, nullptr, pools, g, pairs,
-                  blocks);
+    const Rider none = {};
+    if (!aligned16)
+        return launch_copy<1, 256, 4, 0, 0, kAlone>(pools, npools, g, pairs, none, stream);
+    return launch_copy<16, 512, 1, 2, 19, kAlone>(pools, npools, g, pairs, none, stream);
 }
 
 // ---- append --------------------------------------------------------------------
@@ -245,49 +295,56 @@ __global__ __launch_bounds__(1024) void fork_plan_kernel(CacheState s, const int
     }
 }
 
-// The children's rows and the references: x is the place in the row, y the entry (strided).
-__global__ __launch_bounds__(256) void fork_rows_kernel(CacheState s, const int32_t *parents, const int32_t *children,
-                                                        uint32_t n) {
-    const uint32_t j = blockIdx.x * 256 + threadIdx.x;
-    for (uint32_t i = blockIdx.y; i < n; i += gridDim.y) {
+// The children's rows and the references.
+__device__ void fork_rows(const Rider &r, uint32_t block, uint32_t blocks) {
+    const CacheState &s = r.s;
+    for (uint32_t i = block; i < r.n; i += blocks) {
         const int32_t len = s.w.aux[i];
         if (len <= 0)
             continue;
         const uint32_t full = (uint32_t)len / s.page_tokens;
-        const uint64_t to = (uint64_t)children[i] * s.max_pages;
-        if (j < full) {
-            const int32_t page = s.table[(uint64_t)parents[i] * s.max_pages + j];
+        const uint64_t to = (uint64_t)r.children[i] * s.max_pages, from = (uint64_t)r.parents[i] * s.max_pages;
+        for (uint32_t j = threadIdx.x; j < full; j += blockDim.x) {
+            const int32_t page = s.table[from + j];
             s.table[to + j] = page;
             if ((uint32_t)page < s.num_pages)
                 atomicAdd(&s.refs[page], 1);
-        } else if (j == full && (uint32_t)len % s.page_tokens != 0) {
+        }
+        if (threadIdx.x == 0 && (uint32_t)len % s.page_tokens != 0) {
             const int32_t page = s.w.to[i];
-            s.table[to + j] = page;
+            s.table[to + full] = page;
             if ((uint32_t)page < s.num_pages)
                 s.refs[page] = 1;
         }
     }
 }
 
-hipError_t launch_fork_tables(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
-                              hipStream_t stream) {
-    hipError_t e = launch(fork_plan_kernel, 1, 1024, stream, nullptr, s, parents, children, n);
-    if (e != hipSuccess)
-        return e;
-    return launch(fork_rows_kernel, dim3((s.max_pages + 255) / 256, n < 65535 ? n : 65535), 256, stream, nullptr, s,
-                  parents, children, n);
+hipError_t launch_fork_plan(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
+                            hipStream_t stream) {
+    return launch(fork_plan_kernel, 1, 1024, stream, nullptr, s, parents, children, n);
+}
+
+hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
+                            bool aligned16, const CacheState &s, const int32_t *parents, const int32_t *children,
+                            uint32_t n, bool rows, hipStream_t stream) {
+    const Rider rider = {s, parents, children, rows ? n : 0};
+    return aligned16 ? launch_copy<16, 64, 4, 0, 2, kWithFork>(pools, npools, g, pairs, rider, stream)
+                     : launch_copy<1, 256, 4, 0, 0, kWithFork>(pools, npools, g, pairs, rider, stream);
 }
 
 // ---- resize --------------------------------------------------------------------
 
-// Release: one workgroup an entry.  from[i]: pages the row had, -1 for an
-// entry that is skipped; to[i]: pages it is to have.
-__global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_t *seqs, const int32_t *lens) {
-    __shared__ int again;
-    const uint32_t i = blockIdx.x;
+// The three steps of a resize.  With many table entries each is a launch of its own, spread over
+// the chip; with few, one workgroup does all three.
+
+// Release of entry i by one workgroup.  from[i]: pages the row had, -1 for an entry
+// that is skipped; to[i]: pages it is to have.  *again: a word of LDS.
+template <int BS>
+__device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i, int *again) {
     const int32_t q = seqs[i], len = lens[i];
+    __syncthreads();
     if (threadIdx.x == 0)
-        again = 0;
+        *again = 0;
     __syncthreads();
     bool ok = q >= 0;
     if (ok && ((uint32_t)q >= s.max_seqs || len < 0 || (uint32_t)len > s.max_pages * s.page_tokens)) {
@@ -296,12 +353,12 @@ __global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_
             raise(s, TB_CACHE_RANGE);
     }
     if (ok) {
-        for (uint32_t k = threadIdx.x; k < i; k += 256)
+        for (uint32_t k = threadIdx.x; k < i; k += BS)
             if (seqs[k] == q)
-                again = 1;
+                *again = 1;
     }
     __syncthreads();
-    if (ok && again) {
+    if (ok && *again) {
         ok = false;
         if (threadIdx.x == 0)
             raise(s, TB_CACHE_TWICE);
@@ -316,44 +373,53 @@ __global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_
         s.w.from[i] = had;
         s.w.to[i] = has;
     }
-    for (int32_t j = has + (int32_t)threadIdx.x; j < had; j += 256) {
+    for (int32_t j = has + (int32_t)threadIdx.x; j < had; j += BS) {
         const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
         if (page < s.num_pages && atomicSub(&s.refs[page], 1) == 1)
             atomicOr(&s.w.bits[page >> 5], 1u << (page & 31));
     }
 }
 
-// One workgroup pushes the released pages and deals the new ones.
-__global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
-    __shared__ uint32_t lds[16];
+// Pushes the released pages of one chunk of kStackWords words of their bits, the highest page
+// first, on a stack that had `top` pages.  The chunks above are counted first; the one
+// with the lowest pages then knows all of them, and deals the new pages.
+constexpr uint32_t kStackWords = 4096;
+// Up to this much resize_few_kernel does a whole resize.
+constexpr uint32_t kFewEntries = 16, kFewPages = 8192;
+__device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
+                                        uint32_t chunk, uint32_t top, uint32_t *lds) {
     const uint32_t t = threadIdx.x, words = (s.num_pages + 31) / 32;
-    uint32_t top = (uint32_t)s.counts[0];
-    if (top > s.num_pages)
-        top = s.num_pages;
-    // words in descending order
-    for (uint32_t w0 = 0; w0 < words; w0 += 1024) {
-        const uint32_t k = w0 + t;
-        uint32_t word = 0, total;
-        if (k < words) {
-            word = s.w.bits[words - 1 - k];
-            if (word != 0)
-                s.w.bits[words - 1 - k] = 0;
-        }
-        uint32_t at = top + block_sum<1024>(__popc(word), &total, lds);
-        while (word != 0) {
-            const int b = 31 - __clz((int)word);
-            word &= ~(1u << b);
-            if (at < s.num_pages)
-                s.free_list[at++] = (int32_t)((words - 1 - k) * 32 + b);
-        }
-        top += total;
+    uint32_t total, above = 0;
+#pragma unroll 4
+    for (uint32_t k = (chunk + 1) * kStackWords + t; k < words; k += 1024)
+        above += (uint32_t)__popc(fresh(&s.w.bits[k]));
+    (void)block_sum<1024>(above, &total, lds);
+    top += total;
+    // thread t has the words 4 t' .. 4 t' + 3 of the chunk, t' counted from its end
+    uint32_t word[4], count = 0;
+    const uint32_t at0 = chunk * kStackWords + (1023 - t) * 4;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        word[k] = at0 + k < words ? fresh(&s.w.bits[at0 + k]) : 0;
+        count += (uint32_t)__popc(word[k]);
     }
-    if (top > s.num_pages)
-        top = s.num_pages;
+    uint32_t at = top + block_sum<1024>(count, &total, lds);
+#pragma unroll
+    for (int k = 3; k >= 0; k--)
+        while (word[k] != 0) {
+            const int b = 31 - __clz((int)word[k]);
+            word[k] &= ~(1u << b);
+            if (at < s.num_pages)
+                s.free_list[at] = (int32_t)((at0 + k) * 32 + b);
+            at++;
+        }
+    if (chunk != 0)
+        return;
+    top = min(top + total, s.num_pages);
     uint32_t need_all = 0;
     for (uint32_t i0 = 0; i0 < n; i0 += 1024) {
         const uint32_t i = i0 + t;
-        uint32_t need = 0, total;
+        uint32_t need = 0;
         if (i < n && s.w.from[i] >= 0 && s.w.to[i] > s.w.from[i])
             need = (uint32_t)(s.w.to[i] - s.w.from[i]);
         const uint32_t before = block_sum<1024>(need, &total, lds);
@@ -365,7 +431,7 @@ __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32
     for (uint32_t i = t; i < n; i += 1024) {
         if (s.w.from[i] < 0)
             continue;
-        if (!enough && pages_of(lens[i], s.page_tokens) > s.w.from[i]) {
+        if (!enough && s.w.to[i] > s.w.from[i]) {
             s.w.from[i] = -1;
             continue;
         }
@@ -378,13 +444,13 @@ __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32
     }
 }
 
-__global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *seqs) {
-    const uint32_t i = blockIdx.x;
+template <int BS>
+__device__ __forceinline__ void grow(const CacheState &s, const int32_t *seqs, uint32_t i) {
     const int32_t had = s.w.from[i];
     if (had < 0)
         return;
     const int32_t has = s.w.to[i], first = s.w.aux[i];
-    for (int32_t j = had + (int32_t)threadIdx.x; j < has; j += 256) {
+    for (int32_t j = had + (int32_t)threadIdx.x; j < has; j += BS) {
         const int32_t page = s.free_list[first - (j - had)];
         s.table[(uint64_t)seqs[i] * s.max_pages + j] = page;
         if ((uint32_t)page < s.num_pages)
@@ -392,15 +458,65 @@ __global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *
     }
 }
 
+__device__ __forceinline__ uint32_t stack_top(const CacheState &s) {
+    const int32_t top = s.counts[0];
+    return top < 0 ? 0 : min((uint32_t)top, s.num_pages);
+}
+
+__global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_t *seqs, const int32_t *lens) {
+    __shared__ int again;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *s.w.top = stack_top(s);   // restack's last chunk writes the new one while others still start
+    release<256>(s, seqs, lens, blockIdx.x, &again);
+}
+
+__global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
+    __shared__ uint32_t lds[16];
+    restack(s, seqs, lens, n, blockIdx.x, *s.w.top, lds);
+}
+
+// Also clears the bits, which every chunk of restack has read by now.
+__global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *seqs, uint32_t n) {
+    if (blockIdx.x < n) {
+        grow<256>(s, seqs, blockIdx.x);
+        return;
+    }
+    const uint32_t words = (s.num_pages + 31) / 32;
+    for (uint32_t k = (blockIdx.x - n) * 256 + threadIdx.x; k < words; k += (gridDim.x - n) * 256)
+        if (s.w.bits[k] != 0)
+            s.w.bits[k] = 0;
+}
+
+__global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
+    __shared__ uint32_t lds[16];
+    __shared__ int again;
+    const uint32_t top = stack_top(s);
+    for (uint32_t i = 0; i < n; i++)
+        release<1024>(s, seqs, lens, i, &again);
+    __syncthreads();
+    restack(s, seqs, lens, n, 0, top, lds);
+    __syncthreads();
+    for (uint32_t i = 0; i < n; i++)
+        grow<1024>(s, seqs, i);
+    for (uint32_t k = threadIdx.x; k < (s.num_pages + 31) / 32; k += 1024)
+        if (s.w.bits[k] != 0)
+            s.w.bits[k] = 0;
+}
+
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream) {
+    const uint32_t words = (s.num_pages + 31) / 32, chunks = (words + kStackWords - 1) / kStackWords;
+    // One workgroup goes over the entries in turn, some half a microsecond each; the three launches cost
+    // some eight, whatever they do.
+    if (chunks == 1 && n <= kFewEntries && s.max_pages <= kFewPages)
+        return launch(resize_few_kernel, 1, 1024, stream, nullptr, s, seqs, lens, n);
     LaunchSeq seq;
     hipError_t e = launch(release_kernel, n, 256, stream, nullptr, s, seqs, lens);
     if (e == hipSuccess)
-        e = launch(restack_kernel, 1, 1024, stream, nullptr, s, seqs, lens, n);
+        e = launch(restack_kernel, chunks, 1024, stream, nullptr, s, seqs, lens, n);
     seq.last();
     if (e == hipSuccess)
-        e = launch(grow_kernel, n, 256, stream, nullptr, s, seqs);
+        e = launch(grow_kernel, n + (words + 1023) / 1024, 256, stream, nullptr, s, seqs, n);
     return e;
 }
 
@@ -411,74 +527,95 @@ __device__ __forceinline__ uint32_t border_of(const CacheState &s) {
     return top < 0 ? s.num_pages : ((uint32_t)top > s.num_pages ? 0 : s.num_pages - (uint32_t)top);
 }
 
-// Free pages below the border L and used ones at or above it, by chunk of pages.
-__global__ __launch_bounds__(256) void compact_count_kernel(CacheState s) {
-    __shared__ uint32_t lds[4];
-    const uint32_t live = border_of(s);
-    uint32_t holes = 0, movers = 0, total;
-    for (uint32_t k = threadIdx.x; k < kScanChunk; k += 256) {
-        const uint32_t p = blockIdx.x * kScanChunk + k;
-        if (p < s.num_pages) {
-            const bool used = s.refs[p] > 0;
-            holes += p < live && !used;
-            movers += p >= live && used;
-        }
+// This thread's four pages of a chunk, as bits: whether page 4 t + k is a hole (free, below the
+// border) and whether it moves (used, at or above it).
+__device__ __forceinline__ void look_at(const CacheState &s, uint32_t chunk, uint32_t live, uint32_t *holes, uint32_t *movers) {
+    typedef int32_t i32x4a __attribute__((ext_vector_type(4), aligned(4)));
+    const uint32_t p = chunk * kScanChunk + threadIdx.x * 4;
+    int32_t r[4] = {0, 0, 0, 0};
+    if (p + 4 <= s.num_pages) {
+        const i32x4a x = *reinterpret_cast<const i32x4a *>(s.refs + p);
+        r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+    } else {
+        for (uint32_t k = 0; k < 4 && p + k < s.num_pages; k++)
+            r[k] = s.refs[p + k];
     }
-    (void)block_sum<256>(holes, &total, lds);
-    if (threadIdx.x == 0)
-        s.w.chunk[2 * blockIdx.x] = total;
-    (void)block_sum<256>(movers, &total, lds);
-    if (threadIdx.x == 0)
-        s.w.chunk[2 * blockIdx.x + 1] = total;
+    *holes = *movers = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; k++) {
+        *holes |= (uint32_t)(r[k] <= 0 && p + k < live) << k;
+        *movers |= (uint32_t)(r[k] > 0 && p + k >= live) << k;
+    }
 }
 
-// to[r]: the r-th hole; from[r]: the r-th mover; rank[p]: r of mover p.
-__global__ __launch_bounds__(256) void compact_rank_kernel(CacheState s, uint32_t chunks) {
-    __shared__ uint32_t lds[4];
-    const uint32_t live = border_of(s);
-    uint32_t holes = 0, movers = 0, total;
-    for (uint32_t k = threadIdx.x; k < blockIdx.x; k += 256) {
-        holes += s.w.chunk[2 * k];
-        movers += s.w.chunk[2 * k + 1];
+__global__ __launch_bounds__(1024) void compact_count_kernel(CacheState s) {
+    __shared__ uint32_t lds[16];
+    uint32_t holes, movers, total;
+    look_at(s, blockIdx.x, border_of(s), &holes, &movers);
+    // both counts are at most kScanChunk, 4096: one sum
+    (void)block_sum<1024>(__popc(holes) | __popc(movers) << 16, &total, lds);
+    if (threadIdx.x == 0) {
+        s.w.chunk[2 * blockIdx.x] = total & 0xffff;
+        s.w.chunk[2 * blockIdx.x + 1] = total >> 16;
     }
-    (void)block_sum<256>(holes, &total, lds);
-    holes = total;
-    (void)block_sum<256>(movers, &total, lds);
-    movers = total;
-    for (uint32_t k0 = 0; k0 < kScanChunk; k0 += 256) {
-        const uint32_t p = blockIdx.x * kScanChunk + k0 + threadIdx.x;
-        const bool in = p < s.num_pages, used = in && s.refs[p] > 0;
-        const bool hole = in && p < live && !used, mover = in && p >= live && used;
-        uint32_t r = holes + block_sum<256>(hole, &total, lds);
-        holes += total;
-        if (hole)
-            s.w.to[r] = (int32_t)p;
-        r = movers + block_sum<256>(mover, &total, lds);
-        movers += total;
-        if (mover) {
-            s.w.from[r] = (int32_t)p;
-            s.w.rank[p] = (int32_t)r;
+}
+
+// to[r]: the r-th hole; from[r]: the r-th mover; rank[p]: r of mover p.  One workgroup a
+// chunk, after compact_count_kernel; or one for all of a few chunks, by itself.
+__global__ __launch_bounds__(1024) void compact_rank_kernel(CacheState s, uint32_t chunks) {
+    __shared__ uint32_t lds[16];
+    const uint32_t live = border_of(s), mine = gridDim.x == 1 ? chunks : 1;
+    uint32_t holes = 0, movers = 0, total;
+    if (gridDim.x > 1) {
+        for (uint32_t k = threadIdx.x; k < blockIdx.x; k += 1024) {
+            holes += s.w.chunk[2 * k];
+            movers += s.w.chunk[2 * k + 1];
         }
+        (void)block_sum<1024>(holes, &total, lds);
+        holes = total;
+        (void)block_sum<1024>(movers, &total, lds);
+        movers = total;
+    }
+    for (uint32_t c = blockIdx.x; c < blockIdx.x + mine; c++) {
+        uint32_t h, m;
+        look_at(s, c, live, &h, &m);
+        const uint32_t before = block_sum<1024>(__popc(h) | __popc(m) << 16, &total, lds);
+        uint32_t at = holes + (before & 0xffff), page = c * kScanChunk + threadIdx.x * 4;
+        for (uint32_t k = 0; k < 4; k++)
+            if (h >> k & 1)
+                s.w.to[at++] = (int32_t)(page + k);
+        at = movers + (before >> 16);
+        for (uint32_t k = 0; k < 4; k++)
+            if (m >> k & 1) {
+                s.w.rank[page + k] = (int32_t)at;
+                s.w.from[at++] = (int32_t)(page + k);
+            }
+        holes += total & 0xffff;
+        movers += total >> 16;
     }
     // pairs that exist on both sides (all of them, in a cache that is in order)
-    if (blockIdx.x == chunks - 1 && threadIdx.x == 0)
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
         *s.w.pairs = holes < movers ? holes : movers;
 }
 
-__global__ __launch_bounds__(256) void compact_apply_kernel(CacheState s) {
+// Tables, references and the stack after the moves.
+__device__ void compact_apply(const Rider &rider, uint32_t block, uint32_t blocks) {
+    const CacheState &s = rider.s;
+    if (rider.n == 0)
+        return;
     const uint32_t live = border_of(s), pairs = *s.w.pairs;
-    const uint32_t n = gridDim.x * 256, at = blockIdx.x * 256 + threadIdx.x;
-    const uint64_t entries = (uint64_t)s.max_seqs * s.max_pages;
-    for (uint64_t k = at; k < entries; k += n) {
-        const uint32_t q = (uint32_t)(k / s.max_pages), j = (uint32_t)(k % s.max_pages);
-        if ((int32_t)j >= pages_of(length_of(s, (int32_t)q), s.page_tokens))
-            continue;
-        const uint32_t page = (uint32_t)s.table[k];
-        if (page < live || page >= s.num_pages)
-            continue;
-        const uint32_t r = (uint32_t)s.w.rank[page];
-        if (r < pairs && s.w.from[r] == (int32_t)page)
-            s.table[k] = s.w.to[r];
+    const uint32_t n = blocks * blockDim.x, at = block * blockDim.x + threadIdx.x;
+    for (uint32_t q = block; q < s.max_seqs; q += blocks) {
+        const uint32_t pages = (uint32_t)pages_of(length_of(s, (int32_t)q), s.page_tokens);
+        int32_t *row = s.table + (uint64_t)q * s.max_pages;
+        for (uint32_t j = threadIdx.x; j < pages; j += blockDim.x) {
+            const uint32_t page = (uint32_t)row[j];
+            if (page < live || page >= s.num_pages)
+                continue;
+            const uint32_t r = (uint32_t)s.w.rank[page];
+            if (r < pairs && s.w.from[r] == (int32_t)page)
+                row[j] = s.w.to[r];
+        }
     }
     for (uint32_t r = at; r < pairs; r += n) {
         s.refs[s.w.to[r]] = s.refs[s.w.from[r]];
@@ -490,14 +627,19 @@ __global__ __launch_bounds__(256) void compact_apply_kernel(CacheState s) {
 
 hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream) {
     const uint32_t chunks = (s.num_pages + kScanChunk - 1) / kScanChunk;
-    hipError_t e = launch(compact_count_kernel, chunks, 256, stream, nullptr, s);
+    if (chunks <= 4)   // a chunk takes a workgroup some 1.5 us, a launch more than 3
+        return launch(compact_rank_kernel, 1, 1024, stream, nullptr, s, chunks);
+    hipError_t e = launch(compact_count_kernel, chunks, 1024, stream, nullptr, s);
     if (e == hipSuccess)
-        e = launch(compact_rank_kernel, chunks, 256, stream, nullptr, s, chunks);
+        e = launch(compact_rank_kernel, chunks, 1024, stream, nullptr, s, chunks);
     return e;
 }
 
-hipError_t launch_compact_apply(const CacheState &s, hipStream_t stream) {
-    return launch(compact_apply_kernel, 1024, 256, stream, nullptr, s);
+hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
+                               bool aligned16, const CacheState &s, bool apply, hipStream_t stream) {
+    const Rider rider = {s, nullptr, nullptr, apply ? 1u : 0u};
+    return aligned16 ? launch_copy<16, 512, 1, 2, 19, kWithCompact>(pools, npools, g, pairs, rider, stream)
+                     : launch_copy<1, 256, 4, 0, 0, kWithCompact>(pools, npools, g, pairs, rider, stream);
 }
 
 }  // namespace tbk

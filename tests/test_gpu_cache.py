@@ -184,6 +184,26 @@ def test_more_pools_than_one_launch_takes():
     m.check(c, "130 pools")
 
 
+def test_no_pools_and_two_pages():
+    """The bookkeeping alone, through the C call; the smallest caches."""
+    note("paged cache, no pools")
+    import copy_reduce_amd as tb
+    c, m = make(pages=2, pt=2, seqs=3, width=2)
+    c._c.npools = 0
+    a, b = ints([0]), ints([3])
+    s = torch.cuda.current_stream().cuda_stream
+    for name, args in (("resize", ([0], [2])), ("fork", ([0], [2])), ("resize", ([0], [0])), ("compact", ()), ("resize", ([2], [0]))):
+        getattr(c, name)(*[ints(x) for x in args])
+        getattr(m, name)(*args)
+        m.check(c, name)
+    assert tb.lib.tb_page_append(c._c, a.data_ptr(), 1, 32, 32, a.data_ptr(), b.data_ptr(), None, 1, s) == tb.TB_OK
+    c, m = make(pages=1, pt=2, seqs=1, width=1)
+    for name, args in (("resize", ([0], [2])), ("compact", ()), ("resize", ([0], [1])), ("resize", ([0], [0])), ("compact", ())):
+        getattr(c, name)(*[ints(x) for x in args])
+        getattr(m, name)(*args)
+        m.check(c, name)
+
+
 def test_far_pages():
     """Byte offsets past 2^32 within one pool."""
     note("paged cache, a pool of 6 GiB")
