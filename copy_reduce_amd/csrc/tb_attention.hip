@@ -62,7 +62,7 @@ struct AttnArgs {
     uint32_t num_pages, page_tokens, max_seqs, max_pages;
     uint32_t div_mul, div_shift;       // token / page_tokens = token * div_mul >> div_shift
     uint32_t row_blocks;               // workgroups that share a head's rows
-    uint32_t budget;                   // shares that a head's stream of keys is cut into
+    uint32_t budget;                   // shares that a head's stream of keys is cut into; 0: one for each sequence
     float scale, scale2;               // |scale| log2 e; 1 for scale 0, see load_q
     int32_t sign;                      // of scale
     int32_t *split_base, *split_count; // [batch] workspace
@@ -175,18 +175,31 @@ __device__ __forceinline__ uint32_t weight_of(const Sequence &s) {
     return ((s.context + s.nodes + kUnit - 1) / kUnit + 1) * kUnit;
 }
 
+constexpr uint64_t kWhole = 1ull << 40;   // a share longer than any sequence
 struct Place {
     uint64_t start;   // of sequence `batch` in the stream
     uint64_t share;
     uint32_t batch;   // the sequence in which the share begins; g.batch: no share
 };
 
+// `known`: LDS for a sequence a thread; filled where the batch has no more than that.
 template <int WAVES>
-__device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds) {
+__device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds, Sequence *known) {
+    if (g.budget == 0) {   // one sequence, from its first key to its last
+        if (threadIdx.x == 0)
+            *out = {0, kWhole, mine};
+        __syncthreads();
+        return;
+    }
     const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
     uint64_t total = 0, w = 0;
     for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {
-        w = b0 + t < g.batch ? weight_of(sequence_of(g, b0 + t)) : 0;
+        w = 0;
+        if (b0 + t < g.batch) {
+            const Sequence q = sequence_of(g, b0 + t);
+            known[t] = q;
+            w = weight_of(q);
+        }
         total += w;
     }
 #pragma unroll
@@ -241,12 +254,21 @@ struct Part {
     uint64_t end;       // of the sequence in the stream
     bool first, last;
 
-    __device__ __forceinline__ Part(const AttnArgs &g, const Place &at, uint32_t mine) : b(at.batch) {
-        const Sequence s = sequence_of(g, b);
+    // known: what find_place() left, for up to `room` sequences
+    __device__ __forceinline__ Part(const AttnArgs &g, const Place &at, uint32_t mine, const Sequence *known, uint32_t room) : b(at.batch) {
+        const Sequence s = g.batch <= room && at.share != kWhole ? known[b] : sequence_of(g, b);
         seq.row = uniform(s.row);
         seq.context = uniform(s.context);
         seq.nodes = uniform(s.nodes);
         end = at.start + weight_of(seq);
+        if (at.share == kWhole) {
+            c0 = slot = 0;
+            c1 = seq.context;
+            splits = 1;
+            first = last = true;
+            end = ~0ull;   // no other sequence follows
+            return;
+        }
         const uint64_t begin = mine * at.share;
         const uint64_t lo = begin > at.start ? begin - at.start : 0;
         const uint64_t hi = min(begin + at.share, end) - at.start;
@@ -564,7 +586,7 @@ struct Rows {
 
 // The combine kernel's way into the slots.
 __device__ __forceinline__ void note_splits(const AttnArgs &g, const Part &w, uint32_t head, uint32_t block) {
-    if (block == 0 && head == 0 && w.first && threadIdx.x == 0) {
+    if (g.budget != 0 && block == 0 && head == 0 && w.first && threadIdx.x == 0) {
         g.split_base[w.b] = (int32_t)w.slot;
         g.split_count[w.b] = (int32_t)w.splits;
     }
@@ -585,17 +607,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void
     typedef typename R::V8 V8;
     constexpr int KS = R::KS, DJ = R::DJ;
     __shared__ Place place;
+    __shared__ Sequence known[64 * kWaves];
     __shared__ uint64_t sums[kWaves];
     __shared__ uint32_t list[kListPages];
     __shared__ float merge[kWaves / 2 * R::kMergeFloats];
 
     const uint32_t wk = uniform(threadIdx.x >> 6), mine = blockIdx.x / g.heads, head = blockIdx.x % g.heads;
-    find_place<kWaves>(g, mine, &place, sums);
+    find_place<kWaves>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
-    for (; at.batch < g.batch && at.start < (mine + 1) * at.share; at.batch++) {
+    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end; at.batch++) {
     const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-    const Part w(g, at, mine);
+    const Part w(g, at, mine, known, 64 * kWaves);
     at.start = w.end;
     note_splits(g, w, head, 0);
     const Keys<kWaves> keys(g, w, head, list);
@@ -760,6 +783,7 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
     // two buffers, keys before values
     __shared__ __attribute__((aligned(16))) uint8_t data[4 * kBuffer > kMerge ? 4 * kBuffer : kMerge];
     __shared__ Place place;
+    __shared__ Sequence known[kThreads];
     __shared__ uint64_t sums[kSharedWaves];
     __shared__ uint32_t list[kListPages];
     __shared__ uint32_t wild_step;           // the last step of nodes with values that are not finite, plus 1
@@ -773,14 +797,14 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
         unit = at / g.row_blocks * 8 + (blockIdx.x & 7);
     }
     const uint32_t mine = unit / g.heads, head = unit % g.heads;
-    if (mine >= g.budget)
+    if (mine >= (g.budget != 0 ? g.budget : g.batch))
         return;
-    find_place<kSharedWaves>(g, mine, &place, sums);
+    find_place<kSharedWaves>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
-    for (; at.batch < g.batch && at.start < (mine + 1) * at.share; at.batch++) {
+    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end; at.batch++) {
     const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-    const Part w(g, at, mine);
+    const Part w(g, at, mine, known, kThreads);
     at.start = w.end;
     note_splits(g, w, head, block);
     const Keys<kSharedWaves> keys(g, w, head, list);
@@ -832,6 +856,27 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
             __builtin_amdgcn_global_load_lds((const gvoid *)(from + pools_apart), (svoid *)(there + kBuffer), 16, 0, kStream);
         }
     };
+    // A step of the drafted nodes, likewise.
+    const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
+    const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+    const auto fetch_nodes = [&](uint8_t *to, uint32_t first) {
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const uint32_t at = i * kThreads + thread, key = at / kPieces, piece = piece_at_place<D>(key, at % kPieces);
+            const uint32_t u = min(first + key, count - 1);
+            uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
+            __builtin_amdgcn_global_load_lds((const gvoid *)(kb + u * g.k_stride[1] + piece * 16), (svoid *)there, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const gvoid *)(vb + u * g.v_stride[1] + piece * 16), (svoid *)(there + kBuffer), 16, 0, 0);
+        }
+    };
+    // What follows the context's step before `next`: its next step, or the first of the nodes.
+    const auto fetch_after = [&](uint8_t *to, uint32_t next) {
+        if (next < c1)
+            fetch(to, next);
+        else if (w.last && count > 0)
+            fetch_nodes(to, 0);
+    };
+    const auto buffer_at = [&](uint32_t buffer) { return data + buffer * 2 * kBuffer; };
     // Waits for the step's loads; values of keys past the end meet weights of 0 and have to be finite: 0.
     const auto arrived = [&](uint8_t *to, uint32_t left) {
         __builtin_amdgcn_s_waitcnt(0);
@@ -907,12 +952,12 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
     // to be raised alike: with a branch or a break inside, the compiler moves all accumulators in
     // every turn.  (After the last tile the scores of it are had once more, for nothing.)
     constexpr uint32_t kTurns = kStep / kTile / WK, kTileBytes = kTile * D * 2;
+    uint32_t buffer = 0;
+    fetch_after(data, c0);
     if (c0 < c1) {
-        fetch(data, c0);
         arrived(data, c1 - c0);
-        if (c0 + kStep < c1)
-            fetch(data + 2 * kBuffer, c0 + kStep);
-        uint32_t first = c0, turn = 0, buffer = 0;
+        fetch_after(buffer_at(1), c0 + kStep);
+        uint32_t first = c0, turn = 0;
         const auto look = [&] {
             tile_at = uniform(data_at + buffer * 2 * kBuffer + (turn * WK + wk) * kTileBytes);
             const uint32_t t0 = first + (turn * WK + wk) * kTile;
@@ -932,9 +977,8 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
                         turn = 0;
                         buffer ^= 1;
                         first += kStep;
-                        arrived(data + buffer * 2 * kBuffer, c1 - first);
-                        if (first + kStep < c1)
-                            fetch(data + (buffer ^ 1) * 2 * kBuffer, first + kStep);
+                        arrived(buffer_at(buffer), c1 - first);
+                        fetch_after(buffer_at(buffer ^ 1), first + kStep);
                     } else {
                         turn = kTurns - 1;
                     }
@@ -942,28 +986,29 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
                 raise = look();
             } while (more && !raise);
         } while (more);
-        __syncthreads();
+        buffer ^= 1;
     }
 
-    // the drafted nodes, with the sequence's last chunk
-    const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
-    const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+    // the drafted nodes, with the sequence's last part
 #pragma unroll 1
-    for (uint32_t first = 0; w.last && first < count; first += kStep) {
+    for (uint32_t first = 0; w.last && first < count; first += kStep, buffer ^= 1) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (first + kStep < count)
+            fetch_nodes(buffer_at(buffer ^ 1), first + kStep);
+        // A value that is not finite would turn a weight of 0 into NaN: here it counts as 0, and
+        // the rows that do see it get it added afterwards.  Nodes past the last count as 0 altogether.
         uint32_t wild = 0;
 #pragma unroll 1
         for (uint32_t at = thread; at < kStep * kPieces; at += kThreads) {
-            const uint32_t key = at / kPieces, piece = at % kPieces;
-            const uint32_t u = min(first + key, count - 1), to = (key * kPieces + place_of_piece<D>(key, piece)) * 16;
-            *reinterpret_cast<u32x4 *>(data + to) = *(const gu32x4 *)(kb + u * g.k_stride[1] + piece * 16);
-            // A value that is not finite would turn a weight of 0 into NaN: here it counts
-            // as 0, and the rows that do see it get it added afterwards.
+            u32x4 *const place = reinterpret_cast<u32x4 *>(buffer_at(buffer) + kBuffer + at * 16);
             u32x4 x = {0, 0, 0, 0};
-            if (first + key < count)
-                x = *(const gu32x4 *)(vb + u * g.v_stride[1] + piece * 16);
-            for (int e = 0; e < 4; e++)
-                x[e] = tamed<T>(x[e], &wild);
-            *reinterpret_cast<u32x4 *>(data + kBuffer + to) = x;
+            if (first + at / kPieces < count) {
+                x = *place;
+                for (int e = 0; e < 4; e++)
+                    x[e] = tamed<T>(x[e], &wild);
+            }
+            *place = x;
         }
         if (wild)
             wild_step = first + 1;
@@ -974,7 +1019,7 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
             const uint32_t tile = turn * WK + wk, t0 = first + tile * kTile;
             if (t0 >= count)
                 break;
-            tile_at = uniform(data_at + tile * kTileBytes);
+            tile_at = uniform(data_at + buffer * 2 * kBuffer + tile * kTileBytes);
             uint32_t bits[NT];
 #pragma unroll
             for (int t = 0; t < NT; t++)
@@ -985,8 +1030,8 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
             if (any_wild)
                 rows.add_wild(g, vb, t0, min(t0 + kTile, count), bits, [&](int j, int r) { return 16 * j + 4 * q4 + r; });
         }
-        __syncthreads();
     }
+    __syncthreads();
 
     rows.template join<WM, WK>(g, reinterpret_cast<float *>(data), wave, lane);
     if (wk == 0)
@@ -1093,12 +1138,19 @@ static uint32_t resident(const Shape &s, uint32_t head_dim) {
     return head_dim == 64 ? 3 : (head_dim <= 128 ? 2 : 1);
 }
 
+// Up to this many tokens a sequence (by the table's room, the lengths are not known here) a workgroup
+// takes a whole sequence; up to the second, where many rows' workgroups fill the chip that way.
+// Measured with lengths spread evenly up to the bound, whole against shares: 4 sequences of 2 heads,
+// one node of 4 rows, 500 tokens 16.7 us against 19.5, 1,000 tokens 19.6 against 18.0; 32 sequences of
+// 8 heads, 64 rows, 2,000 tokens 53 us against 70, 4,000 tokens 89 against 92, 8,000 tokens 156 against 142.
+constexpr uint64_t kShort = 768, kShortMany = 4096;
+
 struct Plan {
     Shape shape;
     uint32_t rows, row_blocks, budget;
     uint64_t slots;
 };
-static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count) {
+static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count, uint64_t longest = ~0ull) {
     Plan p;
     p.rows = a.nodes * (a.heads_q / heads);
     p.shape = shape_of(p.rows, a.head_dim);
@@ -1118,6 +1170,10 @@ static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count) {
     }
     p.budget = (uint32_t)best;
     p.slots = (uint64_t)p.budget + a.batch;
+    // Where the table has room for short contexts only, a workgroup takes a whole sequence, and
+    // there is nothing to find and nothing to join.
+    if (longest <= kShort || (p.shape.shared && longest <= kShortMany && a.batch * each >= room))
+        p.budget = 0;
     return p;
 }
 
@@ -1133,6 +1189,8 @@ template <typename T, int D>
 static hipError_t launch_dim(const AttnArgs &g, Shape s, uint32_t grid, hipStream_t stream) {
     LaunchSeq seq;
     hipError_t e;
+    if (g.budget == 0)
+        seq.last();
     if (!s.shared) {
         e = launch(tree_attention_kernel<T, D>, grid, 64 * kWaves, stream, nullptr, g);
     } else if (s.wm == 8) {
@@ -1145,7 +1203,7 @@ static hipError_t launch_dim(const AttnArgs &g, Shape s, uint32_t grid, hipStrea
         else
             e = hipErrorInvalidValue;
     }
-    if (e != hipSuccess)
+    if (e != hipSuccess || g.budget == 0)
         return e;
     seq.last();
     const uint64_t rows = (uint64_t)g.batch * g.heads * g.rows;
@@ -1164,7 +1222,7 @@ static hipError_t launch_type(const AttnArgs &g, uint32_t dim, Shape s, uint32_t
 }
 
 hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream) {
-    const Plan p = plan_of(a, c.heads, cu_count);
+    const Plan p = plan_of(a, c.heads, cu_count, (uint64_t)c.max_pages * c.page_tokens);
     AttnArgs g;
     g.q = static_cast<const uint8_t *>(a.q);
     g.k = static_cast<const uint8_t *>(a.k);
@@ -1217,7 +1275,7 @@ hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int c
     g.split_count = g.split_base + a.batch;
     g.part_ml = reinterpret_cast<float *>(ws + round16(8ull * a.batch));
     g.part_o = reinterpret_cast<float *>(ws + round16(8ull * a.batch) + round16(8 * rows));
-    const uint64_t units = (uint64_t)p.budget * c.heads;
+    const uint64_t units = (uint64_t)(p.budget != 0 ? p.budget : a.batch) * c.heads;
     const uint64_t grid = p.row_blocks > 1 ? (units + 7) / 8 * 8 * p.row_blocks : units;
     if (grid > (1u << 30))
         return hipErrorInvalidValue;

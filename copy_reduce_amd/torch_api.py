@@ -148,12 +148,14 @@ class DescRing:
 
 
 _NO_CONTEXT = nullcontext()
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _list_arg(t: torch.Tensor, n: Optional[int], device: torch.device, what: str) -> int:
     """Address of an int32 index list on the cache's device."""
     if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 1
-            or not t.is_contiguous() or (n is not None and t.shape[0] != n)):
+            or not t.is_contiguous() or (n is not None and len(t) != n)):
         raise ValueError(f"{what} must be a contiguous one-dimensional int32 tensor on {device}"
                          + ("" if n is None else f" of {n} entries"))
     return t.data_ptr()
@@ -235,14 +237,14 @@ class PagedCache:
 
     def _there(self):
         """The cache's device as the current one, for the length of a call."""
-        return (_NO_CONTEXT if torch.cuda.current_device() == self.device.index
-                else torch.cuda.device(self.device))
+        return _NO_CONTEXT if _current_device() == self.device.index else torch.cuda.device(self.device)
 
     def _stream(self, stream: Optional[torch.cuda.Stream]) -> int:
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if s.device != self.device:
+        if stream is None:
+            return _current_raw_stream(self.device.index)
+        if stream.device != self.device:
             raise ValueError(f"the stream must be one of {self.device}")
-        return int(s.cuda_stream)
+        return int(stream.cuda_stream)
 
     def flags(self, clear: bool = False) -> int:
         """The TB_CACHE_* bits raised so far (waits for the device)."""
@@ -258,42 +260,43 @@ class PagedCache:
         if src.device != self.device or src.dtype != self.dtype:
             raise ValueError("both caches must be of one device and type")
         d = _list_arg(dst_pages, None, self.device, "dst_pages")
-        s = _list_arg(src_pages, dst_pages.shape[0], self.device, "src_pages")
+        s = _list_arg(src_pages, len(dst_pages), self.device, "src_pages")
         with self._there():
-            _tb_cache.tb_page_copy(self._c, src._c, d, s, dst_pages.shape[0], self._stream(stream))
+            _tb_cache.tb_page_copy(self._c, src._c, d, s, len(dst_pages), self._stream(stream))
 
     def append(self, rows: torch.Tensor, seqs: torch.Tensor, positions: torch.Tensor,
                index: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Write rows[:, index[i]] ([npools, n, heads, head_dim]) to position positions[i] of sequence seqs[i]."""
-        if (rows.dtype != self.dtype or rows.device != self.device or rows.dim() != 4
-                or rows.shape[0] != len(self.pools) or rows.shape[2:] != (self.heads, self.head_dim)
-                or rows.stride(3) != 1 or (self.heads > 1 and rows.stride(2) != self.head_dim)):
+        shape, stride = rows.shape, rows.stride()
+        if (rows.dtype != self.dtype or rows.device != self.device or len(shape) != 4 or shape[0] != len(self.pools)
+                or shape[2] != self.heads or shape[3] != self.head_dim or stride[3] != 1
+                or (self.heads > 1 and stride[2] != self.head_dim)):
             raise ValueError("rows must be [npools, n, heads, head_dim] of the cache's type and device, "
                              "each token contiguous")
-        n = seqs.shape[0]
+        n = len(seqs)
         q, p = _list_arg(seqs, None, self.device, "seqs"), _list_arg(positions, n, self.device, "positions")
         x = 0 if index is None else _list_arg(index, n, self.device, "index")
-        if index is None and rows.shape[1] < n:
+        if index is None and shape[1] < n:
             raise ValueError("rows must hold a row for each entry")
         size = rows.element_size()
-        step = rows.stride(1) if rows.shape[1] > 1 else self.heads * self.head_dim
+        step = stride[1] if shape[1] > 1 else self.heads * self.head_dim
         with self._there():
-            _tb_cache.tb_page_append(self._c, rows.data_ptr(), rows.shape[1], step * size, rows.stride(0) * size, q, p,
-                                     x, n, self._stream(stream))
+            _tb_cache.tb_page_append(self._c, rows.data_ptr(), shape[1], step * size, stride[0] * size, q, p, x, n,
+                                     self._stream(stream))
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Make the empty sequences `children` copies of `parents`, sharing their full pages."""
         p = _list_arg(parents, None, self.device, "parents")
-        c = _list_arg(children, parents.shape[0], self.device, "children")
+        c = _list_arg(children, len(parents), self.device, "children")
         with self._there():
-            _tb_cache.tb_page_fork(self._c, p, c, parents.shape[0], self._stream(stream))
+            _tb_cache.tb_page_fork(self._c, p, c, len(parents), self._stream(stream))
 
     def resize(self, seqs: torch.Tensor, lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Give the sequences `seqs` the lengths `lens`, 0 freeing one: releases pages, then takes new ones."""
         q = _list_arg(seqs, None, self.device, "seqs")
-        n = _list_arg(lens, seqs.shape[0], self.device, "lens")
+        n = _list_arg(lens, len(seqs), self.device, "lens")
         with self._there():
-            _tb_cache.tb_page_resize(self._c, q, n, seqs.shape[0], self._stream(stream))
+            _tb_cache.tb_page_resize(self._c, q, n, len(seqs), self._stream(stream))
 
     def free(self, seqs: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Free whole sequences."""
@@ -334,43 +337,48 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     sqrt(head_dim) by default.  Returns (out, lse): out as q, lse float32 [batch, nodes, heads_q], the natural
     logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf."""
     dtype, dev = q.dtype, cache.device
-    if dtype not in _ATTN_TYPES or cache.dtype != dtype:
+    kind = _ATTN_TYPES.get(dtype)
+    if kind is None or cache.dtype != dtype:
         raise ValueError("q and the cache must be both bfloat16 or both float16")
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [batch, nodes, heads_q, head_dim]")
-    b, t, hq, d = q.shape
+    b, t, hq, d = shape
     if d != cache.head_dim:
         raise ValueError("q's head_dim must be the cache's")
     if not 0 <= layer < len(cache.pools) // 2:
         raise ValueError("the cache has no such layer")
     kv_shape = (b, t, cache.heads, d)
-    for x, shape, name in ((q, q.shape, "q"), (k, kv_shape, "k"), (v, kv_shape, "v")):
-        if x.dtype != dtype or x.device != dev or x.shape != shape or x.stride(3) != 1:
-            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {dev}, head_dim contiguous")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if q.device != dev or qs[3] != 1:
+        raise ValueError(f"q must be on {dev}, head_dim contiguous")
+    for x, st in ((k, ks), (v, vs)):
+        if x.dtype != dtype or x.device != dev or x.shape != kv_shape or st[3] != 1:
+            raise ValueError(f"k and v must be {dtype} of shape {kv_shape} on {dev}, head_dim contiguous")
     sq = _list_arg(seqs, b, dev, "seqs")
     if mask is not None and (mask.dtype != torch.int64 or mask.device != dev or mask.shape != (b, t, (t + 63) // 64)
                              or not mask.is_contiguous()):
         raise ValueError(f"mask must be a contiguous int64 tensor of shape {(b, t, (t + 63) // 64)} on {dev}")
-    tn = None if nodes is None else _list_arg(nodes, b, dev, "nodes")
-    with cache._there():
+    tn = 0 if nodes is None else _list_arg(nodes, b, dev, "nodes")
+    if out is not None and (out.dtype != dtype or out.device != dev or out.shape != shape or out.stride(3) != 1):
+        raise ValueError("out must have q's type, shape and device, head_dim contiguous")
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (b, t, hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [batch, nodes, heads_q]")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    # what is allocated here belongs to the stream that the call runs on
+    with cache._there(), _NO_CONTEXT if stream is None else torch.cuda.stream(stream):
         sh = cache._stream(stream)
-        with torch.cuda.stream(stream) if stream is not None else _NO_CONTEXT:
-            if out is None:
-                out = torch.empty(q.shape, dtype=dtype, device=dev)
-            elif out.dtype != dtype or out.device != dev or out.shape != q.shape or out.stride(3) != 1:
-                raise ValueError("out must have q's type, shape and device, head_dim contiguous")
-            if lse is None:
-                lse = torch.empty((b, t, hq), dtype=torch.float32, device=dev)
-            elif lse.dtype != torch.float32 or lse.device != dev or lse.shape != (b, t, hq) or not lse.is_contiguous():
-                raise ValueError("lse must be a contiguous float32 tensor [batch, nodes, heads_q]")
-            if workspace is None:
-                workspace = tree_attention_workspace(q, cache)
-            elif workspace.device != dev or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        a = _tb_cache.tb_tree_attn(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), q.stride()[:3],
-            k.stride()[:3], v.stride()[:3], out.stride()[:3], sq, None if mask is None else mask.data_ptr(), tn,
-            b, t, hq, d, _ATTN_TYPES[dtype], 2 * layer, 2 * layer + 1, 1 / math.sqrt(d) if scale is None else scale,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        if out is None:
+            out = q.new_empty(shape)
+        if lse is None:
+            lse = q.new_empty((b, t, hq), dtype=torch.float32)
+        if workspace is None:
+            workspace = tree_attention_workspace(q, cache)
+        a = _tb_cache.pack_tree_attn(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *qs[:3], *ks[:3], *vs[:3],
+            *out.stride()[:3], sq, 0 if mask is None else mask.data_ptr(), tn, b, t, hq, d, kind, 2 * layer,
+            2 * layer + 1, 1 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), workspace.nbytes)
         _tb_cache.tb_tree_attention(a, cache._c, sh)
     return out, lse

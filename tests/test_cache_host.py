@@ -42,6 +42,17 @@ def test_header_is_plain_c_and_the_binding_has_its_layout(tmp_path):
             assert int(got[f"{s}.{f}"]) == getattr(cls, f).offset
 
 
+def test_packed_arguments_have_the_structure_s_layout():
+    values = range(1, 31)                             # one for each field, the strides three each
+    a = _tb_cache.tb_tree_attn.from_buffer_copy(_tb_cache.pack_tree_attn(*values))
+    flat = []
+    for name, _ in _tb_cache.tb_tree_attn._fields_:
+        x = getattr(a, name)
+        flat += list(x) if name.endswith("_stride") else [x]
+    assert len(flat) == 5 + 12 + 3 + 7 + 1 + 2
+    assert flat == [*range(1, len(flat) + 1)]
+
+
 def test_constants_match_the_header():
     text = open(os.path.join(ROOT, "include", "tb_cache.h")).read()
     for name in ("TB_CACHE_TOKEN_MAJOR", "TB_CACHE_HEAD_MAJOR", "TB_CACHE_SHORT", "TB_CACHE_RANGE", "TB_CACHE_BUSY",
