@@ -53,6 +53,11 @@ def test_packed_arguments_have_the_structure_s_layout():
     assert flat == [*range(1, len(flat) + 1)]
 
 
+def test_c_consumer_calls_every_entry_point():
+    consumer = open(os.path.join(ROOT, "tests", "capi", "cache_check.c")).read()
+    assert [d for d in _tb_cache.EXPORTS if d + "(" not in consumer] == []
+
+
 def test_constants_match_the_header():
     text = open(os.path.join(ROOT, "include", "tb_cache.h")).read()
     for name in ("TB_CACHE_TOKEN_MAJOR", "TB_CACHE_HEAD_MAJOR", "TB_CACHE_SHORT", "TB_CACHE_RANGE", "TB_CACHE_BUSY",
