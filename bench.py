@@ -18,7 +18,7 @@ Default output is ONE JSON line:
 --suite additionally prints one line per configuration (C1-C5, sweep);
 --cpu-suite times the oracle alone on one host core for every configuration.
 The other flags (--baselines, --cache-study, --roofs, --interference, --ring,
---scatter-study, --misaligned, --calibrate-copy) each run one study instead; see --help.
+--scatter-study, --misaligned, --paged, --calibrate-copy) each run one study instead; see --help.
 """
 import argparse
 import hashlib
@@ -1265,6 +1265,110 @@ def misaligned_study(args, torch, tb, wl):
             "validated": ok}}), flush=True)
 
 
+# ---------------------------------------------------------------------------
+# --paged: a serving step over a paged key/value cache
+# ---------------------------------------------------------------------------
+
+def paged_study(args, torch, tb, wl):
+    """A paged key/value cache as a decoding engine uses it (include/tb_cache.h): 32 sequences whose prompts'
+    pages of 32 KiB arrive by the batched copy, as transferred from a prefill, in pools of 8 layers; then the calls
+    of a step, each timed by its launches' own events: one token attending to its context, trees of 16 and
+    of 64 drafted tokens, accepted tokens appended, sequences forked, freed and the cache compacted.
+    One layer's attention is checked against its definition in 64 bits."""
+    import numpy as np
+    from copy_reduce_amd.torch_api import PagedCache, batched_copy, make_desc, tree_attention, tree_attention_workspace
+
+    layers, pages, pt, heads, dim, seqs, group = 8, 16384, 16, 8, 128, 32, 4
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    kv = torch.empty(2 * layers, pages, pt, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    cache = PagedCache(kv, pt, 4 * seqs, 600)
+    lens = [250 * (i + 1) - 3 for i in range(seqs)]
+
+    def ints(v):
+        return torch.tensor(list(v), dtype=torch.int32, device="cuda")
+
+    def timed(name, call, nbytes, flops=0, restore=False):
+        held = cache.state.clone()
+        ms = []
+        for i in range(-args.warmup, args.steps):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            for x in e:
+                x.record()
+            torch.cuda.synchronize()
+            tb.tb_time_next_launch(e[0].cuda_event, e[1].cuda_event)
+            call()
+            torch.cuda.synchronize()
+            if i >= 0:
+                ms.append(e[0].elapsed_time(e[1]))
+            if restore:   # the next turn finds the same tables
+                cache.state.copy_(held)
+        us = statistics.median(ms) * 1e3
+        print(json.dumps({"paged": {"call": name, "kernel_us": round(us, 2), "bytes": nbytes,
+                                    "gbps": round(nbytes / us / 1e3, 1),
+                                    "frac_of_hbm_peak": round(nbytes / us / 1e3 / HBM_PEAK_GBPS, 4),
+                                    "tflops": round(flops / us / 1e6, 1)}}), flush=True)
+
+    print(json.dumps({"paged_device": device_record(torch, tb)}), flush=True)
+    rows = ints(range(seqs))
+    cache.resize(rows, ints(lens))
+    # the prompts' pages, from a staging buffer as another GPU's would be: one copy a page and pool
+    page_bytes = pt * heads * dim * 2
+    used = [int(p) for q in range(seqs) for p in cache.table[q, :-(-lens[q] // pt)]]
+    staged = torch.randint(0, 1 << 14, (2, len(used) * page_bytes // 2), dtype=torch.int16, device="cuda", generator=gen)
+    off = np.zeros((2 * len(used), 3), dtype=np.uint64)
+    off[:, 0] = np.arange(2 * len(used)) * page_bytes
+    off[:, 1] = [kv[i, p].data_ptr() - kv.data_ptr() for i in range(2) for p in used]
+    off[:, 2] = page_bytes
+    desc = make_desc(off, staged.data_ptr(), kv.data_ptr())
+    timed("pages of one layer from a transfer (tb_batched_copy)", lambda: batched_copy(desc), 4 * len(used) * page_bytes)
+
+    token = heads * dim * 2
+    for nodes in (1, 16, 64):
+        q = torch.empty(seqs, nodes, heads * group, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+        k, v = [torch.empty(seqs, nodes, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2)]
+        ws = tree_attention_workspace(q, cache)
+        keys = sum(lens) + seqs * nodes
+        timed(f"attention of {nodes} drafted tokens (tb_tree_attention)",
+              lambda: tree_attention(q, k, v, cache, 1, rows, workspace=ws),
+              2 * keys * token + 2 * q.nbytes, 4 * dim * heads * group * nodes * keys)
+        out, _ = tree_attention(q, k, v, cache, 1, rows, workspace=ws)
+        n, b = lens[5], 5
+        at = cache.table[b, :-(-n // pt)].long()
+        key = torch.cat([kv[2][at].reshape(-1, heads, dim)[:n], k[b]]).double()
+        val = torch.cat([kv[3][at].reshape(-1, heads, dim)[:n], v[b]]).double()
+        worst = 0.0
+        for h in range(heads):
+            x = q[b, :, h * group:(h + 1) * group].double().reshape(-1, dim) @ key[:, h].T.contiguous() / dim ** 0.5
+            u = torch.arange(nodes, device="cuda")
+            x[:, n:].masked_fill_((u[None] > u[:, None]).repeat_interleave(group, 0), float("-inf"))
+            want = torch.softmax(x, 1) @ val[:, h]
+            got = out[b, :, h * group:(h + 1) * group].reshape(-1, dim).double()
+            worst = max(worst, float((got - want).norm() / want.norm()))
+        if not worst < 1e-2:
+            raise RuntimeError(f"attention of {nodes} nodes is {worst} off its definition")
+
+    new = torch.empty(2 * layers, 4 * seqs, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    who = ints(q for q in range(seqs) for _ in range(4))
+    where = ints(lens[q] - 4 + i for q in range(seqs) for i in range(4))
+    timed("4 tokens a sequence appended (tb_page_append)", lambda: cache.append(new, who, where), 2 * new.nbytes)
+    parents, kids = ints(q % seqs for q in range(3 * seqs)), ints(range(seqs, 4 * seqs))
+    tail = sum(n % pt for n in lens)
+    timed("every sequence forked three times (tb_page_fork)", lambda: cache.fork(parents, kids),
+          3 * 2 * 2 * layers * tail * token, restore=True)
+    half, zero = ints(range(0, seqs, 2)), ints([0] * (seqs // 2))
+    timed("half of the sequences freed (tb_page_resize)", lambda: cache.resize(half, zero),
+          16 * sum(-(-lens[q] // pt) for q in range(0, seqs, 2)), restore=True)
+    cache.resize(half, zero)
+    live = pages - int(cache.counts[0])
+    moved = int((cache.refs[live:] > 0).sum())
+    timed("the rest compacted (tb_page_compact)", lambda: cache.compact(), 2 * 2 * layers * moved * page_bytes,
+          restore=True)
+    a, b = ints(range(live, live + 1000)), ints(range(live + 1000, live + 2000))
+    timed("1,000 pages copied (tb_page_copy)", lambda: cache.copy_pages(b, a), 2 * 1000 * 2 * layers * page_bytes)
+    if cache.flags():
+        raise RuntimeError(f"the cache raised flags {cache.flags()}")
+
+
 def calibrate_copy(torch, tb):
     """A plain copy of exactly 268,435,456 bytes read and 268,435,456 written per launch."""
     nbytes = 256 << 20
@@ -1304,6 +1408,9 @@ def main():
     ap.add_argument("--misaligned", action="store_true",
                     help="only time the reduce-copy with sources 0, 4 or 8 bytes off dst's 16-byte alignment "
                          "(1-16 sources of 256 MiB) and C4's batched copies with sources shifted 0-8 bytes, then exit")
+    ap.add_argument("--paged", action="store_true",
+                    help="only time a serving step over a paged key/value cache (pages in by the batched copy, attention "
+                         "of drafted tokens, append, fork, free, compact, copy), then exit")
     ap.add_argument("--only", default="",
                     help="comma-separated suite configurations to run (implies --suite; the bench line is skipped)")
     ap.add_argument("--calibrate-copy", action="store_true",
@@ -1355,6 +1462,9 @@ def main():
         return
     if args.misaligned:
         misaligned_study(args, torch, tb, wl)
+        return
+    if args.paged:
+        paged_study(args, torch, tb, wl)
         return
     if args.suite or args.only:
         suite(args, torch, tb, wl)
