@@ -337,43 +337,34 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // The three steps of a resize.  With many table entries each is a launch of its own, spread over
 // the chip; with few, one workgroup does all three.
 
-// Release of entry i by one workgroup.  from[i]: pages the row had, -1 for an entry
-// that is skipped; to[i]: pages it is to have.  *again: a word of LDS.
+// Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
+// pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have.
 template <int BS>
-__device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i, int *again) {
+__device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i, uint32_t t) {
     const int32_t q = seqs[i], len = lens[i];
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *again = 0;
-    __syncthreads();
-    bool ok = q >= 0;
-    if (ok && ((uint32_t)q >= s.max_seqs || len < 0 || (uint32_t)len > s.max_pages * s.page_tokens)) {
-        ok = false;
-        if (threadIdx.x == 0)
-            raise(s, TB_CACHE_RANGE);
-    }
-    if (ok) {
-        for (uint32_t k = threadIdx.x; k < i; k += BS)
-            if (seqs[k] == q)
-                *again = 1;
-    }
-    __syncthreads();
-    if (ok && *again) {
-        ok = false;
-        if (threadIdx.x == 0)
-            raise(s, TB_CACHE_TWICE);
-    }
-    if (!ok) {
-        if (threadIdx.x == 0)
+    const bool in_range = (uint32_t)q < s.max_seqs && len >= 0 && (uint32_t)len <= s.max_pages * s.page_tokens;
+    bool again = false;
+    if (in_range)
+        for (uint32_t k = t; k < i; k += BS)
+            again |= seqs[k] == q;
+    if constexpr (BS == 64)
+        again = __any(again);
+    else
+        again = __syncthreads_or(again);
+    if (!in_range || again) {
+        if (t == 0) {
             s.w.from[i] = -1;
+            if (q >= 0)
+                raise(s, in_range ? TB_CACHE_TWICE : TB_CACHE_RANGE);
+        }
         return;
     }
     const int32_t had = pages_of(length_of(s, q), s.page_tokens), has = pages_of(len, s.page_tokens);
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         s.w.from[i] = had;
         s.w.to[i] = has;
     }
-    for (int32_t j = has + (int32_t)threadIdx.x; j < had; j += BS) {
+    for (int32_t j = has + (int32_t)t; j < had; j += BS) {
         const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
         if (page < s.num_pages && atomicSub(&s.refs[page], 1) == 1)
             atomicOr(&s.w.bits[page >> 5], 1u << (page & 31));
@@ -384,8 +375,11 @@ __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs
 // first, on a stack that had `top` pages.  The chunks above are counted first; the one
 // with the lowest pages then knows all of them, and deals the new pages.
 constexpr uint32_t kStackWords = 4096;
-// Up to this much resize_few_kernel does a whole resize.
-constexpr uint32_t kFewEntries = 16, kFewPages = 8192;
+// One workgroup does a whole resize up to these limits: a wave takes an entry, 64 pages of its row at
+// a time.  Against the three launches, us a call: 6 rows of 500 tokens 11.2 to 17.9, 16 rows of 8,000
+// (500 pages) 14.4 to 16.4, 32 rows of 2,000 12.1 to 17.1; past the limits 32 rows of 8,000 19.9 to
+// 17.1 and 64 rows of 2,000 17.5 both ways.
+constexpr uint32_t kFewEntries = 32, kFewPages = 512, kFewWork = 8192;
 __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                                         uint32_t chunk, uint32_t top, uint32_t *lds) {
     const uint32_t t = threadIdx.x, words = (s.num_pages + 31) / 32;
@@ -445,12 +439,12 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
 }
 
 template <int BS>
-__device__ __forceinline__ void grow(const CacheState &s, const int32_t *seqs, uint32_t i) {
+__device__ __forceinline__ void grow(const CacheState &s, const int32_t *seqs, uint32_t i, uint32_t t) {
     const int32_t had = s.w.from[i];
     if (had < 0)
         return;
     const int32_t has = s.w.to[i], first = s.w.aux[i];
-    for (int32_t j = had + (int32_t)threadIdx.x; j < has; j += BS) {
+    for (int32_t j = had + (int32_t)t; j < has; j += BS) {
         const int32_t page = s.free_list[first - (j - had)];
         s.table[(uint64_t)seqs[i] * s.max_pages + j] = page;
         if ((uint32_t)page < s.num_pages)
@@ -464,10 +458,9 @@ __device__ __forceinline__ uint32_t stack_top(const CacheState &s) {
 }
 
 __global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_t *seqs, const int32_t *lens) {
-    __shared__ int again;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         *s.w.top = stack_top(s);   // restack's last chunk writes the new one while others still start
-    release<256>(s, seqs, lens, blockIdx.x, &again);
+    release<256>(s, seqs, lens, blockIdx.x, threadIdx.x);
 }
 
 __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
@@ -478,7 +471,7 @@ __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32
 // Also clears the bits, which every chunk of restack has read by now.
 __global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *seqs, uint32_t n) {
     if (blockIdx.x < n) {
-        grow<256>(s, seqs, blockIdx.x);
+        grow<256>(s, seqs, blockIdx.x, threadIdx.x);
         return;
     }
     const uint32_t words = (s.num_pages + 31) / 32;
@@ -487,17 +480,17 @@ __global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *
             s.w.bits[k] = 0;
 }
 
+// A wave an entry.
 __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
     __shared__ uint32_t lds[16];
-    __shared__ int again;
-    const uint32_t top = stack_top(s);
-    for (uint32_t i = 0; i < n; i++)
-        release<1024>(s, seqs, lens, i, &again);
+    const uint32_t top = stack_top(s), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (uint32_t i = wave; i < n; i += 16)
+        release<64>(s, seqs, lens, i, lane);
     __syncthreads();
     restack(s, seqs, lens, n, 0, top, lds);
     __syncthreads();
-    for (uint32_t i = 0; i < n; i++)
-        grow<1024>(s, seqs, i);
+    for (uint32_t i = wave; i < n; i += 16)
+        grow<64>(s, seqs, i, lane);
     for (uint32_t k = threadIdx.x; k < (s.num_pages + 31) / 32; k += 1024)
         if (s.w.bits[k] != 0)
             s.w.bits[k] = 0;
@@ -506,9 +499,7 @@ __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const in
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream) {
     const uint32_t words = (s.num_pages + 31) / 32, chunks = (words + kStackWords - 1) / kStackWords;
-    // One workgroup goes over the entries in turn, some half a microsecond each; the three launches cost
-    // some eight, whatever they do.
-    if (chunks == 1 && n <= kFewEntries && s.max_pages <= kFewPages)
+    if (chunks == 1 && n <= kFewEntries && s.max_pages <= kFewPages && (uint64_t)n * s.max_pages <= kFewWork)
         return launch(resize_few_kernel, 1, 1024, stream, nullptr, s, seqs, lens, n);
     LaunchSeq seq;
     hipError_t e = launch(release_kernel, n, 256, stream, nullptr, s, seqs, lens);
