@@ -1161,7 +1161,7 @@ static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count, uint64_
     const uint64_t most = 4 * room / each > 1 ? 4 * room / each : 1, least = room / each > 1 ? room / each : 1;
     uint64_t best = least;
     double best_use = 0;
-    for (uint64_t n = least; n <= most; n++) {
+    for (uint64_t n = least; n <= most && best_use < 0.96; n++) {
         const double use = (double)(n * each) / (double)((n * each + room - 1) / room * room);
         if (use > best_use + 0.04) {
             best = n;

@@ -206,10 +206,10 @@ def test_no_pools_and_two_pages():
 
 def test_far_pages():
     """Byte offsets past 2^32 within one pool."""
-    note("paged cache, a pool of 6 GiB")
+    note("paged cache, a pool of 5.9 GiB")
     require_gpu()
     from copy_reduce_amd.torch_api import PagedCache
-    pages, pt = 3 << 10, 16
+    pages, pt = 3000, 16
     kv = torch.zeros(2, pages, pt, 8, 8192, dtype=torch.bfloat16, device="cuda")
     c = PagedCache(kv, pt, 2, 4)
     c.free_list[:pages] = torch.arange(pages, dtype=torch.int32, device="cuda")   # highest page on top

@@ -30,13 +30,14 @@ def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def setup(lens, heads=2, dim=64, pt=16, layout="token", dtype=torch.bfloat16, layers=1, seed=0, pad=0, spread=1.0):
+def setup(lens, heads=2, dim=64, pt=16, layout="token", dtype=torch.bfloat16, layers=1, seed=0, pad=0, spread=1.0, room=0):
     """A cache of sequences of these lengths, pages in a random order, and its model.
-    What no sequence holds is NaN."""
+    What no sequence holds is NaN.  room: tokens that a row of the table has place for, if more than these; past some
+    thousands the keys are cut into shares, below a workgroup takes a whole sequence."""
     require_gpu()
     from copy_reduce_amd.torch_api import PagedCache
     g = torch.Generator().manual_seed(seed)
-    seqs, width = max(1, len(lens)), max(1, max([-(-n // pt) for n in lens], default=1)) + 1
+    seqs, width = max(1, len(lens)), max(1, max([-(-n // pt) for n in [room, *lens]])) + 1
     pages = sum(-(-n // pt) for n in lens) + 3
     page = (pt, heads, dim) if layout == "token" else (heads, pt, dim)
     kv = torch.full((2 * layers, pages) + page, math.nan, dtype=dtype)
@@ -108,31 +109,34 @@ def run(c, m, q, k, v, seqs, mask=None, nodes=None, scale=None, what="", **kw):
     return got
 
 
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("dim", [64, 96, 128, 256])
 @pytest.mark.parametrize("layout,pt", [("token", 16), ("head", 16), ("token", 1), ("head", 5), ("token", 20), ("token", 64), ("head", 96)])
-def test_shapes(dim, dtype, layout, pt):
+def test_shapes(dim, dtype, layout, pt, room):
     note(f"tree attention dim {dim} {dtype} {layout} pages of {pt}")
-    c, m, g = setup([1, 37, 128, 200], heads=2, dim=dim, pt=pt, layout=layout, dtype=dtype, seed=dim + pt, pad=8 * (pt == 5))
+    c, m, g = setup([1, 37, 128, 200], heads=2, dim=dim, pt=pt, layout=layout, dtype=dtype, seed=dim + pt, pad=8 * (pt == 5), room=room)
     q, k, v = inputs(g, 4, 5, 6, 2, dim, dtype)
     run(c, m, q, k, v, [2, 0, 3, 1], what="chain")
 
 
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("nodes", [1, 2, 3, 7, 8, 15, 16, 17, 31, 33, 63, 64, 65, 100, 130])
 @pytest.mark.parametrize("group", [1, 4, 7])
-def test_nodes_and_groups(nodes, group):
+def test_nodes_and_groups(nodes, group, room):
     note(f"tree attention {nodes} nodes, {group} query heads a key head")
-    c, m, g = setup([70, 0, 259], heads=1, seed=nodes)
+    c, m, g = setup([70, 0, 259], heads=1, seed=nodes, room=room)
     q, k, v = inputs(g, 3, nodes, group, 1, 64, torch.bfloat16)
     run(c, m, q, k, v, [0, 1, 2], mask=tree_mask(g, 3, nodes), nodes=[nodes, nodes, nodes - nodes // 3], what="tree")
 
 
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("lens", [[0], [1], [15], [16], [31], [32], [33], [127], [128], [129], [255, 256, 257], [511, 513, 1], [1025, 0, 3], [4097],
                                   [2000] + [1] * 30])
 @pytest.mark.parametrize("nodes", [1, 6])
-def test_lengths(lens, nodes):
+def test_lengths(lens, nodes, room):
     note(f"tree attention lengths {lens[:4]} {nodes} nodes")
-    c, m, g = setup(lens, heads=2, seed=sum(lens))
+    c, m, g = setup(lens, heads=2, seed=sum(lens), room=room)
     q, k, v = inputs(g, len(lens), nodes, 8, 2, 64, torch.bfloat16)
     run(c, m, q, k, v, list(range(len(lens))), what="chain")
 
@@ -145,19 +149,31 @@ def test_long(dtype):
     run(c, m, q, k, v, [0, 1], what="long")
 
 
-@pytest.mark.parametrize("batch", [1, 65, 300])
-def test_batches(batch):
-    note(f"tree attention batch {batch}")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
+@pytest.mark.parametrize("batch,nodes", [(1, 1), (65, 1), (300, 1), (2, 20), (513, 17)])
+def test_batches(batch, nodes, room):
+    note(f"tree attention batch {batch} {nodes} nodes")
     lens = [(37 * i) % 90 for i in range(batch)]
-    c, m, g = setup(lens, heads=1, seed=batch)
-    q, k, v = inputs(g, batch, 1, 2, 1, 64, torch.bfloat16)
+    c, m, g = setup(lens, heads=1, seed=batch, room=room)
+    q, k, v = inputs(g, batch, nodes, 2, 1, 64, torch.bfloat16)
     run(c, m, q, k, v, torch.randperm(batch, generator=g).tolist(), what="batch")
 
 
-def test_masks_that_leave_nothing():
+@pytest.mark.parametrize("lens,room,heads,dim,nodes,group", [([4700], 8192, 128, 256, 1, 1), ([4000, 2300, 2049, 5], 0, 64, 64, 17, 1), ([9000], 0, 16, 64, 64, 16)],
+                         ids=["few rows", "many rows, whole", "many rows, shares"])
+def test_more_pages_than_a_workgroup_keeps(lens, room, heads, dim, nodes, group):
+    """Pages of one token: parts of more pages than the 2,048 whose numbers a workgroup keeps."""
+    note(f"tree attention, {lens} pages of one token")
+    c, m, g = setup(lens, heads=heads, dim=dim, pt=1, room=room)
+    q, k, v = inputs(g, len(lens), nodes, heads * group, heads, dim, torch.bfloat16)
+    run(c, m, q, k, v, list(range(len(lens))), what="pages of one token")
+
+
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
+def test_masks_that_leave_nothing(room):
     """Rows that see no node, with and without a context; a node that sees all others; none at all."""
     note("tree attention, empty rows")
-    c, m, g = setup([0, 40, 0, 0], heads=2)
+    c, m, g = setup([0, 40, 0, 0], heads=2, room=room)
     q, k, v = inputs(g, 4, 6, 4, 2, 64, torch.bfloat16)
     mask = torch.zeros(4, 6, 1, dtype=torch.int64)
     mask[0, 2, 0] = 0b111111
@@ -165,20 +181,22 @@ def test_masks_that_leave_nothing():
     mask[2, 0, 0] = 1
     run(c, m, q, k, v, [0, 1, 2, 3], mask=mask, what="masks")
     run(c, m, q, k, v, [0, 1, 2, 3], mask=mask, nodes=[6, 0, 1, 6], what="masks and sizes")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_rows_that_are_not_there():
+def test_rows_that_are_not_there(room):
     note("tree attention, padded batch")
-    c, m, g = setup([33, 20], heads=2)
+    c, m, g = setup([33, 20], heads=2, room=room)
     q, k, v = inputs(g, 5, 3, 4, 2, 64, torch.bfloat16)
     run(c, m, q, k, v, [1, -1, 0, 2, -7], nodes=[3, 3, 2, 3, 9], what="padding")
 
 
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf, 3e38])
-def test_masked_values_have_no_effect(value):
+def test_masked_values_have_no_effect(value, room):
     """What a row does not see may hold anything: nodes of other branches and padded nodes (the cache's unused tokens are NaN in every test)."""
     note(f"tree attention, {value} in masked places")
-    c, m, g = setup([40, 0], heads=2)
+    c, m, g = setup([40, 0], heads=2, room=room)
     q, k, v = inputs(g, 2, 40, 4, 2, 64, torch.bfloat16)
     mask = tree_mask(g, 2, 40)
     from copy_reduce_amd.torch_api import tree_attention
@@ -213,27 +231,30 @@ def test_seen_values_that_are_not_finite():
     assert torch.equal(got[..., rest], want[..., rest]) and torch.equal(got[0, 0, 0, 9], want[0, 0, 0, 9])
 
 
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("spread", [8.0, 30.0])
-def test_sharp_scores(spread):
+def test_sharp_scores(spread, room):
     """Scores of hundreds: single keys decide, running maxima move."""
     note(f"tree attention, scores spread by {spread}")
-    c, m, g = setup([700, 64], heads=1, spread=spread ** 0.5)
+    c, m, g = setup([700, 64], heads=1, spread=spread ** 0.5, room=room)
     q, k, v = inputs(g, 2, 9, 4, 1, 64, torch.bfloat16, spread ** 0.5)
     run(c, m, q, k, v, [0, 1], mask=tree_mask(g, 2, 9), scale=1.0, what="sharp")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_scale_zero_and_negative():
+def test_scale_zero_and_negative(room):
     note("tree attention, scale 0 and negative")
-    c, m, g = setup([100], heads=1)
+    c, m, g = setup([100], heads=1, room=room)
     q, k, v = inputs(g, 1, 2, 2, 1, 64, torch.bfloat16)
     run(c, m, q, k, v, [0], scale=0.0, what="0")
     run(c, m, q, k, v, [0], scale=-0.3, what="negative")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_strides():
+def test_strides(room):
     """q, k, v as parts of one projection, out and its rows in a larger tensor; guards stay."""
     note("tree attention, strides")
-    c, m, g = setup([90, 33], heads=2, dim=64)
+    c, m, g = setup([90, 33], heads=2, dim=64, room=room)
     fused = torch.randn(2, 4, 8 + 2 + 2, 64, generator=g).to(torch.bfloat16).cuda()
     q, k, v = fused[:, :, :8], fused[:, :, 8:10], fused[:, :, 10:]
     big = torch.full((2, 6, 8, 72), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -261,13 +282,14 @@ def test_same_workspace_again_and_determinism():
         assert torch.equal(first[0], x[0]) and torch.equal(first[1], x[1])
     ref = attention(m, 0, q.cpu(), k.cpu(), v.cpu(), [2, 2, 1])
     compare(other, ref, 3004, 64, torch.bfloat16, "rows twice")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_captured():
+def test_captured(room):
     """A graph of two calls that share a workspace, replayed over changing lengths and inputs."""
     note("tree attention, captured")
     from copy_reduce_amd.torch_api import tree_attention, tree_attention_workspace
-    c, m, g = setup([500, 60], heads=2)
+    c, m, g = setup([500, 60], heads=2, room=room)
     q, k, v = [x.cuda() for x in inputs(g, 2, 3, 4, 2, 64, torch.bfloat16)]
     seqs = ints([0, 1])
     w = tree_attention_workspace(q, c)
@@ -320,24 +342,26 @@ def test_second_layer_and_far_pages():
     m = Model(4, 50, 1, 1, new[:, None].expand(4, 4, 50, 16, d), "token")
     m.resize([0], [50])
     compare(got, attention(m, 1, q, k, v, [0]), 52, d, torch.bfloat16, "far")
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_wrong_pages_are_not_followed():
+def test_wrong_pages_are_not_followed(room):
     """Table entries out of range give some values, and no access outside the pools."""
     note("tree attention, page numbers out of range")
     from copy_reduce_amd.torch_api import tree_attention
-    c, m, g = setup([100, 40], heads=1)
+    c, m, g = setup([100, 40], heads=1, room=room)
     c.table[0, 2], c.table[0, 3], c.lens[1] = -5, c.num_pages, 1 << 30
     q, k, v = [x.cuda() for x in inputs(g, 2, 2, 2, 1, 64, torch.bfloat16)]
     tree_attention(q, k, v, c, 0, ints([0, 1]))
     torch.cuda.synchronize()
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 
 
-def test_serving_run():
+def test_serving_run(room):
     """Prompts in, a tree scored, its best path accepted, a fork, a compaction, and the next step over the moved pages."""
     note("tree attention, a serving run")
     from copy_reduce_amd.torch_api import tree_attention
-    c, m, g = setup([45, 17, 0, 0], heads=2, dim=128, layers=2, layout="head")
+    c, m, g = setup([45, 17, 0, 0], heads=2, dim=128, layers=2, layout="head", room=room)
     for step in range(3):
         t = 5
         q, k, v = inputs(g, 2, t, 4, 2, 128, torch.bfloat16)
