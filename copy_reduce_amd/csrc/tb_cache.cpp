@@ -253,6 +253,9 @@ static bool attn_sizes_ok(const tb_tree_attn *a, const tb_cache *c) {
 int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64_t *bytes_out) {
     if (bytes_out == nullptr || !attn_sizes_ok(a, c))
         return TB_ERR_INVALID;
+    *bytes_out = 0;
+    if (a->batch == 0 || a->nodes == 0)
+        return TB_OK;
     int cus = 0;
     const int rc = tbh::cu_count_of_device(&cus);
     if (rc == TB_OK)

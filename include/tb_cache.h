@@ -195,7 +195,7 @@ typedef struct tb_tree_attn {
 
 /*
  * Bytes of workspace a call needs; depends on batch, nodes, heads and head_dim
- * and not on the lengths.  Only those fields of `attn` and heads of `cache`
+ * and not on the lengths; 0 for no batch or no nodes.  Only those fields of `attn` and heads of `cache`
  * are read.  Errors: TB_ERR_INVALID; TB_ERR_HIP if the device cannot be queried.
  */
 int tb_tree_attention_workspace(const tb_tree_attn *attn, const tb_cache *cache, uint64_t *bytes_out);

@@ -177,6 +177,10 @@ def test_attention_refuses_other_caches_and_takes_nothing_to_do():
     n = ctypes.c_uint64()
     assert tb.lib.tb_tree_attention_workspace(_attn(head_dim=1), _cache(), ctypes.byref(n)) == inv
     assert tb.lib.tb_tree_attention_workspace(_attn(), _cache(), None) == inv
+    for nothing in (dict(batch=0), dict(nodes=0)):
+        n.value = 7
+        assert tb.lib.tb_tree_attention_workspace(_attn(**nothing), _cache(), ctypes.byref(n)) == tb.TB_OK
+        assert n.value == 0
 
 
 def test_python_refuses_host_tensors():

@@ -267,6 +267,16 @@ def test_strides(room):
     run(c, m, *one, [0, 1], what="one node of a larger tensor")
 
 
+def test_nothing_to_do():
+    note("tree attention, no batch, no nodes")
+    from copy_reduce_amd.torch_api import tree_attention
+    c, m, g = setup([5], heads=2)
+    for b, t in ((0, 3), (1, 0)):
+        q, k, v = [x.cuda() for x in inputs(g, b, t, 4, 2, 64, torch.bfloat16)]
+        out, lse = tree_attention(q, k, v, c, 0, ints([0] * b))
+        assert out.shape == q.shape and lse.shape == (b, t, 4)
+
+
 def test_same_workspace_again_and_determinism():
     note("tree attention, one workspace for calls in a row")
     from copy_reduce_amd.torch_api import tree_attention, tree_attention_workspace
