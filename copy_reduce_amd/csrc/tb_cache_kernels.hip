@@ -38,13 +38,13 @@ __device__ __forceinline__ uint32_t fresh(const uint32_t *p) {
 
 // Exclusive sum of v over the workgroup's threads in order, *total the whole
 // sum; lds holds one word a wave and is free again after the next barrier.
-template <int BS>
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t *total, uint32_t *lds) {
+template <int BS, typename N>
+__device__ __forceinline__ N block_sum(N v, N *total, N *lds) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t x = v;
+    N x = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(x, d);
+        const N y = __shfl_up(x, d);
         if (lane >= d)
             x += y;
     }
@@ -52,10 +52,10 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t *total, uint3
     if (lane == 63)
         lds[wave] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    N before = 0, all = 0;
 #pragma unroll
     for (int k = 0; k < BS / 64; k++) {
-        const uint32_t t = lds[k];
+        const N t = lds[k];
         before += k < wave ? t : 0;
         all += t;
     }
@@ -381,7 +381,7 @@ constexpr uint32_t kStackWords = 4096;
 // 17.1 and 64 rows of 2,000 17.5 both ways.
 constexpr uint32_t kFewEntries = 32, kFewPages = 512, kFewWork = 8192;
 __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
-                                        uint32_t chunk, uint32_t top, uint32_t *lds) {
+                                        uint32_t chunk, uint32_t top, uint32_t *lds, uint64_t *wide) {
     const uint32_t t = threadIdx.x, words = (s.num_pages + 31) / 32;
     uint32_t total, above = 0;
 #pragma unroll 4
@@ -410,16 +410,16 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
     if (chunk != 0)
         return;
     top = min(top + total, s.num_pages);
-    uint32_t need_all = 0;
+    uint64_t need_all = 0, asked;   // rows may ask for 2^31 pages each
     for (uint32_t i0 = 0; i0 < n; i0 += 1024) {
         const uint32_t i = i0 + t;
-        uint32_t need = 0;
+        uint64_t need = 0;
         if (i < n && s.w.from[i] >= 0 && s.w.to[i] > s.w.from[i])
             need = (uint32_t)(s.w.to[i] - s.w.from[i]);
-        const uint32_t before = block_sum<1024>(need, &total, lds);
+        const uint64_t before = block_sum<1024>(need, &asked, wide);
         if (i < n)
-            s.w.aux[i] = (int32_t)top - 1 - (int32_t)(need_all + before);
-        need_all += total;
+            s.w.aux[i] = (int32_t)(top - 1 - (uint32_t)(need_all + before));   // used only if there are enough
+        need_all += asked;
     }
     const bool enough = need_all <= top;
     for (uint32_t i = t; i < n; i += 1024) {
@@ -432,7 +432,7 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
         s.lens[seqs[i]] = lens[i];
     }
     if (t == 0) {
-        s.counts[0] = (int32_t)(enough ? top - need_all : top);
+        s.counts[0] = (int32_t)(enough ? top - (uint32_t)need_all : top);
         if (!enough)
             raise(s, TB_CACHE_SHORT);
     }
@@ -465,7 +465,8 @@ __global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_
 
 __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
     __shared__ uint32_t lds[16];
-    restack(s, seqs, lens, n, blockIdx.x, *s.w.top, lds);
+    __shared__ uint64_t wide[16];
+    restack(s, seqs, lens, n, blockIdx.x, *s.w.top, lds, wide);
 }
 
 // Also clears the bits, which every chunk of restack has read by now.
@@ -483,11 +484,12 @@ __global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *
 // A wave an entry.
 __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
     __shared__ uint32_t lds[16];
+    __shared__ uint64_t wide[16];
     const uint32_t top = stack_top(s), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (uint32_t i = wave; i < n; i += 16)
         release<64>(s, seqs, lens, i, lane);
     __syncthreads();
-    restack(s, seqs, lens, n, 0, top, lds);
+    restack(s, seqs, lens, n, 0, top, lds, wide);
     __syncthreads();
     for (uint32_t i = wave; i < n; i += 16)
         grow<64>(s, seqs, i, lane);
@@ -544,7 +546,7 @@ __global__ __launch_bounds__(1024) void compact_count_kernel(CacheState s) {
     uint32_t holes, movers, total;
     look_at(s, blockIdx.x, border_of(s), &holes, &movers);
     // both counts are at most kScanChunk, 4096: one sum
-    (void)block_sum<1024>(__popc(holes) | __popc(movers) << 16, &total, lds);
+    (void)block_sum<1024>((uint32_t)(__popc(holes) | __popc(movers) << 16), &total, lds);
     if (threadIdx.x == 0) {
         s.w.chunk[2 * blockIdx.x] = total & 0xffff;
         s.w.chunk[2 * blockIdx.x + 1] = total >> 16;
@@ -570,7 +572,7 @@ __global__ __launch_bounds__(1024) void compact_rank_kernel(CacheState s, uint32
     for (uint32_t c = blockIdx.x; c < blockIdx.x + mine; c++) {
         uint32_t h, m;
         look_at(s, c, live, &h, &m);
-        const uint32_t before = block_sum<1024>(__popc(h) | __popc(m) << 16, &total, lds);
+        const uint32_t before = block_sum<1024>((uint32_t)(__popc(h) | __popc(m) << 16), &total, lds);
         uint32_t at = holes + (before & 0xffff), page = c * kScanChunk + threadIdx.x * 4;
         for (uint32_t k = 0; k < 4; k++)
             if (h >> k & 1)

@@ -151,6 +151,21 @@ def test_short_of_pages():
     assert c.flags() == 0
 
 
+def test_far_too_much_is_asked_for():
+    """Sixteen rows of 2^28 pages: their sum is 0 in 32 bits."""
+    note("paged cache, 2^32 pages asked for")
+    require_gpu()
+    from copy_reduce_amd.torch_api import PagedCache
+    from copy_reduce_amd import _tb_cache as t
+    rows, most = 16, 1 << 28
+    c = PagedCache(torch.zeros(2, 5, 1, 1, 8, dtype=torch.bfloat16, device="cuda"), 1, rows, most)   # a table of 16 GiB
+    c.resize(ints(list(range(rows))), ints([most] * rows))
+    assert c.flags(clear=True) == t.TB_CACHE_SHORT
+    assert not c.lens.any() and not c.refs.any() and int(c.counts[0]) == 5
+    c.resize(ints([rows - 1]), ints([5]))
+    assert c.flags() == 0 and c.table[rows - 1, :5].tolist() == [0, 1, 2, 3, 4] and int(c.counts[0]) == 0
+
+
 def test_shared_pages_are_not_written():
     note("paged cache, append to a shared page")
     from copy_reduce_amd import TB_CACHE_SHARED
