@@ -66,12 +66,12 @@ tbk::CacheState state_of(const tb_cache *c) {
     return s;
 }
 
-// Whether 16-byte accesses fit a cache's pages (and, with heads > 0 apart, each head).
-bool vectors_fit(const tb_cache *c) {
-    if (c->head_bytes % 16 != 0 || c->page_stride % 16 != 0)
+// Whether every page begins at a multiple of `bytes`.
+bool pages_aligned(const tb_cache *c, uint64_t bytes) {
+    if (c->page_stride % bytes != 0)
         return false;
     for (uint32_t p = 0; p < c->npools; p++)
-        if (!aligned(c->pools[p], 16))
+        if (!aligned(c->pools[p], bytes))
             return false;
     return true;
 }
@@ -80,6 +80,7 @@ bool vectors_fit(const tb_cache *c) {
 // with none, for caches without pools).  `parts`: the used tokens of a head-major page are a stretch a head.
 template <typename Launch>
 hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launch launch_one) {
+    const bool whole = !parts;
     tbk::PageShape g;
     g.src_stride = src->page_stride;
     g.dst_stride = dst->page_stride;
@@ -89,7 +90,7 @@ hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launc
     parts = parts && dst->layout == TB_CACHE_HEAD_MAJOR;
     g.runs = parts ? dst->heads : 1;
     g.token_bytes = (uint32_t)(parts ? dst->head_bytes : token_bytes(dst));
-    const bool fit = vectors_fit(dst) && vectors_fit(src);
+    const bool fit = (whole ? page_bytes(dst) : g.token_bytes) % 16 == 0 && pages_aligned(dst, 16) && pages_aligned(src, 16);
     if (dst->npools == 0) {   // what rides along with the copy has to run all the same; no page is in range
         g.src_pages = g.dst_pages = 0;
         const tbk::Pools none = {};
@@ -170,12 +171,15 @@ int tb_page_append(const tb_cache *cache, const void *rows, uint64_t nrows, uint
     a.row_stride = row_stride;
     a.pool_stride = pool_stride;
     a.page_stride = cache->page_stride;
-    a.heads = cache->heads;
-    a.head_bytes = cache->head_bytes;
-    a.token_step = token_major ? bytes : cache->head_bytes;
-    a.head_step = token_major ? cache->head_bytes : (uint64_t)cache->page_tokens * cache->head_bytes;
+    a.heads = token_major ? 1 : cache->heads;   // a token's stretches in the page
+    a.head_bytes = (uint32_t)(token_major ? bytes : cache->head_bytes);
+    a.token_step = a.head_bytes;
+    a.head_step = (uint64_t)cache->page_tokens * cache->head_bytes;
     a.n = n;
-    const bool fit = vectors_fit(cache) && aligned(rows, 16) && row_stride % 16 == 0 && pool_stride % 16 == 0;
+    uint32_t piece = 1;
+    for (uint32_t w : {4u, 16u})
+        if (a.head_bytes % w == 0 && pages_aligned(cache, w) && aligned(rows, w) && row_stride % w == 0 && pool_stride % w == 0)
+            piece = w;
     const tbk::CacheState s = state_of(cache);
     tbk::LaunchSeq seq;
     for (uint32_t p0 = 0; p0 < cache->npools; p0 += tbk::kPoolsPerLaunch) {
@@ -188,7 +192,7 @@ int tb_page_append(const tb_cache *cache, const void *rows, uint64_t nrows, uint
         if (p0 + m == cache->npools)
             seq.last();
         const hipError_t e =
-            tbk::launch_append(pools, m, s, a, fit, static_cast<hipStream_t>(stream));
+            tbk::launch_append(pools, m, s, a, piece, static_cast<hipStream_t>(stream));
         if (e != hipSuccess)
             return hip_fail(e, "page append launch");
     }

@@ -109,8 +109,9 @@ struct AppendArgs {
 hipError_t launch_cache_init(const CacheState &s, hipStream_t stream);
 hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
                             bool aligned16, hipStream_t stream);
+// piece: 16, 4 or 1 bytes, what every address and a head are multiples of.
 hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a,
-                         bool aligned16, hipStream_t stream);
+                         uint32_t piece, hipStream_t stream);
 // A fork: its plan, then its pages (pairs over the plan) and, with the launch that has `rows`, its rows.
 hipError_t launch_fork_plan(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
                             hipStream_t stream);

@@ -186,45 +186,78 @@ hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape
 
 // ---- append --------------------------------------------------------------------
 
-// One thread moves E bytes of one token in one pool (x: token and place, y: pool).
 template <int E>
-__global__ __launch_bounds__(256) void append_kernel(Pools pools, CacheState s, AppendArgs a, uint32_t parts) {
-    const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t i = at / parts;
-    if (i >= a.n)
-        return;
-    const uint32_t off = (uint32_t)(at % parts) * E;
-    const int32_t q = a.seqs[i];
-    if (q < 0)
-        return;
-    const int32_t pos = a.positions[i];
-    const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
-    if ((uint32_t)q >= s.max_seqs || pos < 0 || pos >= length_of(s, q) || row >= a.nrows) {
-        if (off == 0 && blockIdx.y == 0)
-            raise(s, TB_CACHE_RANGE);
-        return;
+struct Piece;
+template <>
+struct Piece<16> {
+    typedef u32x4 T;
+};
+template <>
+struct Piece<4> {
+    typedef uint32_t T;
+};
+template <>
+struct Piece<1> {
+    typedef uint8_t T;
+};
+
+// One thread moves E bytes of one token in kAppendPools pools (x: token and place, strided; y: pools), so
+// that the way to the page (list, length, table, references: four loads, each waiting for the one before) is
+// gone once for all of them and their loads are in flight together.  The bytes are only moved, so HBM
+// bounds it: 4,096 tokens of 2 KiB in 64 pools in 193 us, 5.6 TB/s; with one pool a thread 273 us, with two
+// 225, with eight 534; without nontemporal stores 284 with
+// one.  The loads go through the caches: nontemporal ones cost 512 tokens 36 us where these take 24.
+// A few tokens are a launch: 4 us.  E is what all addresses are multiples of: 2,048 tokens
+// of 1,600 bytes in 16 pools take 18 us by 16 bytes and took 200 by single ones.
+constexpr int kAppendPools = 4;
+template <int E>
+__global__ __launch_bounds__(256) void append_kernel(Pools pools, CacheState s, AppendArgs a, uint32_t parts, uint32_t npools) {
+    typedef typename Piece<E>::T piece;
+    typedef __attribute__((address_space(1))) piece gpiece;
+    const uint64_t all = (uint64_t)a.n * parts;
+    constexpr uint32_t U = kAppendPools;
+    const uint32_t pool = blockIdx.y * U;
+    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
+        const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
+        const uint32_t off = (uint32_t)(at - (uint64_t)i * parts) * E;
+        const int32_t q = a.seqs[i];
+        if (q < 0)
+            continue;
+        const int32_t pos = a.positions[i];
+        const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
+        if ((uint32_t)q >= s.max_seqs || pos < 0 || pos >= length_of(s, q) || row >= a.nrows) {
+            if (off == 0 && blockIdx.y == 0)
+                raise(s, TB_CACHE_RANGE);
+            continue;
+        }
+        const uint32_t j = (uint32_t)pos / s.page_tokens, in_page = (uint32_t)pos % s.page_tokens;
+        const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
+        if (page >= s.num_pages || s.refs[page] > 1) {
+            if (off == 0 && blockIdx.y == 0)
+                raise(s, page >= s.num_pages ? TB_CACHE_RANGE : TB_CACHE_SHARED);
+            continue;
+        }
+        const uint64_t src = a.rows + pool * a.pool_stride + row * a.row_stride + off;
+        const uint64_t dst = page * a.page_stride + in_page * a.token_step + (off / a.head_bytes) * a.head_step + off % a.head_bytes;
+        piece x[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++)
+            if (pool + u < npools)
+                x[u] = *(const gpiece *)(src + u * a.pool_stride);
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++)
+            if (pool + u < npools)
+                __builtin_nontemporal_store(x[u], (gpiece *)(pools.dst[pool + u] + dst));
     }
-    const uint32_t j = (uint32_t)pos / s.page_tokens, in_page = (uint32_t)pos % s.page_tokens;
-    const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
-    if (page >= s.num_pages || s.refs[page] > 1) {
-        if (off == 0 && blockIdx.y == 0)
-            raise(s, page >= s.num_pages ? TB_CACHE_RANGE : TB_CACHE_SHARED);
-        return;
-    }
-    const uint64_t src = a.rows + blockIdx.y * a.pool_stride + row * a.row_stride + off;
-    const uint64_t dst = pools.dst[blockIdx.y] + page * a.page_stride + in_page * a.token_step +
-                         (off / a.head_bytes) * a.head_step + off % a.head_bytes;
-    if constexpr (E == 16)
-        *(gu32x4 *)dst = *(const gu32x4 *)src;
-    else
-        *(gu8 *)dst = *(const gu8 *)src;
 }
 
 hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a,
-                         bool aligned16, hipStream_t stream) {
-    const uint32_t parts = a.heads * a.head_bytes / (aligned16 ? 16 : 1);
-    const dim3 grid((uint32_t)(((uint64_t)a.n * parts + 255) / 256), npools, 1);
-    return launch(aligned16 ? append_kernel<16> : append_kernel<1>, grid, 256, stream, nullptr, pools, s, a, parts);
+                         uint32_t piece, hipStream_t stream) {
+    const uint32_t parts = a.heads * a.head_bytes / piece;
+    const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
+    const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kAppendPools - 1) / kAppendPools, 1);
+    return launch(piece == 16 ? append_kernel<16> : (piece == 4 ? append_kernel<4> : append_kernel<1>), grid, 256, stream, nullptr,
+                  pools, s, a, parts, npools);
 }
 
 // ---- fork ----------------------------------------------------------------------

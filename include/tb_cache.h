@@ -94,7 +94,7 @@ int tb_cache_init(const tb_cache *cache, void *stream);
  * for tb_batched_copy, destinations must be pairwise disjoint and disjoint
  * from every source, else their bytes are unspecified (not checked: the lists
  * are in device memory).  A page number of either list outside its cache is
- * skipped; nothing raises a flag.  n == 0 or npools == 0 is a no-op.  One kernel.
+ * skipped; nothing raises a flag.  n == 0 or npools == 0 is a no-op.
  */
 int tb_page_copy(const tb_cache *dst, const tb_cache *src, const int32_t *dst_pages, const int32_t *src_pages,
                  uint32_t n, void *stream);
@@ -109,7 +109,7 @@ int tb_page_copy(const tb_cache *dst, const tb_cache *src, const int32_t *dst_pa
  * Skipped with a flag: a position at or past the sequence's length or a row
  * at or past nrows (TB_CACHE_RANGE), a page with more than one reference
  * (TB_CACHE_SHARED: another sequence would see the write).  The same position
- * twice gives either row's bytes.  One kernel.
+ * twice gives bytes of either row.
  */
 int tb_page_append(const tb_cache *cache, const void *rows, uint64_t nrows, uint64_t row_stride,
                    uint64_t pool_stride, const int32_t *seqs, const int32_t *positions, const int32_t *index,

@@ -166,6 +166,50 @@ def test_far_too_much_is_asked_for():
     assert c.flags() == 0 and c.table[rows - 1, :5].tolist() == [0, 1, 2, 3, 4] and int(c.counts[0]) == 0
 
 
+@pytest.mark.parametrize("heads,dim,dtype,layout", [(3, 10, torch.bfloat16, "token"), (3, 10, torch.bfloat16, "head"), (2, 7, torch.uint8, "token"),
+                                                    (3, 5, torch.float16, "head"), (4, 4, torch.uint8, "token"), (4, 4, torch.uint8, "head")])
+@pytest.mark.parametrize("pools", [1, 4, 7])
+def test_append_by_every_width(heads, dim, dtype, layout, pools):
+    """Tokens and heads of 16, 4 and fewer bytes, and rows that begin at odd places."""
+    note(f"paged cache, append {heads} x {dim} {dtype} {layout} {pools} pools")
+    require_gpu()
+    from copy_reduce_amd.torch_api import PagedCache
+    pt, n = 3, 8
+    page = (pt, heads, dim) if layout == "token" else (heads, pt, dim)
+    kv = torch.zeros((pools, 6) + page, dtype=dtype, device="cuda")
+    c = PagedCache(kv, pt, 2, 4, layout=layout)
+    c.resize(ints([1]), ints([n]))
+    for shift in (0, 1, 2, 8):
+        flat = torch.randint(1, 100, (shift + pools * (n + 1) * heads * dim,), device="cuda").to(dtype)
+        x = flat[shift:].view(pools, n + 1, heads, dim)
+        kv.zero_()
+        c.append(x, ints([1] * n), ints(list(range(n))), ints([n - i for i in range(n)]))
+        by_token = kv if layout == "token" else kv.transpose(2, 3)
+        for i in range(n):
+            assert torch.equal(by_token[:, int(c.table[1, i // pt]), i % pt], x[:, n - i]), (shift, i)
+        assert int((kv != 0).sum()) == pools * n * heads * dim
+    assert c.flags() == 0
+
+
+def test_append_of_more_pieces_than_a_grid_has_threads():
+    """2^32 and more pieces of 16 bytes: a million tokens of 64 KiB, of few rows, to few positions."""
+    note("paged cache, append of 64 GiB")
+    require_gpu()
+    from copy_reduce_amd.torch_api import PagedCache
+    n, pt = (1 << 20) + 5, 4
+    kv = torch.zeros(1, 3, pt, 256, 128, dtype=torch.bfloat16, device="cuda")
+    c = PagedCache(kv, pt, 1, 3)
+    c.resize(ints([0]), ints([9]))
+    x = torch.randn(1, 9, 256, 128, device="cuda").to(torch.bfloat16)
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos[-9:] = torch.arange(9, dtype=torch.int32, device="cuda")
+    c.append(x, torch.zeros_like(pos), pos, pos)
+    table = c.table[0].tolist()
+    for i in range(9):
+        assert torch.equal(kv[0, table[i // pt], i % pt], x[0, i]), i
+    assert c.flags() == 0
+
+
 def test_shared_pages_are_not_written():
     note("paged cache, append to a shared page")
     from copy_reduce_amd import TB_CACHE_SHARED
