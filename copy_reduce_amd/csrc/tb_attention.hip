@@ -1277,8 +1277,6 @@ hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int c
     g.part_o = reinterpret_cast<float *>(ws + round16(8ull * a.batch) + round16(8 * rows));
     const uint64_t units = (uint64_t)(p.budget != 0 ? p.budget : a.batch) * c.heads;
     const uint64_t grid = p.row_blocks > 1 ? (units + 7) / 8 * 8 * p.row_blocks : units;
-    if (grid > (1u << 30))
-        return hipErrorInvalidValue;
     return a.dtype == TB_BF16 ? launch_type<__bf16>(g, a.head_dim, p.shape, (uint32_t)grid, stream)
                               : launch_type<_Float16>(g, a.head_dim, p.shape, (uint32_t)grid, stream);
 }

@@ -1,5 +1,6 @@
 // tb_cache.cpp -- host half of the paged cache: argument checks and launches.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -23,7 +24,7 @@ uint64_t page_bytes(const tb_cache *c) { return c->page_tokens * token_bytes(c);
 bool pools_ok(const tb_cache *c) {
     if (c == nullptr || c->npools > TB_MAX_POOLS || c->layout > TB_CACHE_HEAD_MAJOR || c->num_pages == 0 ||
         c->num_pages > kMaxPages || c->page_tokens == 0 || c->page_tokens > (1u << 16) || c->heads == 0 ||
-        c->head_bytes == 0 || token_bytes(c) > (1u << 26) || page_bytes(c) > (1u << 30) ||
+        c->heads > (1u << 16) || c->head_bytes == 0 || token_bytes(c) > (1u << 26) || page_bytes(c) > (1u << 30) ||
         c->page_stride < page_bytes(c) || c->page_stride > UINT64_MAX / c->num_pages)
         return false;
     if (c->npools > 0 && c->pools == nullptr)
@@ -251,6 +252,7 @@ int tb_page_compact(const tb_cache *cache, void *stream) {
 static bool attn_sizes_ok(const tb_tree_attn *a, const tb_cache *c) {
     return a != nullptr && c != nullptr && a->batch <= (1u << 16) && a->nodes <= (1u << 12) && c->heads > 0 &&
            a->heads_q > 0 && a->heads_q <= (1u << 10) && a->heads_q % c->heads == 0 &&
+           (uint64_t)a->batch * a->nodes * a->heads_q < (1u << 24) &&   // a workgroup of 256 threads a row at most
            (a->head_dim == 64 || a->head_dim == 96 || a->head_dim == 128 || a->head_dim == 256);
 }
 
@@ -269,7 +271,7 @@ int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64
 
 int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     if (!attn_sizes_ok(a, c) || !pools_ok(c) || !state_ok(c) || a->dtype > TB_FP16 ||
-        c->head_bytes != 2 * a->head_dim || a->k_pool >= c->npools || a->v_pool >= c->npools)
+        !(fabsf(a->scale) <= 1e30f) || c->head_bytes != 2 * a->head_dim || a->k_pool >= c->npools || a->v_pool >= c->npools)
         return TB_ERR_INVALID;
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;

@@ -57,9 +57,10 @@ typedef struct tb_cache {
     uint32_t layout;          /* TB_CACHE_TOKEN_MAJOR or TB_CACHE_HEAD_MAJOR                      */
     uint32_t num_pages;       /* pages of each pool, 1 .. 2^30                                    */
     uint32_t page_tokens;     /* tokens of a page, 1 .. 2^16                                      */
-    uint32_t heads;           /* key/value heads, >= 1                                            */
-    uint32_t head_bytes;      /* bytes of one token's head, >= 1                                  */
-    uint64_t page_stride;     /* bytes between pages, >= page_tokens * heads * head_bytes         */
+    uint32_t heads;           /* key/value heads, 1 .. 2^16                                       */
+    uint32_t head_bytes;      /* bytes of one token's head, >= 1; of a token at most 2^26         */
+    uint64_t page_stride;     /* bytes between pages, >= page_tokens * heads * head_bytes, which is
+                                 at most 2^30                                                      */
     uint32_t max_seqs;        /* rows of the table, >= 1                                          */
     uint32_t max_pages;       /* pages of a row, >= 1; max_pages * page_tokens < 2^31             */
     int32_t *table;           /* device, [max_seqs][max_pages]: a sequence's pages in order; only the
@@ -183,12 +184,12 @@ typedef struct tb_tree_attn {
     const int32_t *seqs;       /* device, [batch]                                                 */
     const uint64_t *mask;      /* device, [batch][nodes][ceil(nodes / 64)], or NULL               */
     const int32_t *tree_nodes; /* device, [batch], or NULL                                        */
-    uint32_t batch, nodes;     /* batch <= 2^16, nodes <= 2^12                                     */
+    uint32_t batch, nodes;     /* batch <= 2^16, nodes <= 2^12, batch * nodes * heads_q < 2^24     */
     uint32_t heads_q;          /* a multiple of cache->heads, at most 2^10                        */
     uint32_t head_dim;         /* 64, 96, 128 or 256; cache->head_bytes = 2 * head_dim            */
     uint32_t dtype;            /* TB_BF16 or TB_FP16, of q, k, v, out and the cache               */
     uint32_t k_pool, v_pool;   /* which pools hold this layer's keys and values                   */
-    float scale;
+    float scale;               /* finite, at most 1e30 either way                                 */
     void *workspace;           /* device, tb_tree_attention_workspace() bytes, 16-byte aligned    */
     uint64_t workspace_bytes;
 } tb_tree_attn;

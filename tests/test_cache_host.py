@@ -90,7 +90,8 @@ def _cache(**kw):
 
 
 BAD_POOLS = [dict(npools=257), dict(layout=2), dict(num_pages=0), dict(num_pages=(1 << 30) + 1), dict(page_tokens=0),
-             dict(page_tokens=(1 << 16) + 1), dict(heads=0), dict(head_bytes=0), dict(pools=None),
+             dict(page_tokens=(1 << 16) + 1), dict(heads=0), dict(head_bytes=0), dict(pools=None), dict(heads=(1 << 16) + 1, head_bytes=1, page_tokens=1, page_stride=1 << 17),
+             dict(head_bytes=1 << 26, page_stride=1 << 33),
              dict(page_stride=16 * 2 * 128 - 1), dict(page_stride=1 << 62)]
 BAD_STATE = [dict(max_seqs=0), dict(max_pages=0), dict(max_pages=1 << 27), dict(table=None), dict(lens=None),
              dict(refs=None), dict(free_list=None), dict(counts=None), dict(scratch=None), dict(scratch=0x6004),
@@ -160,7 +161,9 @@ def _attn(**kw):
                                  dict(tree_nodes=0x8002), dict(heads_q=3), dict(heads_q=0), dict(heads_q=1026),
                                  dict(head_dim=80), dict(head_dim=128), dict(dtype=2), dict(k_pool=2), dict(v_pool=7),
                                  dict(batch=(1 << 16) + 1), dict(nodes=(1 << 12) + 1), dict(q_stride=(1024, 260, 64)),
-                                 dict(v_stride=(1 << 41, 128, 64)), dict(workspace=None), dict(workspace=0x60008)],
+                                 dict(v_stride=(1 << 41, 128, 64)), dict(workspace=None), dict(workspace=0x60008),
+                                 dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-1e31),
+                                 dict(batch=1 << 16, nodes=1 << 6), dict(batch=1 << 12, nodes=1 << 12)],
                          ids=str)
 def test_bad_attention_is_refused(bad):
     assert tb.lib.tb_tree_attention(_attn(**bad), _cache(), None) == tb.TB_ERR_INVALID
@@ -177,6 +180,7 @@ def test_attention_refuses_other_caches_and_takes_nothing_to_do():
     n = ctypes.c_uint64()
     assert tb.lib.tb_tree_attention_workspace(_attn(head_dim=1), _cache(), ctypes.byref(n)) == inv
     assert tb.lib.tb_tree_attention_workspace(_attn(), _cache(), None) == inv
+    assert tb.lib.tb_tree_attention_workspace(_attn(batch=1 << 16, nodes=1 << 6), _cache(), ctypes.byref(n)) == inv
     for nothing in (dict(batch=0), dict(nodes=0)):
         n.value = 7
         assert tb.lib.tb_tree_attention_workspace(_attn(**nothing), _cache(), ctypes.byref(n)) == tb.TB_OK
