@@ -4,8 +4,9 @@
 // The M = nodes * (heads_q / heads) rows of one sequence that read one
 // key/value head share each of its keys, so a key costs M multiply-adds a
 // byte: up to some 200 rows the cache's bytes decide, beyond that the
-// products.  Either way every key and value goes from memory straight into the
-// registers of the one wave (or, for many rows, the few waves) that multiplies it.
+// products.  With up to 16 rows every key and value goes from memory straight into
+// the registers of the one wave that multiplies it; with more, the waves of a
+// workgroup share them through LDS.
 //
 // A wave owns R = 16 NT rows and walks over tiles of 32 keys with a running
 // maximum and sum.  Both products run on 16x16x32 matrix instructions and are
@@ -15,10 +16,11 @@
 //   O' = V' P'  which are just the k-places that lane has to supply of P', so
 //               that the probabilities never leave their lane.  V' wants, for
 //               one element of the head, the values of those eight keys in one
-//               register quad: each lane loads D/16 neighbouring elements of
-//               its eight keys and pairs them up by byte permutes.  The order
-//               in which elements meet the instruction's rows is free: place n
-//               of instruction j is element n D/16 + j.
+//               register quad.  From registers: each lane loads D/16 neighbouring
+//               elements of its eight keys and pairs them up by byte permutes (the
+//               order in which elements meet the instruction's rows is free: place
+//               n of instruction j is element n D/16 + j).  From LDS: two
+//               transposing reads of four keys each, place n being element 16 j + n.
 // The statistics of row n are in the lanes with that n, as is its column of O'.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -184,7 +186,8 @@ struct Place {
 
 // `known`: LDS for a sequence a thread; filled where the batch has no more than that.
 template <int WAVES>
-__device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds, Sequence *known) {
+__device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds,
+        Sequence *known) {
     if (g.budget == 0) {   // one sequence, from its first key to its last
         if (threadIdx.x == 0)
             *out = {0, kWhole, mine};
@@ -214,7 +217,8 @@ __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Pla
     for (int k = 0; k < WAVES; k++)
         total += lds[k];
     const uint64_t units = total / kUnit;
-    const uint64_t share = (units <= 0xffffffffu ? ((uint32_t)units + g.budget - 1) / g.budget : (units + g.budget - 1) / g.budget) * kUnit;
+    const uint64_t share = (units <= 0xffffffffu ? ((uint32_t)units + g.budget - 1) / g.budget
+            : (units + g.budget - 1) / g.budget) * kUnit;
     const uint64_t begin = mine * share;
     uint64_t before = 0;
     for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {
@@ -255,7 +259,8 @@ struct Part {
     bool first, last;
 
     // known: what find_place() left, for up to `room` sequences
-    __device__ __forceinline__ Part(const AttnArgs &g, const Place &at, uint32_t mine, const Sequence *known, uint32_t room) : b(at.batch) {
+    __device__ __forceinline__ Part(const AttnArgs &g, const Place &at, uint32_t mine, const Sequence *known,
+            uint32_t room) : b(at.batch) {
         const Sequence s = g.batch <= room && at.share != kWhole ? known[b] : sequence_of(g, b);
         seq.row = uniform(s.row);
         seq.context = uniform(s.context);
@@ -280,7 +285,8 @@ struct Part {
             splits = 1;
         } else {
             const uint64_t u = at.share / kUnit, a = at.start / kUnit, z = end / kUnit - 1;
-            splits = uniform(z <= 0xffffffffu ? (uint32_t)z / (uint32_t)u - (uint32_t)a / (uint32_t)u + 1 : (uint32_t)(z / u - a / u + 1));
+            splits = uniform(z <= 0xffffffffu ? (uint32_t)z / (uint32_t)u - (uint32_t)a / (uint32_t)u + 1
+                    : (uint32_t)(z / u - a / u + 1));
         }
         slot = mine + b;
     }
@@ -408,7 +414,8 @@ struct Rows {
     // keys(k, x): x[2 e + z] becomes step k + e's operand for keys 16 z .. 16 z + 15, e and z 0 and 1;
     // keep(t, i): whether row t * 16 + n sees the lane's i-th key, asked only if `some` row may not see all.
     template <typename Keys2, typename Keep>
-    __device__ __forceinline__ bool scores(const AttnArgs &g, bool some, Keys2 keys, Keep keep, f32x4 (&s)[NT][2], float (&tops)[NT]) {
+    __device__ __forceinline__ bool scores(const AttnArgs &g, bool some, Keys2 keys, Keep keep, f32x4 (&s)[NT][2],
+            float (&tops)[NT]) {
 #pragma unroll
         for (int t = 0; t < NT; t++)
             s[t][0] = s[t][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -539,7 +546,8 @@ struct Rows {
     // Each lane holds, of row n, runs of RUN neighbouring elements: run i begins at element
     // begin(i), and its element e is value(t, i, e).
     template <int RUN, typename Begin, typename Value>
-    __device__ __forceinline__ void close(const AttnArgs &g, const Part &w, uint32_t head, uint32_t row0, uint32_t lane, Begin begin, Value value) {
+    __device__ __forceinline__ void close(const AttnArgs &g, const Part &w, uint32_t head, uint32_t row0,
+            uint32_t lane, Begin begin, Value value) {
         constexpr int kRuns = 4 * DJ / RUN;
         typedef T tv __attribute__((ext_vector_type(RUN)));
         const uint32_t n = lane & 15, q4 = lane >> 4;
@@ -598,6 +606,14 @@ __device__ __forceinline__ void note_splits(const AttnArgs &g, const Part &w, ui
 // takes every fourth tile and reads its keys and values straight into the registers
 // from which they are multiplied; the next tile's keys are on their way during the
 // second product, its values during the first.
+//
+// 64 sequences of up to 8,191 tokens, 8 heads of 128, 4 rows a head: 1.09 GB of keys and values in 206 us,
+// 5.3 TB/s, where a large copy reaches 6.5 TB/s; every request to memory is of 128 bytes and nothing is read
+// twice.  Pages by token spread a head over slices of 256 bytes, and two heads of the eight take 175 us
+// for theirs where the others take 139, on whichever XCD they run: memory channels, which pages by head
+// (200 us) meet less.  Three waves a SIMD instead of two spill at D = 128 (372 us); more shares, and heads in
+// another order, gain nothing.  A short part is its latencies one after the other, some 10 us: lengths,
+// page numbers, first keys, the join of the waves.
 constexpr int kWaves = 4;
 
 template <typename T, int D>
@@ -616,124 +632,128 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void
     find_place<kWaves>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
-    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end; at.batch++) {
-    const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-    const Part w(g, at, mine, known, 64 * kWaves);
-    at.start = w.end;
-    note_splits(g, w, head, 0);
-    const Keys<kWaves> keys(g, w, head, list);
-    const uint32_t c0 = w.c0, c1 = w.c1;
-    R rows;
-    rows.open(g, keys.b, head, 0, lane);
-    __syncthreads();
+    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end;
+            at.batch++) {
+        const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
+        const Part w(g, at, mine, known, 64 * kWaves);
+        at.start = w.end;
+        note_splits(g, w, head, 0);
+        const Keys<kWaves> keys(g, w, head, list);
+        const uint32_t c0 = w.c0, c1 = w.c1;
+        R rows;
+        rows.open(g, keys.b, head, 0, lane);
+        __syncthreads();
 
-    uint32_t kr[2][KS][4], vr[8][DJ / 2];
-    const auto load_k = [&](uint64_t at0, uint64_t at1) {
+        uint32_t kr[2][KS][4], vr[8][DJ / 2];
+        const auto load_k = [&](uint64_t at0, uint64_t at1) {
 #pragma unroll
-        for (int s = 0; s < KS; s++) {
-            load_dwords<4>(kr[0][s], at0 + s * 64 + q4 * 16);
-            load_dwords<4>(kr[1][s], at1 + s * 64 + q4 * 16);
-        }
-    };
-    // tokens first .. first + 31, those past the chunk its last one
-    const auto load_ctx_k = [&](uint32_t first) {
-        const uint64_t base = reinterpret_cast<uint64_t>(g.k_cache);
-        load_k(base + keys.offset_of(min(first + n, c1 - 1)), base + keys.offset_of(min(first + 16 + n, c1 - 1)));
-    };
-    const auto load_ctx_v = [&](uint32_t first) {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            load_dwords<DJ / 2>(vr[i], reinterpret_cast<uint64_t>(g.v_cache) + n * (2 * DJ) +
-                                           keys.offset_of(min(first + key_of(q4, i), c1 - 1)));
-    };
-    const auto key = [&](int k, V8 *x) {
-#pragma unroll
-        for (int i = 0; i < 4 && k + i / 2 < KS; i++) {
-            const uint32_t *r = kr[i % 2][k + i / 2];
-            x[i] = __builtin_bit_cast(V8, (u32x4){r[0], r[1], r[2], r[3]});
-        }
-    };
-    // element j + e of the lane's D/16 elements of keys 2i and 2i + 1 side by side
-    const auto values = [&](int j, V8 *x) {
-#pragma unroll
-        for (int e = 0; e < R::GJ; e++) {
-            u32x4 y;
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                y[i] = __builtin_amdgcn_perm(vr[2 * i + 1][(j + e) / 2], vr[2 * i][(j + e) / 2],
-                                             (j + e) % 2 == 0 ? 0x05040100u : 0x07060302u);
-            x[e] = __builtin_bit_cast(V8, y);
-        }
-    };
-
-    // the chunk of the context
-    if (c1 > c0 + wk * kTile) {
-        load_ctx_k(c0 + wk * kTile);
-        load_ctx_v(c0 + wk * kTile);
-    }
-    f32x4 score[NT][2];
-    float tops[NT];
-#pragma unroll 1
-    for (uint32_t first = c0 + wk * kTile; first < c1; first += kWaves * kTile) {
-        const uint32_t next = first + kWaves * kTile;
-        const bool some = first + kTile > c1;
-        const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; }, score, tops);
-        if (next < c1)
-            load_ctx_k(next);
-        if (some) {
-            // values of keys past the end meet weights of 0 and have to be finite: 0
+            for (int s = 0; s < KS; s++) {
+                load_dwords<4>(kr[0][s], at0 + s * 64 + q4 * 16);
+                load_dwords<4>(kr[1][s], at1 + s * 64 + q4 * 16);
+            }
+        };
+        // tokens first .. first + 31, those past the chunk its last one
+        const auto load_ctx_k = [&](uint32_t first) {
+            const uint64_t base = reinterpret_cast<uint64_t>(g.k_cache);
+            load_k(base + keys.offset_of(min(first + n, c1 - 1)), base + keys.offset_of(min(first + 16 + n, c1 - 1)));
+        };
+        const auto load_ctx_v = [&](uint32_t first) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
+                load_dwords<DJ / 2>(vr[i], reinterpret_cast<uint64_t>(g.v_cache) + n * (2 * DJ) +
+                                               keys.offset_of(min(first + key_of(q4, i), c1 - 1)));
+        };
+        const auto key = [&](int k, V8 *x) {
 #pragma unroll
-                for (int j = 0; j < DJ / 2; j++)
-                    vr[i][j] = key_of(q4, i) < c1 - first ? vr[i][j] : 0;
-        }
-        if (raise)
-            rows.raise_maxima(g, tops);
-        rows.apply(g, score, values);
-        if (next < c1)
-            load_ctx_v(next);
-    }
-
-    // the drafted nodes, with the sequence's last chunk
-    if (w.last) {
-        const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
-        const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
-        const uint32_t count = keys.count;
-        for (uint32_t first = wk * kTile; first < count; first += kWaves * kTile) {
-            load_k(kb + min(first + n, count - 1) * g.k_stride[1], kb + min(first + 16 + n, count - 1) * g.k_stride[1]);
-            // A value that is not finite would turn a weight of 0 into NaN: here it counts
-            // as 0, and the rows that do see it get it added afterwards.
-            uint32_t wild = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint32_t u = first + key_of(q4, i);
-                load_dwords<DJ / 2>(vr[i], vb + min(u, count - 1) * g.v_stride[1] + n * (2 * DJ));
-#pragma unroll
-                for (int j = 0; j < DJ / 2; j++)
-                    vr[i][j] = tamed<T>(u < count ? vr[i][j] : 0, &wild);
+            for (int i = 0; i < 4 && k + i / 2 < KS; i++) {
+                const uint32_t *r = kr[i % 2][k + i / 2];
+                x[i] = __builtin_bit_cast(V8, (u32x4){r[0], r[1], r[2], r[3]});
             }
-            uint32_t bits[NT];
+        };
+        // element j + e of the lane's D/16 elements of keys 2i and 2i + 1 side by side
+        const auto values = [&](int j, V8 *x) {
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-                bits[t] = keys.seen(t * 16 + n, first);
-            if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, score, tops))
+            for (int e = 0; e < R::GJ; e++) {
+                u32x4 y;
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    y[i] = __builtin_amdgcn_perm(vr[2 * i + 1][(j + e) / 2], vr[2 * i][(j + e) / 2],
+                                                 (j + e) % 2 == 0 ? 0x05040100u : 0x07060302u);
+                x[e] = __builtin_bit_cast(V8, y);
+            }
+        };
+
+        // the chunk of the context
+        if (c1 > c0 + wk * kTile) {
+            load_ctx_k(c0 + wk * kTile);
+            load_ctx_v(c0 + wk * kTile);
+        }
+        f32x4 score[NT][2];
+        float tops[NT];
+#pragma unroll 1
+        for (uint32_t first = c0 + wk * kTile; first < c1; first += kWaves * kTile) {
+            const uint32_t next = first + kWaves * kTile;
+            const bool some = first + kTile > c1;
+            const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
+                    score, tops);
+            if (next < c1)
+                load_ctx_k(next);
+            if (some) {
+                // values of keys past the end meet weights of 0 and have to be finite: 0
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+#pragma unroll
+                    for (int j = 0; j < DJ / 2; j++)
+                        vr[i][j] = key_of(q4, i) < c1 - first ? vr[i][j] : 0;
+            }
+            if (raise)
                 rows.raise_maxima(g, tops);
             rows.apply(g, score, values);
-            if (__any(wild))
-                rows.add_wild(g, vb, first, min(first + kTile, count), bits,
-                              [&](int j, int r) { return (4 * q4 + r) * DJ + j; });
+            if (next < c1)
+                load_ctx_v(next);
         }
-    }
 
-    rows.template join<1, kWaves>(g, merge, wk, lane);
-    if (wk == 0)
-        rows.template close<2 * DJ % 8 == 0 ? 8 : 4>(
-            g, w, head, 0, lane, [&](int i) { return 4 * q4 * DJ + i * (2 * DJ % 8 == 0 ? 8 : 4); },
-            [&](int t, int i, int e) {
-                const int k = i * (2 * DJ % 8 == 0 ? 8 : 4) + e;
-                return rows.o[t][k % DJ][k / DJ];
-            });
+        // the drafted nodes, with the sequence's last chunk
+        if (w.last) {
+            const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
+            const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+            const uint32_t count = keys.count;
+            for (uint32_t first = wk * kTile; first < count; first += kWaves * kTile) {
+                load_k(kb + min(first + n, count - 1) * g.k_stride[1],
+                        kb + min(first + 16 + n, count - 1) * g.k_stride[1]);
+                // A value that is not finite would turn a weight of 0 into NaN: here it counts
+                // as 0, and the rows that do see it get it added afterwards.
+                uint32_t wild = 0;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const uint32_t u = first + key_of(q4, i);
+                    load_dwords<DJ / 2>(vr[i], vb + min(u, count - 1) * g.v_stride[1] + n * (2 * DJ));
+#pragma unroll
+                    for (int j = 0; j < DJ / 2; j++)
+                        vr[i][j] = tamed<T>(u < count ? vr[i][j] : 0, &wild);
+                }
+                uint32_t bits[NT];
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    bits[t] = keys.seen(t * 16 + n, first);
+                if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
+                        score, tops))
+                    rows.raise_maxima(g, tops);
+                rows.apply(g, score, values);
+                if (__any(wild))
+                    rows.add_wild(g, vb, first, min(first + kTile, count), bits,
+                                  [&](int j, int r) { return (4 * q4 + r) * DJ + j; });
+            }
+        }
+
+        rows.template join<1, kWaves>(g, merge, wk, lane);
+        if (wk == 0)
+            rows.template close<2 * DJ % 8 == 0 ? 8 : 4>(
+                g, w, head, 0, lane, [&](int i) { return 4 * q4 * DJ + i * (2 * DJ % 8 == 0 ? 8 : 4); },
+                [&](int t, int i, int e) {
+                    const int k = i * (2 * DJ % 8 == 0 ? 8 : 4) + e;
+                    return rows.o[t][k % DJ][k / DJ];
+                });
     }   // join() left the LDS free
 }
 
@@ -742,9 +762,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void
 // More rows than one wave can hold: eight waves share the keys and values of a
 // workgroup's steps through LDS, WM of them with rows of their own, 8 / WM
 // dividing the step's tiles.  A step of kStep keys comes from memory to one of two
-// LDS buffers while the step before is worked on in the other.  A key's 16-byte pieces are stored at places
-// piece ^ (key % 16), so that neither product's reads, one a column of
-// pieces and one a transposing read of four keys, meet in the banks.
+// LDS buffers while the step before is worked on in the other.  Its pieces lie so that neither
+// product's reads meet in the banks, see place_of_piece().
+//
+// 16 trees of 64 nodes over up to 16,383 tokens, 8 heads of 128, 256 rows a head: 0.59 GB and 147 GFLOP in
+// 202 us, where either alone would take some 100 us.  A turn of the loop, 32 keys by the 256 rows, takes 2,340 cycles;
+// 735 of them are waits for the other waves at the ends of steps, and each wave has 32 matrix instructions, some 100 of
+// the vector unit and 16 exponentials.  Steps of 32 keys cost 2 % more, steps of 128 the same; the waves' priorities
+// make no difference.  The same with 8 nodes, 32 rows a head: 126 us, and 173 with two
+// rows' worth of registers in the kernel for few.
 constexpr int kSharedWaves = 8;
 constexpr int shared_nt(int head_dim) { return head_dim <= 128 ? 2 : 1; }
 // Keys of a step: a tile at least for each wave that divides them, whole pieces for each thread.
@@ -802,246 +828,257 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
     find_place<kSharedWaves>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
-    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end; at.batch++) {
-    const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-    const Part w(g, at, mine, known, kThreads);
-    at.start = w.end;
-    note_splits(g, w, head, block);
-    const Keys<kSharedWaves> keys(g, w, head, list);
-    const uint32_t c0 = w.c0, c1 = w.c1, count = w.seq.nodes;
-    const uint32_t row0 = (block * WM + wm) * 16 * NT;
-    R rows;
-    rows.open(g, keys.b, head, row0, lane);
-    if (threadIdx.x == 0)
-        wild_step = 0;
-    __syncthreads();
+    for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end;
+            at.batch++) {
+        const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
+        const Part w(g, at, mine, known, kThreads);
+        at.start = w.end;
+        note_splits(g, w, head, block);
+        const Keys<kSharedWaves> keys(g, w, head, list);
+        const uint32_t c0 = w.c0, c1 = w.c1, count = w.seq.nodes;
+        const uint32_t row0 = (block * WM + wm) * 16 * NT;
+        R rows;
+        rows.open(g, keys.b, head, row0, lane);
+        if (threadIdx.x == 0)
+            wild_step = 0;
+        __syncthreads();
 
-    // This thread's pieces of a step: place at % kPieces of key at / kPieces, at = i * kThreads + thread.
-    // Each wave's loads go straight to LDS, 64 places in a row.
-    const uint64_t pools_apart = reinterpret_cast<uint64_t>(g.v_cache) - reinterpret_cast<uint64_t>(g.k_cache);
-    // The key of each piece as its page in the list and its place in the page, carried from step to step.
-    const uint32_t head_at = head * g.head_step, page_end = g.page_tokens * g.token_step;
-    const uint32_t pages_on = keys.page_of(kStep), places_on = (kStep - pages_on * g.page_tokens) * g.token_step;
-    uint32_t in_list[kEach], in_page[kEach];
+        // This thread's pieces of a step: place at % kPieces of key at / kPieces, at = i * kThreads + thread.
+        // Each wave's loads go straight to LDS, 64 places in a row.
+        const uint64_t pools_apart = reinterpret_cast<uint64_t>(g.v_cache) - reinterpret_cast<uint64_t>(g.k_cache);
+        // The key of each piece as its page in the list and its place in the page, carried from step to step.
+        const uint32_t head_at = head * g.head_step, page_end = g.page_tokens * g.token_step;
+        const uint32_t pages_on = keys.page_of(kStep), places_on = (kStep - pages_on * g.page_tokens) * g.token_step;
+        uint32_t in_list[kEach], in_page[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; i++) {
-        const uint32_t token = c0 + (i * kThreads + thread) / kPieces, p = keys.page_of(token);
-        in_list[i] = p - keys.p0;
-        in_page[i] = (token - p * g.page_tokens) * g.token_step;
-    }
-    // Called for the part's steps in turn.
-    const auto fetch = [&](uint8_t *to, uint32_t first) {
-        uint32_t place[kEach];
-        const bool whole = keys.listed && first + kStep <= c1;
-        if (whole) {
+        for (int i = 0; i < kEach; i++) {
+            const uint32_t token = c0 + (i * kThreads + thread) / kPieces, p = keys.page_of(token);
+            in_list[i] = p - keys.p0;
+            in_page[i] = (token - p * g.page_tokens) * g.token_step;
+        }
+        // Called for the part's steps in turn.
+        const auto fetch = [&](uint8_t *to, uint32_t first) {
+            uint32_t place[kEach];
+            const bool whole = keys.listed && first + kStep <= c1;
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < kEach; i++) {
+                    place[i] = list[in_list[i]] + in_page[i] + head_at;
+                    const uint32_t next = in_page[i] + places_on;
+                    const bool over = next >= page_end;
+                    in_page[i] = over ? next - page_end : next;
+                    in_list[i] += over ? pages_on + 1 : pages_on;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; i++)
+                    place[i] = keys.place_of(min(first + (i * kThreads + thread) / kPieces, c1 - 1));
+            }
 #pragma unroll
             for (int i = 0; i < kEach; i++) {
-                place[i] = list[in_list[i]] + in_page[i] + head_at;
-                const uint32_t next = in_page[i] + places_on;
-                const bool over = next >= page_end;
-                in_page[i] = over ? next - page_end : next;
-                in_list[i] += over ? pages_on + 1 : pages_on;
+                const uint32_t at = i * kThreads + thread, key = at / kPieces,
+                        piece = piece_at_place<D>(key, at % kPieces);
+                const uint64_t from = reinterpret_cast<uint64_t>(g.k_cache) + (uint64_t)(place[i] + piece) * 16;
+                uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
+                __builtin_amdgcn_global_load_lds((const gvoid *)from, (svoid *)there, 16, 0, kStream);
+                __builtin_amdgcn_global_load_lds((const gvoid *)(from + pools_apart), (svoid *)(there + kBuffer), 16,
+                        0, kStream);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; i++)
-                place[i] = keys.place_of(min(first + (i * kThreads + thread) / kPieces, c1 - 1));
-        }
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const uint32_t at = i * kThreads + thread, key = at / kPieces, piece = piece_at_place<D>(key, at % kPieces);
-            const uint64_t from = reinterpret_cast<uint64_t>(g.k_cache) + (uint64_t)(place[i] + piece) * 16;
-            uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
-            __builtin_amdgcn_global_load_lds((const gvoid *)from, (svoid *)there, 16, 0, kStream);
-            __builtin_amdgcn_global_load_lds((const gvoid *)(from + pools_apart), (svoid *)(there + kBuffer), 16, 0, kStream);
-        }
-    };
-    // A step of the drafted nodes, likewise.
-    const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
-    const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
-    const auto fetch_nodes = [&](uint8_t *to, uint32_t first) {
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const uint32_t at = i * kThreads + thread, key = at / kPieces, piece = piece_at_place<D>(key, at % kPieces);
-            const uint32_t u = min(first + key, count - 1);
-            uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
-            __builtin_amdgcn_global_load_lds((const gvoid *)(kb + u * g.k_stride[1] + piece * 16), (svoid *)there, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const gvoid *)(vb + u * g.v_stride[1] + piece * 16), (svoid *)(there + kBuffer), 16, 0, 0);
-        }
-    };
-    // What follows the context's step before `next`: its next step, or the first of the nodes.
-    const auto fetch_after = [&](uint8_t *to, uint32_t next) {
-        if (next < c1)
-            fetch(to, next);
-        else if (w.last && count > 0)
-            fetch_nodes(to, 0);
-    };
-    const auto buffer_at = [&](uint32_t buffer) { return data + buffer * 2 * kBuffer; };
-    // Waits for the step's loads; values of keys past the end meet weights of 0 and have to be finite: 0.
-    const auto arrived = [&](uint8_t *to, uint32_t left) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (left < kStep) {
-            for (uint32_t at = left * kPieces + thread; at < kStep * kPieces; at += kThreads)
-                *reinterpret_cast<u32x4 *>(to + kBuffer + at * 16) = (u32x4){0, 0, 0, 0};
-            __syncthreads();
-        }
-    };
-
-    // Where this lane reads in a tile.  The reads are in assembly, each group with its own wait: the compiler
-    // does not see that they have nothing to do with the loads on their way to the other buffer, and
-    // would wait for those as well.
-    const uint32_t data_at = (uint32_t)(uintptr_t)(svoid *)data;
-    uint32_t key_at[R::KS], value_at[R::DJ];
-#pragma unroll
-    for (int k = 0; k < R::KS; k++)
-        key_at[k] = (n * kPieces + place_of_piece<D>(n, k * 4 + q4)) * 16;
-#pragma unroll
-    for (int j = 0; j < R::DJ; j++) {
-        const uint32_t row = 4 * q4 + n / 4;
-        value_at[j] = kBuffer + (row * kPieces + place_of_piece<D>(row, 2 * j + (n % 4) / 2)) * 16 + (n & 1) * 8;
-    }
-    uint32_t tile_at = 0;   // of the tile in LDS
-    const auto key = [&](int k, V8 *x) {
-        u32x4 y[4];
-        if (k + 1 < R::KS)
-            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\t"
-                         "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
-                         : "v"(tile_at + key_at[k]), "v"(tile_at + key_at[k + 1 < R::KS ? k + 1 : k]), "n"(16 * D * 2)
-                         : "memory");
-        else
-            asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
-                         : "=&v"(y[0]), "=&v"(y[1])
-                         : "v"(tile_at + key_at[k]), "n"(16 * D * 2)
-                         : "memory");
-#pragma unroll
-        for (int i = 0; i < 4 && k + i / 2 < R::KS; i++)
-            x[i] = __builtin_bit_cast(V8, y[i]);
-    };
-    // Elements 16 j .. 16 j + 15 of the lane group's eight keys, transposed on the way: two reads of four keys.
-    const auto values = [&](int j, V8 *x) {
-        u32x2 y[2 * R::GJ];
-        if constexpr (R::GJ == 4)
-            asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7])
-                         : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "v"(tile_at + value_at[j + R::GJ - 2]),
-                           "v"(tile_at + value_at[j + R::GJ - 1]), "n"(16 * D * 2)
-                         : "memory");
-        else
-            asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
-                         "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
-                         "s_waitcnt lgkmcnt(0)"
-                         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
-                         : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "n"(16 * D * 2)
-                         : "memory");
-#pragma unroll
-        for (int e = 0; e < R::GJ; e++)
-            x[e] = __builtin_bit_cast(V8, (u32x4){y[2 * e].x, y[2 * e].y, y[2 * e + 1].x, y[2 * e + 1].y});
-    };
-    f32x4 score[NT][2];
-    float tops[NT];
-
-    // The part of the context.  Every wave does kTurns tiles of each step, also of the last one, where keys past
-    // the end are masked.  The scores of a tile are had at the end of the turn before its
-    // own, so that the loop has one way out, at its end, for the end and for maxima that have
-    // to be raised alike: with a branch or a break inside, the compiler moves all accumulators in
-    // every turn.  (After the last tile the scores of it are had once more, for nothing.)
-    constexpr uint32_t kTurns = kStep / kTile / WK, kTileBytes = kTile * D * 2;
-    uint32_t buffer = 0;
-    fetch_after(data, c0);
-    if (c0 < c1) {
-        arrived(data, c1 - c0);
-        fetch_after(buffer_at(1), c0 + kStep);
-        uint32_t first = c0, turn = 0;
-        const auto look = [&] {
-            tile_at = uniform(data_at + buffer * 2 * kBuffer + (turn * WK + wk) * kTileBytes);
-            const uint32_t t0 = first + (turn * WK + wk) * kTile;
-            return rows.scores(g, t0 + kTile > c1, key, [&](int, int i) { return t0 + key_of(q4, i) < c1; }, score, tops);
         };
-        bool raise = look();
-        bool more = true;
-        do {
-            if (raise)
-                rows.raise_maxima(g, tops);
-            do {
-                rows.apply(g, score, values);
-                turn++;
-                if (turn == kTurns) {
-                    more = first + kStep < c1;
-                    if (more) {
-                        turn = 0;
-                        buffer ^= 1;
-                        first += kStep;
-                        arrived(buffer_at(buffer), c1 - first);
-                        fetch_after(buffer_at(buffer ^ 1), first + kStep);
-                    } else {
-                        turn = kTurns - 1;
-                    }
-                }
-                raise = look();
-            } while (more && !raise);
-        } while (more);
-        buffer ^= 1;
-    }
-
-    // the drafted nodes, with the sequence's last part
-#pragma unroll 1
-    for (uint32_t first = 0; w.last && first < count; first += kStep, buffer ^= 1) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (first + kStep < count)
-            fetch_nodes(buffer_at(buffer ^ 1), first + kStep);
-        // A value that is not finite would turn a weight of 0 into NaN: here it counts as 0, and
-        // the rows that do see it get it added afterwards.  Nodes past the last count as 0 altogether.
-        uint32_t wild = 0;
-#pragma unroll 1
-        for (uint32_t at = thread; at < kStep * kPieces; at += kThreads) {
-            u32x4 *const place = reinterpret_cast<u32x4 *>(buffer_at(buffer) + kBuffer + at * 16);
-            u32x4 x = {0, 0, 0, 0};
-            if (first + at / kPieces < count) {
-                x = *place;
-                for (int e = 0; e < 4; e++)
-                    x[e] = tamed<T>(x[e], &wild);
-            }
-            *place = x;
-        }
-        if (wild)
-            wild_step = first + 1;
-        __syncthreads();
-        const bool any_wild = wild_step == first + 1;
-#pragma unroll 1
-        for (uint32_t turn = 0; turn < kTurns; turn++) {
-            const uint32_t tile = turn * WK + wk, t0 = first + tile * kTile;
-            if (t0 >= count)
-                break;
-            tile_at = uniform(data_at + buffer * 2 * kBuffer + tile * kTileBytes);
-            uint32_t bits[NT];
+        // A step of the drafted nodes, likewise.
+        const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
+        const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+        const auto fetch_nodes = [&](uint8_t *to, uint32_t first) {
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-                bits[t] = keys.seen(row0 + t * 16 + n, t0);
-            if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; }, score, tops))
-                rows.raise_maxima(g, tops);
-            rows.apply(g, score, values);
-            if (any_wild)
-                rows.add_wild(g, vb, t0, min(t0 + kTile, count), bits, [&](int j, int r) { return 16 * j + 4 * q4 + r; });
-        }
-    }
-    __syncthreads();
+            for (int i = 0; i < kEach; i++) {
+                const uint32_t at = i * kThreads + thread, key = at / kPieces,
+                        piece = piece_at_place<D>(key, at % kPieces);
+                const uint32_t u = min(first + key, count - 1);
+                uint8_t *const there = to + (i * kThreads + wave * 64) * 16;
+                __builtin_amdgcn_global_load_lds((const gvoid *)(kb + u * g.k_stride[1] + piece * 16), (svoid *)there,
+                        16, 0, 0);
+                __builtin_amdgcn_global_load_lds((const gvoid *)(vb + u * g.v_stride[1] + piece * 16),
+                        (svoid *)(there + kBuffer), 16, 0, 0);
+            }
+        };
+        // What follows the context's step before `next`: its next step, or the first of the nodes.
+        const auto fetch_after = [&](uint8_t *to, uint32_t next) {
+            if (next < c1)
+                fetch(to, next);
+            else if (w.last && count > 0)
+                fetch_nodes(to, 0);
+        };
+        const auto buffer_at = [&](uint32_t buffer) { return data + buffer * 2 * kBuffer; };
+        // Waits for the step's loads; values of keys past the end meet weights of 0 and have to be finite: 0.
+        const auto arrived = [&](uint8_t *to, uint32_t left) {
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            if (left < kStep) {
+                for (uint32_t at = left * kPieces + thread; at < kStep * kPieces; at += kThreads)
+                    *reinterpret_cast<u32x4 *>(to + kBuffer + at * 16) = (u32x4){0, 0, 0, 0};
+                __syncthreads();
+            }
+        };
 
-    rows.template join<WM, WK>(g, reinterpret_cast<float *>(data), wave, lane);
-    if (wk == 0)
-        rows.template close<4>(g, w, head, row0, lane, [&](int i) { return 16 * i + 4 * q4; },
-                               [&](int t, int i, int e) { return rows.o[t][i][e]; });
-    __syncthreads();   // before the next part fills the LDS
+        // Where this lane reads in a tile.  The reads are in assembly, each group with its own wait: the compiler
+        // does not see that they have nothing to do with the loads on their way to the other buffer, and
+        // would wait for those as well.
+        const uint32_t data_at = (uint32_t)(uintptr_t)(svoid *)data;
+        uint32_t key_at[R::KS], value_at[R::DJ];
+#pragma unroll
+        for (int k = 0; k < R::KS; k++)
+            key_at[k] = (n * kPieces + place_of_piece<D>(n, k * 4 + q4)) * 16;
+#pragma unroll
+        for (int j = 0; j < R::DJ; j++) {
+            const uint32_t row = 4 * q4 + n / 4;
+            value_at[j] = kBuffer + (row * kPieces + place_of_piece<D>(row, 2 * j + (n % 4) / 2)) * 16 + (n & 1) * 8;
+        }
+        uint32_t tile_at = 0;   // of the tile in LDS
+        const auto key = [&](int k, V8 *x) {
+            u32x4 y[4];
+            if (k + 1 < R::KS)
+                asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\t"
+                             "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+                             : "v"(tile_at + key_at[k]), "v"(tile_at + key_at[k + 1 < R::KS ? k + 1 : k]), "n"(16 * D * 2)
+                             : "memory");
+            else
+                asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(y[0]), "=&v"(y[1])
+                             : "v"(tile_at + key_at[k]), "n"(16 * D * 2)
+                             : "memory");
+#pragma unroll
+            for (int i = 0; i < 4 && k + i / 2 < R::KS; i++)
+                x[i] = __builtin_bit_cast(V8, y[i]);
+        };
+        // Elements 16 j .. 16 j + 15 of the lane group's eight keys, transposed on the way: two reads of four keys.
+        const auto values = [&](int j, V8 *x) {
+            u32x2 y[2 * R::GJ];
+            if constexpr (R::GJ == 4)
+                asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                             "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                             "ds_read_b64_tr_b16 %4, %10\n\tds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                             "ds_read_b64_tr_b16 %6, %11\n\tds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                             "s_waitcnt lgkmcnt(0)"
+                             : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7])
+                             : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "v"(tile_at + value_at[j + R::GJ - 2]),
+                               "v"(tile_at + value_at[j + R::GJ - 1]), "n"(16 * D * 2)
+                             : "memory");
+            else
+                asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                             "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                             "s_waitcnt lgkmcnt(0)"
+                             : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+                             : "v"(tile_at + value_at[j]), "v"(tile_at + value_at[j + 1]), "n"(16 * D * 2)
+                             : "memory");
+#pragma unroll
+            for (int e = 0; e < R::GJ; e++)
+                x[e] = __builtin_bit_cast(V8, (u32x4){y[2 * e].x, y[2 * e].y, y[2 * e + 1].x, y[2 * e + 1].y});
+        };
+        f32x4 score[NT][2];
+        float tops[NT];
+
+        // The part of the context.  Every wave does kTurns tiles of each step, also of the last one, where keys past
+        // the end are masked.  The scores of a tile are had at the end of the turn before its
+        // own, so that the loop has one way out, at its end, for the end and for maxima that have
+        // to be raised alike: with a branch or a break inside, the compiler moves all accumulators in
+        // every turn.  (After the last tile the scores of it are had once more, for nothing.)
+        constexpr uint32_t kTurns = kStep / kTile / WK, kTileBytes = kTile * D * 2;
+        uint32_t buffer = 0;
+        fetch_after(data, c0);
+        if (c0 < c1) {
+            arrived(data, c1 - c0);
+            fetch_after(buffer_at(1), c0 + kStep);
+            uint32_t first = c0, turn = 0;
+            const auto look = [&] {
+                tile_at = uniform(data_at + buffer * 2 * kBuffer + (turn * WK + wk) * kTileBytes);
+                const uint32_t t0 = first + (turn * WK + wk) * kTile;
+                return rows.scores(g, t0 + kTile > c1, key, [&](int, int i) { return t0 + key_of(q4, i) < c1; },
+                        score, tops);
+            };
+            bool raise = look();
+            bool more = true;
+            do {
+                if (raise)
+                    rows.raise_maxima(g, tops);
+                do {
+                    rows.apply(g, score, values);
+                    turn++;
+                    if (turn == kTurns) {
+                        more = first + kStep < c1;
+                        if (more) {
+                            turn = 0;
+                            buffer ^= 1;
+                            first += kStep;
+                            arrived(buffer_at(buffer), c1 - first);
+                            fetch_after(buffer_at(buffer ^ 1), first + kStep);
+                        } else {
+                            turn = kTurns - 1;
+                        }
+                    }
+                    raise = look();
+                } while (more && !raise);
+            } while (more);
+            buffer ^= 1;
+        }
+
+        // the drafted nodes, with the sequence's last part
+#pragma unroll 1
+        for (uint32_t first = 0; w.last && first < count; first += kStep, buffer ^= 1) {
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            if (first + kStep < count)
+                fetch_nodes(buffer_at(buffer ^ 1), first + kStep);
+            // A value that is not finite would turn a weight of 0 into NaN: here it counts as 0, and
+            // the rows that do see it get it added afterwards.  Nodes past the last count as 0 altogether.
+            uint32_t wild = 0;
+#pragma unroll 1
+            for (uint32_t at = thread; at < kStep * kPieces; at += kThreads) {
+                u32x4 *const place = reinterpret_cast<u32x4 *>(buffer_at(buffer) + kBuffer + at * 16);
+                u32x4 x = {0, 0, 0, 0};
+                if (first + at / kPieces < count) {
+                    x = *place;
+                    for (int e = 0; e < 4; e++)
+                        x[e] = tamed<T>(x[e], &wild);
+                }
+                *place = x;
+            }
+            if (wild)
+                wild_step = first + 1;
+            __syncthreads();
+            const bool any_wild = wild_step == first + 1;
+#pragma unroll 1
+            for (uint32_t turn = 0; turn < kTurns; turn++) {
+                const uint32_t tile = turn * WK + wk, t0 = first + tile * kTile;
+                if (t0 >= count)
+                    break;
+                tile_at = uniform(data_at + buffer * 2 * kBuffer + tile * kTileBytes);
+                uint32_t bits[NT];
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    bits[t] = keys.seen(row0 + t * 16 + n, t0);
+                if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
+                        score, tops))
+                    rows.raise_maxima(g, tops);
+                rows.apply(g, score, values);
+                if (any_wild)
+                    rows.add_wild(g, vb, t0, min(t0 + kTile, count), bits,
+                            [&](int j, int r) { return 16 * j + 4 * q4 + r; });
+            }
+        }
+        __syncthreads();
+
+        rows.template join<WM, WK>(g, reinterpret_cast<float *>(data), wave, lane);
+        if (wk == 0)
+            rows.template close<4>(g, w, head, row0, lane, [&](int i) { return 16 * i + 4 * q4; },
+                                   [&](int t, int i, int e) { return rows.o[t][i][e]; });
+        __syncthreads();   // before the next part fills the LDS
     }
 }
 
-// Joins the chunks of sequences that have several: one wave a row.
+// Joins the shares of sequences that have several: one wave a row.  With m the largest of the shares' maxima,
+// l = sum_s exp(m_s - m) l_s and o likewise.  The shares' rows are read once, mostly from the caches that
+// they were written to a moment ago: 32,768 rows of 128 elements, some three shares each, 18 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
     const uint32_t lane = threadIdx.x & 63;
@@ -1107,7 +1144,8 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
         t4 x;
         for (int e = 0; e < 4; e++)
             x[e] = (T)(empty ? 0.f : o[e] / l);
-        *reinterpret_cast<t4 *>(g.out + b * g.out_stride[0] + node * g.out_stride[1] + h * g.out_stride[2] + lane * 8) = x;
+        *reinterpret_cast<t4 *>(g.out + b * g.out_stride[0] + node * g.out_stride[1] + h * g.out_stride[2]
+                + lane * 8) = x;
     }
     if (g.lse != nullptr && lane == 0)
         g.lse[(b * g.nodes + node) * g.heads_q + h] = empty ? -INFINITY : m * g.scale + logf(l);

@@ -91,7 +91,8 @@ hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launc
     parts = parts && dst->layout == TB_CACHE_HEAD_MAJOR;
     g.runs = parts ? dst->heads : 1;
     g.token_bytes = (uint32_t)(parts ? dst->head_bytes : token_bytes(dst));
-    const bool fit = (whole ? page_bytes(dst) : g.token_bytes) % 16 == 0 && pages_aligned(dst, 16) && pages_aligned(src, 16);
+    const bool fit = (whole ? page_bytes(dst) : g.token_bytes) % 16 == 0 && pages_aligned(dst, 16)
+            && pages_aligned(src, 16);
     if (dst->npools == 0) {   // what rides along with the copy has to run all the same; no page is in range
         g.src_pages = g.dst_pages = 0;
         const tbk::Pools none = {};
@@ -143,7 +144,8 @@ int tb_page_copy(const tb_cache *dst, const tb_cache *src, const int32_t *dst_pa
         return TB_ERR_INVALID;
     tbk::PagePairs pairs = {src_pages, dst_pages, nullptr, nullptr, n};
     tbk::LaunchSeq seq;
-    const hipError_t e = for_pools(dst, src, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+    const hipError_t e = for_pools(dst, src, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g,
+            bool fit, bool last) {
         if (last)
             seq.last();
         return tbk::launch_page_copy(pools, np, g, pairs, fit, static_cast<hipStream_t>(stream));
@@ -179,7 +181,8 @@ int tb_page_append(const tb_cache *cache, const void *rows, uint64_t nrows, uint
     a.n = n;
     uint32_t piece = 1;
     for (uint32_t w : {4u, 16u})
-        if (a.head_bytes % w == 0 && pages_aligned(cache, w) && aligned(rows, w) && row_stride % w == 0 && pool_stride % w == 0)
+        if (a.head_bytes % w == 0 && pages_aligned(cache, w) && aligned(rows, w) && row_stride % w == 0
+                && pool_stride % w == 0)
             piece = w;
     const tbk::CacheState s = state_of(cache);
     tbk::LaunchSeq seq;
@@ -213,7 +216,8 @@ int tb_page_fork(const tb_cache *cache, const int32_t *parents, const int32_t *c
     hipError_t e = tbk::launch_fork_plan(s, parents, children, n, st);
     const tbk::PagePairs pairs = {s.w.from, s.w.to, s.w.aux, nullptr, n};
     if (e == hipSuccess)
-        e = for_pools(cache, cache, true, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+        e = for_pools(cache, cache, true, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit,
+                bool last) {
             if (last)
                 seq.last();
             return tbk::launch_fork_copy(pools, np, g, pairs, fit, s, parents, children, n, last, st);
@@ -241,7 +245,8 @@ int tb_page_compact(const tb_cache *cache, void *stream) {
     hipError_t e = tbk::launch_compact_plan(s, st);
     const tbk::PagePairs pairs = {s.w.from, s.w.to, nullptr, s.w.pairs, cache->num_pages / 2};
     if (e == hipSuccess)
-        e = for_pools(cache, cache, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit, bool last) {
+        e = for_pools(cache, cache, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g,
+                bool fit, bool last) {
             if (last)
                 seq.last();
             return tbk::launch_compact_copy(pools, np, g, pairs, fit, s, last, st);
@@ -271,12 +276,14 @@ int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64
 
 int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     if (!attn_sizes_ok(a, c) || !pools_ok(c) || !state_ok(c) || a->dtype > TB_FP16 ||
-        !(fabsf(a->scale) <= 1e30f) || c->head_bytes != 2 * a->head_dim || a->k_pool >= c->npools || a->v_pool >= c->npools)
+        !(fabsf(a->scale) <= 1e30f) || c->head_bytes != 2 * a->head_dim || a->k_pool >= c->npools
+                || a->v_pool >= c->npools)
         return TB_ERR_INVALID;
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;
     if (!aligned(c->pools[a->k_pool], 16) || !aligned(c->pools[a->v_pool], 16) || c->page_stride % 16 != 0 ||
-        c->page_stride * c->num_pages > TB_ATTN_MAX_POOL || a->q == nullptr || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
+        c->page_stride * c->num_pages > TB_ATTN_MAX_POOL || a->q == nullptr || a->k == nullptr || a->v == nullptr
+                || a->out == nullptr || !aligned(a->q, 16) ||
         !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
         !list_ok(a->seqs) || !aligned(a->mask, 8) || !aligned(a->tree_nodes, 4))
         return TB_ERR_INVALID;

@@ -112,7 +112,8 @@ __device__ void compact_apply(const Rider &r, uint32_t block, uint32_t blocks);
 // through the caches, several children reading one page: 192 such pages of 32 KiB in 32 pools in 24 us;
 // nt loads 46 us for the whole call against 34.
 template <int E, int TH, int U, int LD, int ST, int WITH>
-__global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks, Rider rider) {
+__global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks,
+        Rider rider) {
     constexpr uint32_t kBlock = TH * 16 * U;
     if constexpr (WITH != kAlone) {
         if (blockIdx.x == blocks * g.runs) {
@@ -211,7 +212,8 @@ struct Piece<1> {
 // of 1,600 bytes in 16 pools take 18 us by 16 bytes and took 200 by single ones.
 constexpr int kAppendPools = 4;
 template <int E>
-__global__ __launch_bounds__(256) void append_kernel(Pools pools, CacheState s, AppendArgs a, uint32_t parts, uint32_t npools) {
+__global__ __launch_bounds__(256) void append_kernel(Pools pools, CacheState s, AppendArgs a, uint32_t parts,
+        uint32_t npools) {
     typedef typename Piece<E>::T piece;
     typedef __attribute__((address_space(1))) piece gpiece;
     const uint64_t all = (uint64_t)a.n * parts;
@@ -238,7 +240,8 @@ __global__ __launch_bounds__(256) void append_kernel(Pools pools, CacheState s, 
             continue;
         }
         const uint64_t src = a.rows + pool * a.pool_stride + row * a.row_stride + off;
-        const uint64_t dst = page * a.page_stride + in_page * a.token_step + (off / a.head_bytes) * a.head_step + off % a.head_bytes;
+        const uint64_t dst = page * a.page_stride + in_page * a.token_step + (off / a.head_bytes) * a.head_step
+                + off % a.head_bytes;
         piece x[U];
 #pragma unroll
         for (uint32_t u = 0; u < U; u++)
@@ -256,8 +259,8 @@ hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &
     const uint32_t parts = a.heads * a.head_bytes / piece;
     const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
     const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kAppendPools - 1) / kAppendPools, 1);
-    return launch(piece == 16 ? append_kernel<16> : (piece == 4 ? append_kernel<4> : append_kernel<1>), grid, 256, stream, nullptr,
-                  pools, s, a, parts, npools);
+    return launch(piece == 16 ? append_kernel<16> : (piece == 4 ? append_kernel<4> : append_kernel<1>), grid, 256,
+            stream, nullptr, pools, s, a, parts, npools);
 }
 
 // ---- fork ----------------------------------------------------------------------
@@ -373,7 +376,8 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
 // pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have.
 template <int BS>
-__device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i, uint32_t t) {
+__device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i,
+        uint32_t t) {
     const int32_t q = seqs[i], len = lens[i];
     const bool in_range = (uint32_t)q < s.max_seqs && len >= 0 && (uint32_t)len <= s.max_pages * s.page_tokens;
     bool again = false;
@@ -496,7 +500,8 @@ __global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_
     release<256>(s, seqs, lens, blockIdx.x, threadIdx.x);
 }
 
-__global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
+__global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens,
+        uint32_t n) {
     __shared__ uint32_t lds[16];
     __shared__ uint64_t wide[16];
     restack(s, seqs, lens, n, blockIdx.x, *s.w.top, lds, wide);
@@ -515,7 +520,8 @@ __global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *
 }
 
 // A wave an entry.
-__global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const int32_t *seqs, const int32_t *lens, uint32_t n) {
+__global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const int32_t *seqs, const int32_t *lens,
+        uint32_t n) {
     __shared__ uint32_t lds[16];
     __shared__ uint64_t wide[16];
     const uint32_t top = stack_top(s), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -555,7 +561,8 @@ __device__ __forceinline__ uint32_t border_of(const CacheState &s) {
 
 // This thread's four pages of a chunk, as bits: whether page 4 t + k is a hole (free, below the
 // border) and whether it moves (used, at or above it).
-__device__ __forceinline__ void look_at(const CacheState &s, uint32_t chunk, uint32_t live, uint32_t *holes, uint32_t *movers) {
+__device__ __forceinline__ void look_at(const CacheState &s, uint32_t chunk, uint32_t live, uint32_t *holes,
+        uint32_t *movers) {
     typedef int32_t i32x4a __attribute__((ext_vector_type(4), aligned(4)));
     const uint32_t p = chunk * kScanChunk + threadIdx.x * 4;
     int32_t r[4] = {0, 0, 0, 0};
