@@ -335,7 +335,7 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     64)]: bit u % 64 of word u / 64 lets a node see node u (default: node t sees u <= t, so that one node is
     ordinary decoding).  nodes int32 [batch]: how many of the nodes are real (default: all).  scale: 1 /
     sqrt(head_dim) by default.  Returns (out, lse): out as q, lse float32 [batch, nodes, heads_q], the natural
-    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf."""
+    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf.  For serving: there is no gradient."""
     dtype, dev = q.dtype, cache.device
     kind = _ATTN_TYPES.get(dtype)
     if kind is None or cache.dtype != dtype:
@@ -355,6 +355,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     for x, st in ((k, ks), (v, vs)):
         if x.dtype != dtype or x.device != dev or x.shape != kv_shape or st[3] != 1:
             raise ValueError(f"k and v must be {dtype} of shape {kv_shape} on {dev}, head_dim contiguous")
+    if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("tree_attention has no gradient: call it under torch.no_grad(), or detach its inputs")
     sq = _list_arg(seqs, b, dev, "seqs")
     if mask is not None and (mask.dtype != torch.int64 or mask.device != dev or mask.shape != (b, t, (t + 63) // 64)
                              or not mask.is_contiguous()):

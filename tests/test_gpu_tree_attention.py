@@ -415,3 +415,50 @@ def test_refusals():
         tree_attention(q, k, v, c, 0, seqs, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TBError):      # three query heads over two key heads
         tree_attention(q[:, :, :3], k, v, c, 0, seqs)
+
+
+def test_inputs_that_want_a_gradient_are_refused():
+    note("tree attention, gradients")
+    from copy_reduce_amd.torch_api import tree_attention
+    c, m, g = setup([10], heads=2)
+    q, k, v = [x.cuda() for x in inputs(g, 1, 2, 4, 2, 64, torch.bfloat16)]
+    want = tree_attention(q, k, v, c, 0, ints([0]))
+    for x in (q, k, v):
+        x.requires_grad_()
+        with pytest.raises(ValueError):
+            tree_attention(q, k, v, c, 0, ints([0]))
+        with torch.no_grad():
+            got = tree_attention(q, k, v, c, 0, ints([0]))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        x.requires_grad_(False)
+
+
+@pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
+def test_two_graphs_share_a_workspace(room):
+    """Captured apart, of other batches and trees, replayed in turn over growing lengths with eager calls between."""
+    note("tree attention, two graphs with one workspace")
+    from copy_reduce_amd.torch_api import tree_attention, tree_attention_workspace
+    c, m, g = setup([600, 300, 90], heads=2, room=room)
+    small = [x.cuda() for x in inputs(g, 2, 1, 4, 2, 64, torch.bfloat16)]
+    large = [x.cuda() for x in inputs(g, 3, 9, 8, 2, 64, torch.bfloat16)]
+    w = max((tree_attention_workspace(x[0], c) for x in (small, large)), key=lambda t: t.nbytes)
+    calls = [(small, ints([2, 0])), (large, ints([0, 1, 2]))]
+    graphs, outs = [], []
+    for x, seqs in calls:
+        tree_attention(*x, c, 0, seqs, workspace=w)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(tree_attention(*x, c, 0, seqs, workspace=w))
+        graphs.append(graph)
+    for lens in ([1, 0, 90], [600, 300, 90], [257, 128, 31], [600, 1, 0]):
+        c.lens.copy_(ints(lens))
+        for graph in graphs:
+            graph.replay()
+        got = [(o.clone(), l.clone()) for o, l in outs]
+        for (x, seqs), (o, l) in zip(calls, got):
+            eo, el = tree_attention(*x, c, 0, seqs, workspace=w)
+            torch.cuda.synchronize()
+            assert torch.equal(o, eo) and torch.equal(l, el), lens
+        m.lens[:] = lens
+        compare(got[1], attention(m, 0, *[x.cpu() for x in large], [0, 1, 2]), 609, 64, torch.bfloat16, f"lengths {lens}")
