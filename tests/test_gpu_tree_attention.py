@@ -149,6 +149,17 @@ def test_long(dtype):
     run(c, m, q, k, v, [0, 1], what="long")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("dim,pt,layout", [(64, 16, "token"), (96, 20, "head"), (128, 7, "token"), (256, 16, "head"), (128, 128, "head")])
+@pytest.mark.parametrize("nodes,group", [(1, 16), (5, 4), (17, 4), (40, 8)])
+def test_trees_over_several_shares(dim, pt, layout, dtype, nodes, group):
+    """Contexts that several workgroups divide, each part ending anywhere in a page."""
+    note(f"tree attention, {nodes} nodes of {group} rows over shares, dim {dim} pages of {pt} {dtype}")
+    c, m, g = setup([3000, 0, 1501, 7], heads=2, dim=dim, pt=pt, layout=layout, dtype=dtype, seed=nodes + dim, room=8192)
+    q, k, v = inputs(g, 4, nodes, 2 * group, 2, dim, dtype)
+    run(c, m, q, k, v, [0, 1, 2, 3], mask=tree_mask(g, 4, nodes), nodes=[nodes, 1, nodes - nodes // 3, nodes], what="shares")
+
+
 @pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("batch,nodes", [(1, 1), (65, 1), (300, 1), (2, 20), (513, 17)])
 def test_batches(batch, nodes, room):
