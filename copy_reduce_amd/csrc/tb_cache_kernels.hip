@@ -265,8 +265,9 @@ hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &
 
 // ---- fork ----------------------------------------------------------------------
 
-// One workgroup plans the whole call: which entries count, who gets which new
-// page.  from[i], to[i]: the tail's page and its copy's; aux[i]: the length, or
+// One workgroup plans the whole call: which entries count (the first of a child, by a minimum over
+// its entries), who gets which new page (its rank among those that need one, by a sum over the list).  Chains
+// of dependent loads bound it: 3 entries 4 us, 192 entries 5 us.  from[i], to[i]: the tail's page and its copy's; aux[i]: the length, or
 // -1 for an entry that is skipped.
 __global__ __launch_bounds__(1024) void fork_plan_kernel(CacheState s, const int32_t *parents, const int32_t *children,
                                                          uint32_t n) {
@@ -371,7 +372,10 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // ---- resize --------------------------------------------------------------------
 
 // The three steps of a resize.  With many table entries each is a launch of its own, spread over
-// the chip; with few, one workgroup does all three.
+// the chip; with few, one workgroup does all three.  A page's last reference is found by the atomic that takes
+// it away; which pages those were is a set of bits, so that the stack's order does not depend on the order
+// of the atomics.  511 rows of up to 1,000 pages: 12 us of release (its atomics; 128 to 1,024 threads a row, or
+// four pages of a thread at once, change nothing), 6 of restack, 4 of grow.
 
 // Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
 // pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have.
@@ -408,17 +412,21 @@ __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs
     }
 }
 
-// Pushes the released pages of one chunk of kStackWords words of their bits, the highest page
+// Pushes the released pages of one chunk of 1,024 W words of their bits, the highest page
 // first, on a stack that had `top` pages.  The chunks above are counted first; the one
 // with the lowest pages then knows all of them, and deals the new pages.
-constexpr uint32_t kStackWords = 4096;
 // One workgroup does a whole resize up to these limits: a wave takes an entry, 64 pages of its row at
 // a time.  Against the three launches, us a call: 6 rows of 500 tokens 11.2 to 17.9, 16 rows of 8,000
 // (500 pages) 14.4 to 16.4, 32 rows of 2,000 12.1 to 17.1; past the limits 32 rows of 8,000 19.9 to
 // 17.1 and 64 rows of 2,000 17.5 both ways.
+// Words a thread of restack(): with many pages one, over as many workgroups as that makes (half a million
+// pages, 28 us the whole resize; with two 29, with four 32), with few the one workgroup's four.
+constexpr int kFewWords = 4, kManyWords = 1;
 constexpr uint32_t kFewEntries = 32, kFewPages = 512, kFewWork = 8192;
+template <int W>
 __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                                         uint32_t chunk, uint32_t top, uint32_t *lds, uint64_t *wide) {
+    constexpr uint32_t kStackWords = 1024 * W;
     const uint32_t t = threadIdx.x, words = (s.num_pages + 31) / 32;
     uint32_t total, above = 0;
 #pragma unroll 4
@@ -426,17 +434,17 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
         above += (uint32_t)__popc(fresh(&s.w.bits[k]));
     (void)block_sum<1024>(above, &total, lds);
     top += total;
-    // thread t has the words 4 t' .. 4 t' + 3 of the chunk, t' counted from its end
-    uint32_t word[4], count = 0;
-    const uint32_t at0 = chunk * kStackWords + (1023 - t) * 4;
+    // thread t has the words W t' .. W t' + W - 1 of the chunk, t' counted from its end
+    uint32_t word[W], count = 0;
+    const uint32_t at0 = chunk * kStackWords + (1023 - t) * W;
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
+    for (int k = 0; k < W; k++) {
         word[k] = at0 + k < words ? fresh(&s.w.bits[at0 + k]) : 0;
         count += (uint32_t)__popc(word[k]);
     }
     uint32_t at = top + block_sum<1024>(count, &total, lds);
 #pragma unroll
-    for (int k = 3; k >= 0; k--)
+    for (int k = W - 1; k >= 0; k--)
         while (word[k] != 0) {
             const int b = 31 - __clz((int)word[k]);
             word[k] &= ~(1u << b);
@@ -504,7 +512,7 @@ __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32
         uint32_t n) {
     __shared__ uint32_t lds[16];
     __shared__ uint64_t wide[16];
-    restack(s, seqs, lens, n, blockIdx.x, *s.w.top, lds, wide);
+    restack<kManyWords>(s, seqs, lens, n, blockIdx.x, *s.w.top, lds, wide);
 }
 
 // Also clears the bits, which every chunk of restack has read by now.
@@ -528,7 +536,7 @@ __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const in
     for (uint32_t i = wave; i < n; i += 16)
         release<64>(s, seqs, lens, i, lane);
     __syncthreads();
-    restack(s, seqs, lens, n, 0, top, lds, wide);
+    restack<kFewWords>(s, seqs, lens, n, 0, top, lds, wide);
     __syncthreads();
     for (uint32_t i = wave; i < n; i += 16)
         grow<64>(s, seqs, i, lane);
@@ -539,8 +547,8 @@ __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const in
 
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream) {
-    const uint32_t words = (s.num_pages + 31) / 32, chunks = (words + kStackWords - 1) / kStackWords;
-    if (chunks == 1 && n <= kFewEntries && s.max_pages <= kFewPages && (uint64_t)n * s.max_pages <= kFewWork)
+    const uint32_t words = (s.num_pages + 31) / 32, chunks = (words + 1024 * kManyWords - 1) / (1024 * kManyWords);
+    if (words <= 1024 * kFewWords && n <= kFewEntries && s.max_pages <= kFewPages && (uint64_t)n * s.max_pages <= kFewWork)
         return launch(resize_few_kernel, 1, 1024, stream, nullptr, s, seqs, lens, n);
     LaunchSeq seq;
     hipError_t e = launch(release_kernel, n, 256, stream, nullptr, s, seqs, lens);
@@ -581,6 +589,8 @@ __device__ __forceinline__ void look_at(const CacheState &s, uint32_t chunk, uin
     }
 }
 
+// The two sums that rank holes and movers, by chunks: 16 KiB of references a workgroup, read by this kernel
+// and again, from the L2, by the next.  131,072 pages 5 us each.
 __global__ __launch_bounds__(1024) void compact_count_kernel(CacheState s) {
     __shared__ uint32_t lds[16];
     uint32_t holes, movers, total;
