@@ -177,12 +177,24 @@ static hipError_t launch_copy(const Pools &pools, uint32_t npools, const PageSha
     return launch(page_copy_kernel<E, TH, U, LD, ST, WITH>, grid, TH, stream, nullptr, pools, g, pairs, blocks, rider);
 }
 
+// Whole pages, of `run` bytes, alone or with what rides along.  Where a page fills the 512 threads of a
+// workgroup, one load each; smaller ones, whose threads would be idle, go in workgroups of one wave with two
+// loads.  420 MB copied in 64 pools, us by the first and the second: pages of 16 KiB 146 and 155, 8 KiB
+// 162 and 165, 4 KiB 210 and 168, 2 KiB 356 and 166; a compaction of pages of 16, 4 and 2 KiB 161 and 166, 270
+// and 168, 434 and 188.  (64 threads with one load: 152 to 177 and 182 to 190; 128: 150 to 167, 172 to 197.)
+template <int WITH>
+static hipError_t launch_whole(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
+                               const Rider &rider, bool aligned16, hipStream_t stream) {
+    if (!aligned16)
+        return launch_copy<1, 256, 4, 0, 0, WITH>(pools, npools, g, pairs, rider, stream);
+    if ((uint64_t)g.page_tokens * g.token_bytes < 16 * 512)
+        return launch_copy<16, 64, 2, 2, 19, WITH>(pools, npools, g, pairs, rider, stream);
+    return launch_copy<16, 512, 1, 2, 19, WITH>(pools, npools, g, pairs, rider, stream);
+}
+
 hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
                             bool aligned16, hipStream_t stream) {
-    const Rider none = {};
-    if (!aligned16)
-        return launch_copy<1, 256, 4, 0, 0, kAlone>(pools, npools, g, pairs, none, stream);
-    return launch_copy<16, 512, 1, 2, 19, kAlone>(pools, npools, g, pairs, none, stream);
+    return launch_whole<kAlone>(pools, npools, g, pairs, Rider(), aligned16, stream);
 }
 
 // ---- append --------------------------------------------------------------------
@@ -681,8 +693,7 @@ hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream) {
 hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
                                bool aligned16, const CacheState &s, bool apply, hipStream_t stream) {
     const Rider rider = {s, nullptr, nullptr, apply ? 1u : 0u};
-    return aligned16 ? launch_copy<16, 512, 1, 2, 19, kWithCompact>(pools, npools, g, pairs, rider, stream)
-                     : launch_copy<1, 256, 4, 0, 0, kWithCompact>(pools, npools, g, pairs, rider, stream);
+    return launch_whole<kWithCompact>(pools, npools, g, pairs, rider, aligned16, stream);
 }
 
 }  // namespace tbk
