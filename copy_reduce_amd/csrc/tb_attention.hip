@@ -1078,16 +1078,23 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
     }
 }
 
-// Joins the shares of sequences that have several: one wave a row.  With m the largest of the shares' maxima,
+constexpr uint32_t combine_lanes(int head_dim) { return head_dim <= 64 ? 16 : (head_dim <= 128 ? 32 : 64); }
+// From so many rows on a wave has several, a row's lanes go through all of its shares, and the kernel takes fewer rounds
+// of waves; below, its lanes divide the shares.  The whole call by the second and the first way: 32,768 rows, some three
+// shares each, 202 us and 196; 16,384 rows 147 and 145; 8,192 rows 134 either way; 128 rows, 32 shares, 26 and 31.
+constexpr uint32_t kCombineMany = 16384;
+
+// Joins the shares of sequences that have several.  With m the largest of the shares' maxima,
 // l = sum_s exp(m_s - m) l_s and o likewise.  The shares' rows are read once, mostly from the caches that
-// they were written to a moment ago: 32,768 rows of 128 elements, some three shares each, 18 us.
+// they were written to a moment ago: 32,768 rows of 128 elements, some three shares each, 12 us.
 // With many shares the latency of its loads counts, so a few are made at once: for one sequence of 16,383 tokens in
 // 64 shares the whole call takes 30 us, and 35 with one at a time; eight at once cost the trees 4 us.
-template <typename T, int D>
+template <typename T, int D, bool MANY>
 __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
-    const uint32_t lane = threadIdx.x & 63;
-    const uint64_t at = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const uint32_t r = (uint32_t)(at % g.rows), head = (uint32_t)(at / g.rows % g.heads);
+    // kLanes lanes have a row's elements, four each; the other lanes of a wave have other splits, or other rows
+    constexpr uint32_t kLanes = combine_lanes(D), kGroups = MANY ? 1 : 64 / kLanes, kWidth = MANY ? kLanes : 64;
+    const uint32_t lane = threadIdx.x % kWidth, at = blockIdx.x * (256 / kWidth) + threadIdx.x / kWidth;
+    const uint32_t r = at % g.rows, head = at / g.rows % g.heads;
     const uint64_t b = at / g.rows / g.heads;
     if (b >= g.batch)
         return;
@@ -1096,12 +1103,10 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
         return;
     const uint64_t first = (uint64_t)g.split_base[b], step = (uint64_t)g.heads * g.rows;
     const uint64_t slot0 = first * step + (uint64_t)head * g.rows + r;
-    // 64 / kLanes groups of lanes take every so many-th split, kLanes * 4 elements each
-    constexpr uint32_t kLanes = D <= 64 ? 16 : (D <= 128 ? 32 : 64), kGroups = 64 / kLanes;
     const uint32_t part = lane / kLanes, at4 = lane % kLanes * 4;
     float m = -INFINITY, l = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int32_t s0 = 0; s0 < splits; s0 += 64) {   // lane s has split s0 + s's maximum and sum
+    for (int32_t s0 = 0; s0 < splits; s0 += kWidth) {   // lane s has split s0 + s's maximum and sum
         const bool there = s0 + (int32_t)lane < splits;
         float ms = -INFINITY, ls = 0.f;
         if (there) {
@@ -1111,7 +1116,7 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
         }
         float top = fmaxf(ms, m);
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1)
+        for (int d = kWidth / 2; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor(top, d));
         const float base = top == -INFINITY ? 0.f : top * g.scale2;
         const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m, g.scale2, -base));
@@ -1120,10 +1125,10 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
         o *= fade;
         float sum = f * ls;
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1)
+        for (int d = kWidth / 2; d > 0; d >>= 1)
             sum += __shfl_xor(sum, d);
         l = l * fade + sum;
-        const int32_t n = splits - s0 < 64 ? splits - s0 : 64;
+        const int32_t n = min(splits - s0, (int32_t)kWidth);
         // The loads of four splits a group are on their way together; past the last, the last once more.
         constexpr int kLoads = 4;
         for (int32_t i = 0; i < n; i += kLoads * (int32_t)kGroups) {
@@ -1135,15 +1140,15 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
                 x[u] = *(const gf32x4 *)(reinterpret_cast<uint64_t>(g.part_o) + (k * D + min(at4, D - 4u)) * 4);
             }
 #pragma unroll
-            for (int u = 0; u < kLoads; u++) {   // every lane in every turn: all supply their f
+            for (int u = 0; u < kLoads; u++) {   // every lane of the row in every turn: all supply their f
                 const int32_t s = i + u * (int32_t)kGroups + (int32_t)part;
-                const float fs = __shfl(f, s < 64 ? s : 63);
+                const float fs = __shfl(f, min(s, (int32_t)kWidth - 1), kWidth);
                 o += s < n ? x[u] * fs : (f32x4){0.f, 0.f, 0.f, 0.f};
             }
         }
     }
 #pragma unroll
-    for (uint32_t d = kLanes; d < 64; d <<= 1)
+    for (uint32_t d = kLanes; d < kWidth; d <<= 1)
 #pragma unroll
         for (int e = 0; e < 4; e++)
             o[e] += __shfl_xor(o[e], (int)d);
@@ -1257,8 +1262,11 @@ static hipError_t launch_dim(const AttnArgs &g, Shape s, uint32_t grid, hipStrea
     if (e != hipSuccess || g.budget == 0)
         return e;
     seq.last();
-    const uint64_t rows = (uint64_t)g.batch * g.heads * g.rows;
-    return launch(tree_combine_kernel<T, D>, (uint32_t)((rows + 3) / 4), 256, stream, nullptr, g);
+    const uint32_t rows = g.batch * g.heads * g.rows;   // < 2^24
+    constexpr uint32_t kMany = 256 / combine_lanes(D);
+    if (D < 256 && rows >= kCombineMany)
+        return launch(tree_combine_kernel<T, D, D < 256>, (rows + kMany - 1) / kMany, 256, stream, nullptr, g);
+    return launch(tree_combine_kernel<T, D, false>, (rows + 3) / 4, 256, stream, nullptr, g);
 }
 
 template <typename T>

@@ -160,6 +160,16 @@ def test_trees_over_several_shares(dim, pt, layout, dtype, nodes, group):
     run(c, m, q, k, v, [0, 1, 2, 3], mask=tree_mask(g, 4, nodes), nodes=[nodes, 1, nodes - nodes // 3, nodes], what="shares")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_many_rows_that_are_joined(dim, dtype):
+    """16,384 rows and more, some of one share and some of several."""
+    note(f"tree attention, many rows over shares, dim {dim} {dtype}")
+    c, m, g = setup([2000, 0, 700, 7, 130], heads=2, dim=dim, pt=16, dtype=dtype, seed=dim, room=8192)
+    q, k, v = inputs(g, 6, 131, 26, 2, dim, dtype)
+    run(c, m, q, k, v, [0, 1, -1, 2, 3, 4], mask=tree_mask(g, 6, 131), nodes=[131, 90, 131, 131, 0, 64], what="many rows")
+
+
 @pytest.mark.parametrize("room", [0, 8192], ids=["whole", "shares"])
 @pytest.mark.parametrize("batch,nodes", [(1, 1), (65, 1), (300, 1), (2, 20), (513, 17)])
 def test_batches(batch, nodes, room):
