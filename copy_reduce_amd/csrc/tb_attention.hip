@@ -766,7 +766,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void
 // product's reads meet in the banks, see place_of_piece().
 //
 // 16 trees of 64 nodes over up to 16,383 tokens, 8 heads of 128, 256 rows a head: 0.59 GB and 147 GFLOP in
-// 202 us, where either alone would take some 100 us.  A turn of the loop, 32 keys by the 256 rows, takes 2,340 cycles;
+// 198 us, where either alone would take some 100 us.  A turn of the loop, 32 keys by the 256 rows, takes 2,340 cycles;
 // 735 of them are waits for the other waves at the ends of steps, and each wave has 32 matrix instructions, some 100 of
 // the vector unit and 16 exponentials.  Steps of 32 keys cost 2 % more, steps of 128 the same; the waves' priorities
 // make no difference.  The same with 8 nodes, 32 rows a head: 126 us, and 173 with two
