@@ -390,7 +390,8 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // four pages of a thread at once, change nothing), 6 of restack, 4 of grow.
 
 // Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
-// pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have.
+// pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have; aux[i]: the page in which
+// a growing row's present tokens end, -1 if they fill it.
 template <int BS>
 __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i,
         uint32_t t) {
@@ -412,10 +413,12 @@ __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs
         }
         return;
     }
-    const int32_t had = pages_of(length_of(s, q), s.page_tokens), has = pages_of(len, s.page_tokens);
+    const int32_t before = length_of(s, q), had = pages_of(before, s.page_tokens), has = pages_of(len, s.page_tokens);
     if (t == 0) {
         s.w.from[i] = had;
         s.w.to[i] = has;
+        const bool inside = len > before && (uint32_t)before % s.page_tokens != 0;
+        s.w.aux[i] = inside ? s.table[(uint64_t)q * s.max_pages + had - 1] : -1;
     }
     for (int32_t j = has + (int32_t)t; j < had; j += BS) {
         const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
@@ -471,8 +474,16 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
     for (uint32_t i0 = 0; i0 < n; i0 += 1024) {
         const uint32_t i = i0 + t;
         uint64_t need = 0;
-        if (i < n && s.w.from[i] >= 0 && s.w.to[i] > s.w.from[i])
-            need = (uint32_t)(s.w.to[i] - s.w.from[i]);
+        if (i < n && s.w.from[i] >= 0) {
+            // The references are final by now: a row that would grow in a page of another row's, too, stays as it is.
+            const uint32_t page = (uint32_t)s.w.aux[i];
+            if (page < s.num_pages && fresh(&s.refs[page]) > 1) {
+                s.w.from[i] = -1;
+                raise(s, TB_CACHE_SHARED);
+            } else if (s.w.to[i] > s.w.from[i]) {
+                need = (uint32_t)(s.w.to[i] - s.w.from[i]);
+            }
+        }
         const uint64_t before = block_sum<1024>(need, &asked, wide);
         if (i < n)
             s.w.aux[i] = (int32_t)(top - 1 - (uint32_t)(need_all + before));   // used only if there are enough

@@ -292,7 +292,10 @@ class PagedCache:
             _tb_cache.tb_page_fork(self._c, p, c, len(parents), self._stream(stream))
 
     def resize(self, seqs: torch.Tensor, lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
-        """Give the sequences `seqs` the lengths `lens`, 0 freeing one: releases pages, then takes new ones."""
+        """Give the sequences `seqs` the lengths `lens`, 0 freeing one: releases pages, then takes new ones.
+
+        A sequence that was cut back into a page which another one shares cannot grow in it: it is skipped, with
+        TB_CACHE_SHARED.  Fork it to an empty row, whose last page is its own, and go on with that one."""
         q = _list_arg(seqs, None, self.device, "seqs")
         n = _list_arg(lens, len(seqs), self.device, "lens")
         with self._there():

@@ -48,7 +48,8 @@ enum {
     TB_CACHE_RANGE = 2,   /* an entry's sequence, page, position or length was out of range        */
     TB_CACHE_BUSY = 4,    /* a fork's child already holds tokens, or is its own parent             */
     TB_CACHE_TWICE = 8,   /* a sequence came again in one list (the first entry counts)            */
-    TB_CACHE_SHARED = 16  /* an appended token lies in a page that another sequence also refers to */
+    TB_CACHE_SHARED = 16  /* an appended token lies in a page that another sequence also refers to,
+                             or a sequence was to grow in one                                      */
 };
 
 typedef struct tb_cache {
@@ -134,9 +135,15 @@ int tb_page_fork(const tb_cache *cache, const int32_t *parents, const int32_t *c
  * Shrinking releases the pages behind the new end; those that nothing refers
  * to any more are pushed in descending order of their number (the lowest comes
  * off first).  Then growing sequences take their new pages off the stack, in
- * list order and in order of position; with too few, none of them grows
- * (TB_CACHE_SHORT) while the released pages stay released.  Page contents are
- * not touched.  n <= max_seqs.
+ * list order and in order of position; with too few, no sequence that needs one
+ * grows (TB_CACHE_SHORT) while the released pages stay released and the others
+ * get their lengths.  Page contents are not touched.
+ * A sequence whose last page is partly used and, after the call's releases,
+ * referred to by another one as well (it was cut back into a page that a fork
+ * shares) does not grow: the new tokens would be the other's too.  It is
+ * skipped and raises TB_CACHE_SHARED; tb_page_fork to an empty row copies the
+ * used tokens to a page of that row's own, which then can grow.
+ * n <= max_seqs.
  */
 int tb_page_resize(const tb_cache *cache, const int32_t *seqs, const int32_t *lens, uint32_t n, void *stream);
 
