@@ -392,19 +392,24 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
 // pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have; aux[i]: the page in which
 // a growing row's present tokens end, -1 if they fill it.
-template <int BS>
+// CLAIMED: an entry's row came earlier in the list if the row's claim says so, else if one of the earlier entries does.
+template <int BS, bool CLAIMED>
 __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t i,
         uint32_t t) {
     const int32_t q = seqs[i], len = lens[i];
     const bool in_range = (uint32_t)q < s.max_seqs && len >= 0 && (uint32_t)len <= s.max_pages * s.page_tokens;
     bool again = false;
-    if (in_range)
-        for (uint32_t k = t; k < i; k += BS)
-            again |= seqs[k] == q;
-    if constexpr (BS == 64)
-        again = __any(again);
-    else
-        again = __syncthreads_or(again);
+    if constexpr (CLAIMED) {
+        again = in_range && s.w.claim[q] != (int32_t)i;
+    } else {
+        if (in_range)
+            for (uint32_t k = t; k < i; k += BS)
+                again |= seqs[k] == q;
+        if constexpr (BS == 64)
+            again = __any(again);
+        else
+            again = __syncthreads_or(again);
+    }
     if (!in_range || again) {
         if (t == 0) {
             s.w.from[i] = -1;
@@ -474,14 +479,15 @@ __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs
     for (uint32_t i0 = 0; i0 < n; i0 += 1024) {
         const uint32_t i = i0 + t;
         uint64_t need = 0;
-        if (i < n && s.w.from[i] >= 0) {
+        if (i < n) {
+            const int32_t had = s.w.from[i], has = s.w.to[i];
+            const uint32_t page = (uint32_t)s.w.aux[i];   // of an entry that counts
             // The references are final by now: a row that would grow in a page of another row's, too, stays as it is.
-            const uint32_t page = (uint32_t)s.w.aux[i];
-            if (page < s.num_pages && fresh(&s.refs[page]) > 1) {
+            if (had >= 0 && page < s.num_pages && fresh(&s.refs[page]) > 1) {
                 s.w.from[i] = -1;
                 raise(s, TB_CACHE_SHARED);
-            } else if (s.w.to[i] > s.w.from[i]) {
-                need = (uint32_t)(s.w.to[i] - s.w.from[i]);
+            } else if (had >= 0 && has > had) {
+                need = (uint32_t)(has - had);
             }
         }
         const uint64_t before = block_sum<1024>(need, &asked, wide);
@@ -525,10 +531,26 @@ __device__ __forceinline__ uint32_t stack_top(const CacheState &s) {
     return top < 0 ? 0 : min((uint32_t)top, s.num_pages);
 }
 
-__global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_t *seqs, const int32_t *lens) {
+// claim[q]: the first entry of row q, for the rows of a long list.
+__global__ __launch_bounds__(256) void unclaim_kernel(CacheState s, const int32_t *seqs, uint32_t n) {
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256)
+        if ((uint32_t)seqs[i] < s.max_seqs)
+            s.w.claim[seqs[i]] = 0x7fffffff;
+}
+
+__global__ __launch_bounds__(256) void claim_kernel(CacheState s, const int32_t *seqs, uint32_t n) {
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256)
+        if ((uint32_t)seqs[i] < s.max_seqs)
+            atomicMin(&s.w.claim[seqs[i]], (int32_t)i);
+}
+
+template <bool CLAIMED>
+__global__ __launch_bounds__(256) void release_kernel(CacheState s, const int32_t *seqs, const int32_t *lens,
+        uint32_t n) {
     if (blockIdx.x == 0 && threadIdx.x == 0)
         *s.w.top = stack_top(s);   // restack's last chunk writes the new one while others still start
-    release<256>(s, seqs, lens, blockIdx.x, threadIdx.x);
+    for (uint32_t i = blockIdx.x; i < n; i += gridDim.x)
+        release<256, CLAIMED>(s, seqs, lens, i, threadIdx.x);
 }
 
 __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32_t *seqs, const int32_t *lens,
@@ -538,14 +560,15 @@ __global__ __launch_bounds__(1024) void restack_kernel(CacheState s, const int32
     restack<kManyWords>(s, seqs, lens, n, blockIdx.x, *s.w.top, lds, wide);
 }
 
-// Also clears the bits, which every chunk of restack has read by now.
-__global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *seqs, uint32_t n) {
-    if (blockIdx.x < n) {
-        grow<256>(s, seqs, blockIdx.x, threadIdx.x);
+// The first `rows` workgroups.  The others clear the bits, which every chunk of restack has read by now.
+__global__ __launch_bounds__(256) void grow_kernel(CacheState s, const int32_t *seqs, uint32_t n, uint32_t rows) {
+    if (blockIdx.x < rows) {
+        for (uint32_t i = blockIdx.x; i < n; i += rows)
+            grow<256>(s, seqs, i, threadIdx.x);
         return;
     }
     const uint32_t words = (s.num_pages + 31) / 32;
-    for (uint32_t k = (blockIdx.x - n) * 256 + threadIdx.x; k < words; k += (gridDim.x - n) * 256)
+    for (uint32_t k = (blockIdx.x - rows) * 256 + threadIdx.x; k < words; k += (gridDim.x - rows) * 256)
         if (s.w.bits[k] != 0)
             s.w.bits[k] = 0;
 }
@@ -557,7 +580,7 @@ __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const in
     __shared__ uint64_t wide[16];
     const uint32_t top = stack_top(s), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (uint32_t i = wave; i < n; i += 16)
-        release<64>(s, seqs, lens, i, lane);
+        release<64, false>(s, seqs, lens, i, lane);
     __syncthreads();
     restack<kFewWords>(s, seqs, lens, n, 0, top, lds, wide);
     __syncthreads();
@@ -568,18 +591,35 @@ __global__ __launch_bounds__(1024) void resize_few_kernel(CacheState s, const in
             s.w.bits[k] = 0;
 }
 
+// Workgroups of release and grow at most, each then for several entries: a grid holds 2^32 threads, n may be 2^30.
+constexpr uint32_t kMostRows = 1u << 16;
+// Up to so many entries each looks through those before it; past that, where this would grow with the square of the
+// list, two launches more let every row claim its first entry.  Rows of up to 5 pages, us a call by the first and
+// the second: 1,024 entries 16.7 and 22.4, 2,048 21.5 and 24.4, 4,096 33.2 and 34.1, 8,192 60 and 51, 16,384 127 and 86.
+constexpr uint32_t kScanned = 4096;
+
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream) {
     const uint32_t words = (s.num_pages + 31) / 32, chunks = (words + 1024 * kManyWords - 1) / (1024 * kManyWords);
     if (words <= 1024 * kFewWords && n <= kFewEntries && s.max_pages <= kFewPages && (uint64_t)n * s.max_pages <= kFewWork)
         return launch(resize_few_kernel, 1, 1024, stream, nullptr, s, seqs, lens, n);
+    const uint32_t rows = n < kMostRows ? n : kMostRows;
     LaunchSeq seq;
-    hipError_t e = launch(release_kernel, n, 256, stream, nullptr, s, seqs, lens);
+    hipError_t e = hipSuccess;
+    if (n > kScanned) {
+        const uint32_t grid = (uint32_t)(((uint64_t)n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
+        e = launch(unclaim_kernel, grid, 256, stream, nullptr, s, seqs, n);
+        if (e == hipSuccess)
+            e = launch(claim_kernel, grid, 256, stream, nullptr, s, seqs, n);
+    }
+    if (e == hipSuccess)
+        e = launch(n > kScanned ? release_kernel<true> : release_kernel<false>, rows, 256, stream, nullptr, s, seqs,
+                lens, n);
     if (e == hipSuccess)
         e = launch(restack_kernel, chunks, 1024, stream, nullptr, s, seqs, lens, n);
     seq.last();
     if (e == hipSuccess)
-        e = launch(grow_kernel, n + (words + 1023) / 1024, 256, stream, nullptr, s, seqs, n);
+        e = launch(grow_kernel, rows + (words + 1023) / 1024, 256, stream, nullptr, s, seqs, n, rows);
     return e;
 }
 
