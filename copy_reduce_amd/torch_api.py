@@ -17,6 +17,7 @@ from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 from . import _tb, _tb_cache
 
@@ -161,6 +162,19 @@ def _list_arg(t: torch.Tensor, n: Optional[int], device: torch.device, what: str
     return t.data_ptr()
 
 
+def _no_gradient(what: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses tensors whose gradient, or tangent in forward mode, the call would drop."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{what} has no gradient: call it under torch.no_grad(), or detach its tensors")
+    # outside of a level no tensor has a tangent; where torch does not tell the level, each one is asked
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{what} has no forward mode: its tensors must carry no tangent")
+
+
 class PagedCache:
     """A paged key/value cache over tensors (include/tb_cache.h).
 
@@ -191,6 +205,7 @@ class PagedCache:
             if (not p.is_cuda or p.device != p0.device or p.dtype != p0.dtype or p.shape != p0.shape
                     or p.stride() != p0.stride()):
                 raise ValueError("pools must be CUDA tensors of one device, type, shape and stride")
+        _no_gradient("a paged cache", *pools)
         if p0.dim() != 4 or p0.shape[1 if layout == "token" else 2] != page_tokens or not p0[:1].is_contiguous():
             raise ValueError("a pool is [num_pages, page_tokens, heads, head_dim] (layout 'token') or "
                              "[num_pages, heads, page_tokens, head_dim] (layout 'head'), pages contiguous")
@@ -273,6 +288,7 @@ class PagedCache:
                 or (self.heads > 1 and stride[2] != self.head_dim)):
             raise ValueError("rows must be [npools, n, heads, head_dim] of the cache's type and device, "
                              "each token contiguous")
+        _no_gradient("append", rows)
         n = len(seqs)
         q, p = _list_arg(seqs, None, self.device, "seqs"), _list_arg(positions, n, self.device, "positions")
         x = 0 if index is None else _list_arg(index, n, self.device, "index")
@@ -338,7 +354,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     64)]: bit u % 64 of word u / 64 lets a node see node u (default: node t sees u <= t, so that one node is
     ordinary decoding).  nodes int32 [batch]: how many of the nodes are real (default: all).  scale: 1 /
     sqrt(head_dim) by default.  Returns (out, lse): out as q, lse float32 [batch, nodes, heads_q], the natural
-    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf.  For serving: there is no gradient."""
+    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf.  For serving:
+    there is no gradient and no forward mode, and tensors that carry either are refused."""
     dtype, dev = q.dtype, cache.device
     kind = _ATTN_TYPES.get(dtype)
     if kind is None or cache.dtype != dtype:
@@ -358,8 +375,7 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     for x, st in ((k, ks), (v, vs)):
         if x.dtype != dtype or x.device != dev or x.shape != kv_shape or st[3] != 1:
             raise ValueError(f"k and v must be {dtype} of shape {kv_shape} on {dev}, head_dim contiguous")
-    if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
-        raise ValueError("tree_attention has no gradient: call it under torch.no_grad(), or detach its inputs")
+    _no_gradient("tree_attention", q, k, v, cache.pools[2 * layer], cache.pools[2 * layer + 1], out, lse)
     sq = _list_arg(seqs, b, dev, "seqs")
     if mask is not None and (mask.dtype != torch.int64 or mask.device != dev or mask.shape != (b, t, (t + 63) // 64)
                              or not mask.is_contiguous()):

@@ -1,0 +1,40 @@
+"""CPU tests of refusals by the Python side of the paged cache, made before any call of the library."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from copy_reduce_amd.torch_api import tree_attention
+
+
+class Cache:
+    """What tree_attention looks at before it calls the library; the device has none of its kernels."""
+
+    def __init__(self):
+        self.dtype, self.device, self.head_dim, self.heads = torch.bfloat16, torch.device("cpu"), 64, 2
+        self.pools = [torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16) for _ in range(2)]
+
+
+def arguments():
+    q, k, v = [torch.zeros(1, 2, h, 64, dtype=torch.bfloat16) for h in (4, 2, 2)]
+    return Cache(), dict(q=q, k=k, v=v, layer=0, seqs=torch.zeros(1, dtype=torch.int32),
+                         out=torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16), lse=torch.zeros(1, 2, 4))
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "out", "lse", 0, 1])
+def test_a_gradient_is_refused(name):
+    cache, args = arguments()
+    t = cache.pools[name] if isinstance(name, int) else args[name]
+    t.requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        tree_attention(cache=cache, **args)
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("name", ["q", "k", "v", "out", "lse", 0, 1])
+def test_a_tangent_is_refused(name, grad):
+    cache, args = arguments()
+    where = cache.pools if isinstance(name, int) else args
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        where[name] = forward_ad.make_dual(where[name], torch.ones_like(where[name]))
+        with pytest.raises(ValueError, match="no forward mode"):
+            tree_attention(cache=cache, **args)
