@@ -149,8 +149,6 @@ class DescRing:
 
 
 _NO_CONTEXT = nullcontext()
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _list_arg(t: torch.Tensor, n: Optional[int], device: torch.device, what: str) -> int:
@@ -252,11 +250,11 @@ class PagedCache:
 
     def _there(self):
         """The cache's device as the current one, for the length of a call."""
-        return _NO_CONTEXT if _current_device() == self.device.index else torch.cuda.device(self.device)
+        return _NO_CONTEXT if torch._C._cuda_getDevice() == self.device.index else torch.cuda.device(self.device)
 
     def _stream(self, stream: Optional[torch.cuda.Stream]) -> int:
         if stream is None:
-            return _current_raw_stream(self.device.index)
+            return torch._C._cuda_getCurrentRawStream(self.device.index)   # without building a Stream object
         if stream.device != self.device:
             raise ValueError(f"the stream must be one of {self.device}")
         return int(stream.cuda_stream)

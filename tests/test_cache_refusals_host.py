@@ -1,9 +1,25 @@
-"""CPU tests of refusals by the Python side of the paged cache, made before any call of the library."""
+"""CPU tests of refusals by the Python side of the paged cache, made before any call of the library, and of
+what its import needs."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 from copy_reduce_amd.torch_api import tree_attention
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_import_needs_no_gpu_build_of_torch():
+    """A torch without a GPU runtime lacks the functions that ask it for a device and its stream."""
+    code = ("import torch\nfor n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n    delattr(torch._C, n)\n"
+            "import copy_reduce_amd.torch_api as t\nprint(t.PagedCache.state_words(3, 2, 5))")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["22"]
 
 
 class Cache:
