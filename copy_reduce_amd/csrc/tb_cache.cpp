@@ -254,6 +254,26 @@ int tb_page_compact(const tb_cache *cache, void *stream) {
     return e == hipSuccess ? TB_OK : hip_fail(e, "page compact launch");
 }
 
+// Whether rows of `row` elements, laid out in three dimensions, share none: taken from the smallest stride up, each
+// one has to step over all that the smaller ones reach.
+static bool rows_apart(const uint64_t (&stride)[3], const uint32_t (&extent)[3], uint32_t row) {
+    uint64_t reach = row;   // strides are at most 2^40, extents 2^16
+    uint32_t below = 0;     // dimensions taken
+    for (int k = 0; k < 3; k++) {
+        int next = -1;
+        for (int j = 0; j < 3; j++)
+            if (extent[j] > 1 && (below >> j & 1) == 0 && (next < 0 || stride[j] < stride[next]))
+                next = j;
+        if (next < 0)
+            break;
+        if (stride[next] < reach)
+            return false;
+        reach += stride[next] * (extent[next] - 1);
+        below |= 1u << next;
+    }
+    return true;
+}
+
 static bool attn_sizes_ok(const tb_tree_attn *a, const tb_cache *c) {
     return a != nullptr && c != nullptr && a->batch <= (1u << 16) && a->nodes <= (1u << 12) && c->heads > 0 &&
            a->heads_q > 0 && a->heads_q <= (1u << 10) && a->heads_q % c->heads == 0 &&
@@ -299,7 +319,7 @@ int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
             if (stride % 8 != 0 || stride > (1ull << 40))
                 return TB_ERR_INVALID;
     }
-    if (a->workspace == nullptr || !aligned(a->workspace, 16))
+    if (!rows_apart(args.out_stride, extent_q, a->head_dim) || a->workspace == nullptr || !aligned(a->workspace, 16))
         return TB_ERR_INVALID;
     int cus = 0;
     const int rc = tbh::cu_count_of_device(&cus);

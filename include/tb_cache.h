@@ -187,7 +187,9 @@ typedef struct tb_tree_attn {
     void *out;                 /* device, as q                                                    */
     float *lse;                /* device, [batch][nodes][heads_q] contiguous, or NULL             */
     uint64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3]; /* elements between sequences, nodes, heads: */
-                               /* multiples of 8; head_dim itself is contiguous                   */
+                               /* multiples of 8; head_dim itself is contiguous.  Rows of out must
+                                  lie apart: from the smallest stride up, each steps over all that
+                                  the smaller ones reach                                          */
     const int32_t *seqs;       /* device, [batch]                                                 */
     const uint64_t *mask;      /* device, [batch][nodes][ceil(nodes / 64)], or NULL               */
     const int32_t *tree_nodes; /* device, [batch], or NULL                                        */

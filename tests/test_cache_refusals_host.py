@@ -8,7 +8,9 @@ import pytest
 import torch
 from torch.autograd import forward_ad
 
+import copy_reduce_amd as tb
 from copy_reduce_amd.torch_api import tree_attention
+from test_cache_host import _attn, _cache
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -54,3 +56,19 @@ def test_a_tangent_is_refused(name, grad):
         where[name] = forward_ad.make_dual(where[name], torch.ones_like(where[name]))
         with pytest.raises(ValueError, match="no forward mode"):
             tree_attention(cache=cache, **args)
+
+
+@pytest.mark.parametrize("stride,extent", [((1024, 256, 0), (3, 4, 4)), ((1024, 0, 64), (3, 4, 4)), ((0, 256, 64), (3, 4, 4)), ((1024, 256, 56), (3, 4, 4)),
+                                           ((1024, 192, 64), (3, 4, 4)), ((960, 256, 64), (3, 4, 4)), ((256, 64, 64), (3, 4, 4)),
+                                           ((64, 128, 512), (3, 4, 4)), ((0, 0, 64), (2, 1, 4)), ((64, 128, 64), (2, 2, 2))], ids=str)
+def test_rows_of_out_that_overlap_are_refused(stride, extent):
+    b, t, h = extent
+    assert tb.lib.tb_tree_attention(_attn(out_stride=stride, batch=b, nodes=t, heads_q=h), _cache(), None) == tb.TB_ERR_INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not to be followed: needs a machine on which nothing is launched")
+@pytest.mark.parametrize("stride,extent", [((1024, 256, 64), (3, 4, 4)), ((64, 192, 768), (3, 4, 4)), ((4096, 1024, 72), (3, 4, 4)), ((1 << 40, 256, 64), (3, 4, 4)),
+                                           ((0, 256, 64), (1, 4, 4)), ((256, 0, 64), (3, 1, 4)), ((0, 0, 64), (1, 1, 4))], ids=str)
+def test_rows_of_out_that_lie_apart_are_not_refused(stride, extent):
+    b, t, h = extent
+    assert tb.lib.tb_tree_attention(_attn(out_stride=stride, batch=b, nodes=t, heads_q=h), _cache(), None) == tb.TB_ERR_HIP
