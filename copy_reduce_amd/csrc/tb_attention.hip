@@ -216,9 +216,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Pla
     total = 0;
     for (int k = 0; k < WAVES; k++)
         total += lds[k];
-    const uint64_t units = total / kUnit;
-    const uint64_t share = (units <= 0xffffffffu ? ((uint32_t)units + g.budget - 1) / g.budget
-            : (units + g.budget - 1) / g.budget) * kUnit;
+    const uint64_t share = units_of_share(total / kUnit, g.budget) * kUnit;
     const uint64_t begin = mine * share;
     uint64_t before = 0;
     for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {

@@ -125,6 +125,13 @@ hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream);
 hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
                                bool aligned16, const CacheState &s, bool apply, hipStream_t stream);
 
+// The attention's share of a stream of `units`: a `budget`-th, rounded up.  A division of 32 bits where that is enough,
+// as it nearly always is.
+__host__ __device__ inline uint64_t units_of_share(uint64_t units, uint32_t budget) {
+    const uint64_t most = units + budget - 1;
+    return most <= 0xffffffffu ? (uint32_t)most / budget : most / budget;
+}
+
 hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream);
 uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count);
 
