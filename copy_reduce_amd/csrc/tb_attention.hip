@@ -45,7 +45,7 @@ typedef __attribute__((address_space(3))) void svoid;
 constexpr int kTile = 32;              // keys of a tile
 constexpr uint32_t kListPages = 2048;  // page numbers of a chunk kept in LDS
 // A row's maximum is let stand until a score exceeds it by this much (in powers of
-// two): weights then stay below 2^8, well inside every type here, and after the
+// two): weights then stay below 2^8, or 2^15 with kLift, inside every type here, and after the
 // first tiles the accumulators are hardly ever scaled again.
 constexpr float kSlack = 8.f;
 
@@ -81,6 +81,9 @@ struct Mfma<__bf16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
     static constexpr uint32_t kExp = 0x7f80;   // exponent bits, all set where a value is not finite
+    // Weights are taken times 2^kLift, numerator and denominator alike.  fp16 begins to lose bits below 2^-14 and
+    // everything below 2^-25, where many small weights can still count together: seven bits are to spare above.
+    static constexpr float kLift = 0.f;
 };
 template <>
 struct Mfma<_Float16> {
@@ -89,6 +92,7 @@ struct Mfma<_Float16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
     static constexpr uint32_t kExp = 0x7c00;
+    static constexpr float kLift = 7.f;
 };
 
 // Cache policy of the keys and values: nontemporal, each is read by one workgroup (or by few, at
@@ -115,6 +119,12 @@ __device__ __forceinline__ void load_dwords(uint32_t *r, uint64_t at) {
         const u32x2 x = *(const gu32x2 *)at;
         r[0] = x.x, r[1] = x.y;
     }
+}
+
+// Logarithm of the sum of exponentials, of a row's maximum and its sum of lifted weights.
+template <typename T>
+__device__ __forceinline__ float lse_of(float m, float l, float scale) {
+    return m * scale + logf(l * (1.f / (1 << (int)Mfma<T>::kLift)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -363,7 +373,7 @@ struct Rows {
     V8 q[NT][KS];
     f32x4 o[NT][DJ];
     float m[NT], l[NT];                 // l: this lane's keys only, until join()
-    float base[NT];                     // of the exponents: m scaled, 0 while m is -inf
+    float base[NT];                     // of the exponents: m scaled, less the lift; any while m is -inf
 
     // Row r is node r / group of query head head * group + r % group.
     __device__ __forceinline__ void open(const AttnArgs &g, uint32_t b, uint32_t head, uint32_t row0, uint32_t lane) {
@@ -395,9 +405,10 @@ struct Rows {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const float top = fmaxf(lanes_max(tops[t]), m[t]);
-            base[t] = top == -INFINITY ? 0.f : top * g.scale2;
+            const float to = top == -INFINITY ? 0.f : top * g.scale2;
+            base[t] = to - Mfma<T>::kLift;
             // a row's first keys: m = -inf, the factor 0 meets sums that are 0
-            const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -base[t]));
+            const float fade = __builtin_amdgcn_exp2f(__builtin_fmaf(m[t], g.scale2, -to));
             m[t] = top;
             l[t] *= fade;
 #pragma unroll
@@ -585,7 +596,7 @@ struct Rows {
             }
             if (g.lse != nullptr && q4 == 0)
                 g.lse[((uint64_t)w.b * g.nodes + node) * g.heads_q + h] =
-                    empty ? -INFINITY : m[t] * g.scale + logf(l[t]);
+                    empty ? -INFINITY : lse_of<T>(m[t], l[t], g.scale);
         }
     }
 };
@@ -1164,7 +1175,7 @@ __global__ __launch_bounds__(256) void tree_combine_kernel(AttnArgs g) {
                 + lane * 8) = x;
     }
     if (g.lse != nullptr && lane == 0)
-        g.lse[(b * g.nodes + node) * g.heads_q + h] = empty ? -INFINITY : m * g.scale + logf(l);
+        g.lse[(b * g.nodes + node) * g.heads_q + h] = empty ? -INFINITY : lse_of<T>(m, l, g.scale);
 }
 
 // ---- host ----------------------------------------------------------------------

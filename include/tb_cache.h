@@ -179,7 +179,9 @@ enum { TB_BF16 = 0, TB_FP16 = 1 };
  * negative or out of range has no context and no nodes.  Keys and values that
  * a row does not see have no effect on it, whatever they hold.
  * Products are of 16-bit inputs with fp32 sums, softmax statistics and sums are
- * fp32, probabilities are rounded to the element type for the second product.
+ * fp32, probabilities are rounded to the element type for the second product, in
+ * fp16 with steps of 2^-31 of the row's largest or finer, so that the small ones of a long context still
+ * count together.
  */
 typedef struct tb_tree_attn {
     const void *q;             /* device, [batch][nodes][heads_q][head_dim]                       */
