@@ -616,8 +616,8 @@ __device__ __forceinline__ void note_splits(const AttnArgs &g, const Part &w, ui
 // from which they are multiplied; the next tile's keys are on their way during the
 // second product, its values during the first.
 //
-// 64 sequences of up to 8,191 tokens, 8 heads of 128, 4 rows a head: 1.09 GB of keys and values in 206 us,
-// 5.3 TB/s, where a large copy reaches 6.5 TB/s; every request to memory is of 128 bytes and nothing is read
+// 64 sequences of up to 8,191 tokens, 8 heads of 128, 4 rows a head: 1.09 GB of keys and values in 208 us,
+// 5.2 TB/s, where a large copy reaches 6.5 TB/s; every request to memory is of 128 bytes and nothing is read
 // twice.  Pages by token spread a head over slices of 256 bytes, and two heads of the eight take 175 us
 // for theirs where the others take 139, on whichever XCD they run: memory channels, which pages by head
 // (200 us) meet less.  Three waves a SIMD instead of two spill at D = 128 (372 us); more shares, and heads in

@@ -111,6 +111,8 @@ __device__ void compact_apply(const Rider &r, uint32_t block, uint32_t blocks);
 // end only) go in small workgroups, of which those behind the end do nothing, and are loaded
 // through the caches, several children reading one page: 192 such pages of 32 KiB in 32 pools in 24 us;
 // nt loads 46 us for the whole call against 34.
+// E is 16, or 1 where pages (a fork's heads) are no multiple of 16 bytes or do not begin at one: pages of 8,190 bytes
+// take 470 us where those of 8,192 take 163.
 template <int E, int TH, int U, int LD, int ST, int WITH>
 __global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks,
         Rider rider) {
@@ -386,8 +388,9 @@ hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape
 // The three steps of a resize.  With many table entries each is a launch of its own, spread over
 // the chip; with few, one workgroup does all three.  A page's last reference is found by the atomic that takes
 // it away; which pages those were is a set of bits, so that the stack's order does not depend on the order
-// of the atomics.  511 rows of up to 1,000 pages: 12 us of release (its atomics; 128 to 1,024 threads a row, or
-// four pages of a thread at once, change nothing), 6 of restack, 4 of grow.
+// of the atomics.  511 rows of up to 1,000 pages, of which 171 go with 86,000 references: 12.5 us of release (3.8 to
+// where a row's table is read, 5 of taking the references away, 3.7 of setting the bits; 128 to 1,024 threads a
+// row, or four pages of a thread at once, change nothing), 7 of restack, 4.7 of grow.
 
 // Release of entry i by BS threads, a workgroup or a wave, of which this is number t.  from[i]:
 // pages the row had, -1 for an entry that is skipped; to[i]: pages it is to have; aux[i]: the page in which
@@ -432,17 +435,19 @@ __device__ __forceinline__ void release(const CacheState &s, const int32_t *seqs
     }
 }
 
-// Pushes the released pages of one chunk of 1,024 W words of their bits, the highest page
-// first, on a stack that had `top` pages.  The chunks above are counted first; the one
-// with the lowest pages then knows all of them, and deals the new pages.
 // One workgroup does a whole resize up to these limits: a wave takes an entry, 64 pages of its row at
 // a time.  Against the three launches, us a call: 6 rows of 500 tokens 11.2 to 17.9, 16 rows of 8,000
 // (500 pages) 14.4 to 16.4, 32 rows of 2,000 12.1 to 17.1; past the limits 32 rows of 8,000 19.9 to
 // 17.1 and 64 rows of 2,000 17.5 both ways.
-// Words a thread of restack(): with many pages one, over as many workgroups as that makes (half a million
+constexpr uint32_t kFewEntries = 32, kFewPages = 512, kFewWork = 8192;
+
+// Words a thread of restack(): with many pages one, over as many workgroups as that makes (1.2 million
 // pages, 28 us the whole resize; with two 29, with four 32), with few the one workgroup's four.
 constexpr int kFewWords = 4, kManyWords = 1;
-constexpr uint32_t kFewEntries = 32, kFewPages = 512, kFewWork = 8192;
+
+// Pushes the released pages of one chunk of 1,024 W words of their bits, the highest page
+// first, on a stack that had `top` pages.  The chunks above are counted first; the one
+// with the lowest pages then knows all of them, and deals the new pages.
 template <int W>
 __device__ __forceinline__ void restack(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                                         uint32_t chunk, uint32_t top, uint32_t *lds, uint64_t *wide) {

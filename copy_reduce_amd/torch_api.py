@@ -188,7 +188,7 @@ class PagedCache:
     copying `state` keeps the whole bookkeeping.  Index lists are contiguous
     int32 tensors on the cache's device; a negative entry is padding.  Every
     call only enqueues on the current stream of the cache's device, or on `stream`;
-    the caller orders calls on one cache.  What a listed entry asked for and
+    the caller orders calls on one cache (a new one's state is written on the current stream).  What a listed entry asked for and
     could not have shows in counts[1] (TB_CACHE_* bits, see flags())."""
 
     def __init__(self, pools: Union[torch.Tensor, Sequence[torch.Tensor]], page_tokens: int, max_seqs: int,

@@ -23,6 +23,8 @@
  *     entry (a number out of range, say) is skipped and raises a bit of
  *     counts[1]; the rest of the list is still done.  No index makes a kernel
  *     touch memory outside the arrays described here.
+ *   - Index lists, and what a call writes, overlap nothing else that the call
+ *     reads or writes (a list is no part of the cache's own arrays, out is not q).
  *   - A call of several kernels carries the timing hook's start event on its
  *     first kernel and the stop event on its last.
  */
@@ -207,8 +209,9 @@ typedef struct tb_tree_attn {
 
 /*
  * Bytes of workspace a call needs; depends on batch, nodes, heads and head_dim
- * and not on the lengths; 0 for no batch or no nodes.  Only those fields of `attn` and heads of `cache`
- * are read.  Errors: TB_ERR_INVALID; TB_ERR_HIP if the device cannot be queried.
+ * and not on the lengths (room for a share of every sequence beside those of the workgroups: 579 MB for 256
+ * sequences of 64 nodes, 64 query heads of 128 over 8 key heads); 0 for no batch or no nodes.  Only those fields
+ * of `attn` and heads of `cache` are read.  Errors: TB_ERR_INVALID; TB_ERR_HIP if the device cannot be queried.
  */
 int tb_tree_attention_workspace(const tb_tree_attn *attn, const tb_cache *cache, uint64_t *bytes_out);
 
