@@ -1,9 +1,12 @@
 """copy_reduce_amd: the MI355X (gfx950) transfer hot path behind a C ABI.
 
     libtb.so (include/tb.h)      hand-written HIP kernels + host checks
-                                 (include/tb_cache.h: the paged key/value cache)
+                                 (include/tb_cache.h: the paged key/value cache;
+                                 include/tb_serve.h: verification of drafted tokens,
+                                 windows, a cache held in 4 bits)
     copy_reduce_amd._tb          ctypes binding, same names as the C calls
     copy_reduce_amd._tb_cache    the same for tb_cache.h
+    copy_reduce_amd._tb_serve    the same for tb_serve.h
     copy_reduce_amd.torch_api    torch-tensor conveniences (device memory and
                                  streams only; every step runs in libtb)
 
@@ -21,3 +24,4 @@ from ._tb import (  # noqa: F401
 from ._tb_cache import (  # noqa: F401
     TB_CACHE_BUSY, TB_CACHE_RANGE, TB_CACHE_SHARED, TB_CACHE_SHORT, TB_CACHE_TWICE, TB_MAX_POOLS,
 )
+from ._tb_serve import TB_FP4_BLOCK, TB_FP4_HEAD_BYTES, TB_VERIFY_MAX_VOCAB  # noqa: F401

@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libtb.so")
 ARCH = "gfx950"
 
 SOURCES = ["tb_host.cpp", "tb_gen.cpp", "tb_ring.cpp", "tb_kernels.hip",
-           "tb_cache.cpp", "tb_cache_kernels.hip", "tb_attention.hip"]
+           "tb_cache.cpp", "tb_cache_kernels.hip", "tb_attention.hip", "tb_attention_window.hip", "tb_attention_fp4.hip",
+           "tb_serve.cpp", "tb_serve_kernels.hip"]
 # The measuring instruments of bench.py --roofs: a library of their own.
 ROOFS_SOURCES = ["tb_roofs.hip"]
 ROOFS_LIB = os.path.join(PKG, "libtb_roofs.so")

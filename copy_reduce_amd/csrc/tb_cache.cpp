@@ -8,10 +8,12 @@
 #include "tb_cache_internal.h"
 #include "tb_internal.h"
 #include "tb_launch.h"
-
-namespace {
+#include "tb_serve.h"
 
 using tbh::hip_fail;
+
+// Checks that tb_serve.cpp makes as well.
+namespace tbh {
 
 constexpr uint32_t kMaxPages = 1u << 30;
 
@@ -36,7 +38,7 @@ bool pools_ok(const tb_cache *c) {
     return true;
 }
 
-bool sizes_ok(uint32_t num_pages, uint32_t max_seqs) {
+static bool sizes_ok(uint32_t num_pages, uint32_t max_seqs) {
     return num_pages >= 1 && num_pages <= kMaxPages && max_seqs >= 1 && max_seqs <= (1u << 30);
 }
 
@@ -66,6 +68,12 @@ tbk::CacheState state_of(const tb_cache *c) {
     (void)tbk::scratch_words(c->num_pages, c->max_seqs, static_cast<uint32_t *>(c->scratch), &s.w);
     return s;
 }
+
+}  // namespace tbh
+
+namespace {
+
+using namespace tbh;
 
 // Whether every page begins at a multiple of `bytes`.
 bool pages_aligned(const tb_cache *c, uint64_t bytes) {
@@ -281,7 +289,7 @@ static bool attn_sizes_ok(const tb_tree_attn *a, const tb_cache *c) {
            (a->head_dim == 64 || a->head_dim == 96 || a->head_dim == 128 || a->head_dim == 256);
 }
 
-int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64_t *bytes_out) {
+static int attention_workspace(const tb_tree_attn *a, bool fp4, const tb_cache *c, uint64_t *bytes_out) {
     if (bytes_out == nullptr || !attn_sizes_ok(a, c))
         return TB_ERR_INVALID;
     *bytes_out = 0;
@@ -290,22 +298,25 @@ int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64
     int cus = 0;
     const int rc = tbh::cu_count_of_device(&cus);
     if (rc == TB_OK)
-        *bytes_out = tbk::tree_attention_workspace(*a, c->heads, cus);
+        *bytes_out = tbk::tree_attention_workspace(*a, c->heads, fp4, cus);
     return rc;
 }
 
-int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
+static int attention(const tb_tree_attn *a, const tb_attn_view &view, const tb_cache *c, void *stream) {
+    const bool fp4 = view.fp4 != 0;
     if (!attn_sizes_ok(a, c) || !pools_ok(c) || !state_ok(c) || a->dtype > TB_FP16 ||
-        !(fabsf(a->scale) <= 1e30f) || c->head_bytes != 2 * a->head_dim || a->k_pool >= c->npools
-                || a->v_pool >= c->npools)
+        !(fabsf(a->scale) <= 1e30f) || c->head_bytes != (fp4 ? TB_FP4_HEAD_BYTES(a->head_dim) : 2 * a->head_dim)
+                || a->k_pool >= c->npools || a->v_pool >= c->npools)
         return TB_ERR_INVALID;
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;
-    if (!aligned(c->pools[a->k_pool], 16) || !aligned(c->pools[a->v_pool], 16) || c->page_stride % 16 != 0 ||
-        c->page_stride * c->num_pages > TB_ATTN_MAX_POOL || a->q == nullptr || a->k == nullptr || a->v == nullptr
-                || a->out == nullptr || !aligned(a->q, 16) ||
+    const uint64_t piece = fp4 ? 4 : 16;
+    if (!aligned(c->pools[a->k_pool], piece) || !aligned(c->pools[a->v_pool], piece) || c->page_stride % piece != 0 ||
+        c->page_stride * c->num_pages > (fp4 ? TB_ATTN_MAX_POOL_FP4 : TB_ATTN_MAX_POOL) || a->q == nullptr
+                || a->k == nullptr || a->v == nullptr || a->out == nullptr || !aligned(a->q, 16) ||
         !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
-        !list_ok(a->seqs) || !aligned(a->mask, 8) || !aligned(a->tree_nodes, 4))
+        !list_ok(a->seqs) || !aligned(a->mask, 8) || !aligned(a->tree_nodes, 4) || !aligned(view.depths, 4)
+                || (view.window != 0 && a->mask != nullptr && view.depths == nullptr))
         return TB_ERR_INVALID;
     // strides over an extent of one are never used
     tb_tree_attn args = *a;
@@ -325,10 +336,31 @@ int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
     const int rc = tbh::cu_count_of_device(&cus);
     if (rc != TB_OK)
         return rc;
-    if (a->workspace_bytes < tbk::tree_attention_workspace(args, c->heads, cus))
+    if (a->workspace_bytes < tbk::tree_attention_workspace(args, c->heads, fp4, cus))
         return TB_ERR_INVALID;
-    const hipError_t e = tbk::launch_tree_attention(args, *c, cus, static_cast<hipStream_t>(stream));
+    const hipError_t e = tbk::launch_tree_attention(args, view, *c, cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? TB_OK : hip_fail(e, "tree attention launch");
+}
+
+int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64_t *bytes_out) {
+    return attention_workspace(a, false, c, bytes_out);
+}
+
+int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
+    return attention(a, tb_attn_view{0, 0, nullptr, 0}, c, stream);
+}
+
+int tb_view_attention_workspace(const tb_tree_attn *a, const tb_attn_view *view, const tb_cache *c,
+                                uint64_t *bytes_out) {
+    if (view == nullptr || view->fp4 > 1)
+        return TB_ERR_INVALID;
+    return attention_workspace(a, view->fp4 != 0, c, bytes_out);
+}
+
+int tb_view_attention(const tb_tree_attn *a, const tb_attn_view *view, const tb_cache *c, void *stream) {
+    if (view == nullptr || view->fp4 > 1)
+        return TB_ERR_INVALID;
+    return attention(a, *view, c, stream);
 }
 
 }  // extern "C"

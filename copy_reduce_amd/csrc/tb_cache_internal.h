@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "tb_cache.h"
+#include "tb_serve.h"
 
 namespace tbk {
 
@@ -132,7 +133,47 @@ __host__ __device__ inline uint64_t units_of_share(uint64_t units, uint32_t budg
     return most <= 0xffffffffu ? (uint32_t)most / budget : most / budget;
 }
 
-hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_cache &c, int cu_count, hipStream_t stream);
-uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count);
+hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_attn_view &view, const tb_cache &c, int cu_count,
+                                 hipStream_t stream);
+uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, bool fp4, int cu_count);
+
+// Tokens in 4 bits: rows of dim elements a head, rounded to the cache's or read from it.
+struct Fp4Args {
+    const int32_t *seqs;
+    const int32_t *positions;
+    const int32_t *index;
+    uint64_t rows;         // of 16 bits
+    uint64_t nrows;
+    uint64_t row_stride;
+    uint64_t pool_stride;
+    uint64_t page_stride;
+    uint64_t head_step;    // bytes between a token's heads
+    uint64_t token_step;   // and between a page's tokens
+    uint32_t heads;
+    uint32_t dim;
+    uint32_t n;
+};
+hipError_t launch_fp4_append(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
+                             uint32_t dtype, hipStream_t stream);
+hipError_t launch_fp4_read(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
+                           uint32_t dtype, hipStream_t stream);
+// The bytes of tokens, back out of their pages: the way of launch_append, rows being written.
+hipError_t launch_read(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a,
+                       uint32_t piece, hipStream_t stream);
+
+uint64_t verify_workspace(uint32_t batch, uint32_t vocab);
+hipError_t launch_verify(const tb_verify &v, hipStream_t stream);
 
 }  // namespace tbk
+
+namespace tbh {
+
+// tb_cache.cpp: the pools and the shape of a page; the bookkeeping; an index list.
+bool aligned(const void *p, uint64_t to);
+uint64_t token_bytes(const tb_cache *c);
+bool pools_ok(const tb_cache *c);
+bool state_ok(const tb_cache *c);
+bool list_ok(const int32_t *p);
+tbk::CacheState state_of(const tb_cache *c);
+
+}  // namespace tbh

@@ -8,18 +8,20 @@ host memory and streams; every step of the path runs in libtb.
     batched_copy     tb_batched_copy on a device descriptor tensor
     DescRing         tb_ring_* (descriptor-slot ring) over host descriptor arrays
     PagedCache       a paged key/value cache: tb_page_* over tensors
-    tree_attention   tb_tree_attention of drafted tokens over a PagedCache
+    tree_attention   tb_tree_attention of drafted tokens over a PagedCache, or over
+                     a window of it (tb_view_attention)
+    verify_drafts    tb_verify_drafts: which of the drafted tokens hold, and the next one
 """
 import ctypes
 import math
 from contextlib import nullcontext
-from typing import List, Optional, Sequence, Tuple, Union
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
 from torch.autograd import forward_ad
 
-from . import _tb, _tb_cache
+from . import _tb, _tb_cache, _tb_serve
 
 
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -173,6 +175,17 @@ def _no_gradient(what: str, *tensors: Optional[torch.Tensor]) -> None:
                 raise ValueError(f"{what} has no forward mode: its tensors must carry no tangent")
 
 
+_ATTN_TYPES = {torch.bfloat16: _tb_cache.TB_BF16, torch.float16: _tb_cache.TB_FP16}
+
+
+def fp4_head_bytes(head_dim: int) -> int:
+    """Bytes of a head of head_dim elements in a cache held in 4 bits: half a byte an element, one for each 32 of
+    them, rounded up to a multiple of 4."""
+    if head_dim < 32 or head_dim % 32 != 0:
+        raise ValueError("a head held in 4 bits has a multiple of 32 elements")
+    return _tb_serve.TB_FP4_HEAD_BYTES(head_dim)
+
+
 class PagedCache:
     """A paged key/value cache over tensors (include/tb_cache.h).
 
@@ -183,6 +196,10 @@ class PagedCache:
     max_seqs     rows of the table, each of max_pages pages
     state        an int32 tensor of state_words() words with a state to go on
                  from; by default a new one, empty
+    fp4          torch.bfloat16 or torch.float16: the pools are uint8, head_dim
+                 being fp4_head_bytes() of the elements, and hold elements of that
+                 type in 4 bits (include/tb_serve.h): append() rounds, read() and
+                 tree_attention() give back what is held.  All else is alike.
 
     table, lens, refs, free_list and counts are views of `state`, on the device:
     copying `state` keeps the whole bookkeeping.  Index lists are contiguous
@@ -192,7 +209,8 @@ class PagedCache:
     could not have shows in counts[1] (TB_CACHE_* bits, see flags())."""
 
     def __init__(self, pools: Union[torch.Tensor, Sequence[torch.Tensor]], page_tokens: int, max_seqs: int,
-                 max_pages: int, layout: str = "token", state: Optional[torch.Tensor] = None):
+                 max_pages: int, layout: str = "token", state: Optional[torch.Tensor] = None,
+                 fp4: Optional[torch.dtype] = None):
         if layout not in ("token", "head"):
             raise ValueError("layout must be 'token' or 'head'")
         pools = list(pools)   # of a tensor: its pools
@@ -209,10 +227,22 @@ class PagedCache:
                              "[num_pages, heads, page_tokens, head_dim] (layout 'head'), pages contiguous")
         self.pools, self.layout, self.page_tokens = pools, layout, page_tokens
         self.num_pages, self.head_dim = p0.shape[0], p0.shape[3]
+        if fp4 is not None:
+            dim = p0.shape[3] // 17 * 32   # 17 bytes for 32 elements, and up to 3
+            if (fp4 not in _ATTN_TYPES or p0.dtype != torch.uint8 or dim == 0
+                    or _tb_serve.TB_FP4_HEAD_BYTES(dim) != p0.shape[3]):
+                raise ValueError("a cache held in 4 bits has uint8 pools with fp4_head_bytes(head_dim) bytes a head, "
+                                 "and fp4 is bfloat16 or float16")
+            if any(p.data_ptr() % 4 or (p.shape[0] > 1 and p.stride(0) % 4) for p in pools):
+                raise ValueError("pools held in 4 bits begin, and their pages lie, at multiples of 4 bytes")
         self.heads = p0.shape[2 if layout == "token" else 1]
         self.max_seqs, self.max_pages = max_seqs, max_pages
         self.device, self.dtype = p0.device, p0.dtype
         page = page_tokens * self.heads * self.head_dim
+        head_bytes = self.head_dim * p0.element_size()
+        self.fp4 = fp4
+        if fp4 is not None:
+            self.head_dim, self.dtype = dim, fp4
         words = self.state_words(self.num_pages, max_seqs, max_pages)
         fresh = state is None
         if fresh:
@@ -233,7 +263,7 @@ class PagedCache:
         c.npools, c.num_pages, c.page_tokens, c.heads = len(pools), self.num_pages, page_tokens, self.heads
         c.layout = _tb_cache.TB_CACHE_TOKEN_MAJOR if layout == "token" else _tb_cache.TB_CACHE_HEAD_MAJOR
         size = p0.element_size()
-        c.head_bytes = self.head_dim * size
+        c.head_bytes = head_bytes
         c.page_stride = (p0.stride(0) if self.num_pages > 1 else page) * size
         c.max_seqs, c.max_pages = max_seqs, max_pages
         c.table, c.lens, c.refs = self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr()
@@ -270,7 +300,7 @@ class PagedCache:
                    stream: Optional[torch.cuda.Stream] = None) -> None:
         """Copy src's pages src_pages (of this cache by default) to dst_pages, in every pool."""
         src = self if src is None else src
-        if src.device != self.device or src.dtype != self.dtype:
+        if src.device != self.device or src.dtype != self.dtype or src.fp4 != self.fp4:
             raise ValueError("both caches must be of one device and type")
         d = _list_arg(dst_pages, None, self.device, "dst_pages")
         s = _list_arg(src_pages, len(dst_pages), self.device, "src_pages")
@@ -279,7 +309,9 @@ class PagedCache:
 
     def append(self, rows: torch.Tensor, seqs: torch.Tensor, positions: torch.Tensor,
                index: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
-        """Write rows[:, index[i]] ([npools, n, heads, head_dim]) to position positions[i] of sequence seqs[i]."""
+        """Write rows[:, index[i]] ([npools, n, heads, head_dim]) to position positions[i] of sequence seqs[i].
+        A cache held in 4 bits takes rows of its type and rounds them: each 32 elements of a head to a common power
+        of two times 0, 0.5, 1, 1.5, 2, 3, 4 or 6, either sign."""
         shape, stride = rows.shape, rows.stride()
         if (rows.dtype != self.dtype or rows.device != self.device or len(shape) != 4 or shape[0] != len(self.pools)
                 or shape[2] != self.heads or shape[3] != self.head_dim or stride[3] != 1
@@ -295,8 +327,46 @@ class PagedCache:
         size = rows.element_size()
         step = stride[1] if shape[1] > 1 else self.heads * self.head_dim
         with self._there():
-            _tb_cache.tb_page_append(self._c, rows.data_ptr(), shape[1], step * size, stride[0] * size, q, p, x, n,
-                                     self._stream(stream))
+            if self.fp4 is None:
+                _tb_cache.tb_page_append(self._c, rows.data_ptr(), shape[1], step * size, stride[0] * size, q, p, x,
+                                         n, self._stream(stream))
+            else:
+                _tb_serve.tb_fp4_append(self._c, _ATTN_TYPES[self.fp4], self.head_dim, rows.data_ptr(), shape[1],
+                                        step * size, stride[0] * size, q, p, x, n, self._stream(stream))
+
+    def read(self, seqs: torch.Tensor, positions: torch.Tensor, layer: Optional[int] = None,
+             out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """What position positions[i] of sequence seqs[i] holds: [npools, n, heads, head_dim], or with `layer` the two
+        pools of that layer.  append()'s way back; a cache held in 4 bits gives the numbers that it holds.
+        A negative sequence reads as zeros, and so does what is out of range, with TB_CACHE_RANGE."""
+        n = len(seqs)
+        q, p = _list_arg(seqs, None, self.device, "seqs"), _list_arg(positions, n, self.device, "positions")
+        if layer is None:
+            first, count = 0, len(self.pools)
+        elif 0 <= layer < len(self.pools) // 2:
+            first, count = 2 * layer, 2
+        else:
+            raise ValueError("the cache has no such layer")
+        shape = (count, n, self.heads, self.head_dim)
+        if out is not None:
+            st = out.stride()
+            if (out.dtype != self.dtype or out.device != self.device or out.shape != shape or st[3] != 1
+                    or (self.heads > 1 and st[2] != self.head_dim)):
+                raise ValueError(f"out must be {self.dtype} of shape {shape} on {self.device}, each token contiguous")
+            _no_gradient("read", out)
+        with self._there(), _NO_CONTEXT if stream is None else torch.cuda.stream(stream):
+            if out is None:   # it belongs to the stream that the call runs on
+                out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            size = out.element_size()
+            row = self.heads * self.head_dim
+            step = (out.stride(1) if n > 1 else row) * size
+            apart = (out.stride(0) if count > 1 else n * row) * size
+            if self.fp4 is None:
+                _tb_serve.tb_page_read(self._c, first, count, out.data_ptr(), step, apart, q, p, n, self._stream(stream))
+            else:
+                _tb_serve.tb_fp4_read(self._c, _ATTN_TYPES[self.fp4], self.head_dim, first, count, out.data_ptr(),
+                                      step, apart, q, p, n, self._stream(stream))
+        return out
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Make the empty sequences `children` copies of `parents`, sharing their full pages."""
@@ -327,16 +397,16 @@ class PagedCache:
             _tb_cache.tb_page_compact(self._c, self._stream(stream))
 
 
-_ATTN_TYPES = {torch.bfloat16: _tb_cache.TB_BF16, torch.float16: _tb_cache.TB_FP16}
-
-
 def tree_attention_workspace(q: torch.Tensor, cache: PagedCache) -> torch.Tensor:
     """Workspace for tree_attention calls with queries of q's shape over `cache`, whatever the lengths.
     One serves any number of calls that follow each other; calls that can overlap need one each."""
     a = _tb_cache.tb_tree_attn()
     a.batch, a.nodes, a.heads_q, a.head_dim = q.shape
     with cache._there():
-        n = _tb_cache.tb_tree_attention_workspace(a, cache._c)
+        if cache.fp4 is None:
+            n = _tb_cache.tb_tree_attention_workspace(a, cache._c)
+        else:
+            n = _tb_serve.tb_view_attention_workspace(a, _tb_serve.tb_attn_view(fp4=1), cache._c)
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
@@ -344,7 +414,8 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
                    seqs: torch.Tensor, mask: Optional[torch.Tensor] = None, nodes: Optional[torch.Tensor] = None,
                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                   stream: Optional[torch.cuda.Stream] = None, window: Optional[int] = None, sinks: int = 0,
+                   depths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of drafted tokens over the cache's context of `layer` and over each other.
 
     q [batch, nodes, heads_q, head_dim]; k, v [batch, nodes, heads, head_dim] of the drafted tokens, which are
@@ -352,8 +423,15 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
     64)]: bit u % 64 of word u / 64 lets a node see node u (default: node t sees u <= t, so that one node is
     ordinary decoding).  nodes int32 [batch]: how many of the nodes are real (default: all).  scale: 1 /
     sqrt(head_dim) by default.  Returns (out, lse): out as q, lse float32 [batch, nodes, heads_q], the natural
-    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf.  For serving:
-    there is no gradient and no forward mode, and tensors that carry either are refused."""
+    logarithm of the sum of exponentials; a row that sees nothing is 0 and -inf.
+
+    window: a node sees what lies less than `window` positions before its own (1: itself only), and the first `sinks`
+    tokens of the sequence; its position is the sequence's length plus its depth.  depths int32 [batch, nodes]: of
+    each node in its tree (default: node t's is t, which a chain's are; a mask with a window needs them, without a
+    window they have no effect).
+    The cache may be held in 4 bits (fp4), of q's type.
+
+    For serving: there is no gradient and no forward mode, and tensors that carry either are refused."""
     dtype, dev = q.dtype, cache.device
     kind = _ATTN_TYPES.get(dtype)
     if kind is None or cache.dtype != dtype:
@@ -386,6 +464,17 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
         raise ValueError("lse must be a contiguous float32 tensor [batch, nodes, heads_q]")
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    if window is not None and not 1 <= window < 1 << 32:
+        raise ValueError("window must be at least 1")
+    if not 0 <= sinks < 1 << 32:
+        raise ValueError("sinks must not be negative")
+    if window is None and sinks:
+        raise ValueError("sinks go with a window")
+    if depths is not None and (depths.dtype != torch.int32 or depths.device != dev or depths.shape != (b, t)
+                               or not depths.is_contiguous()):
+        raise ValueError(f"depths must be a contiguous int32 tensor of shape {(b, t)} on {dev}")
+    if window is not None and mask is not None and depths is None:
+        raise ValueError("a mask with a window needs the nodes' depths")
     # what is allocated here belongs to the stream that the call runs on
     with cache._there(), _NO_CONTEXT if stream is None else torch.cuda.stream(stream):
         sh = cache._stream(stream)
@@ -399,5 +488,94 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pag
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *qs[:3], *ks[:3], *vs[:3],
             *out.stride()[:3], sq, 0 if mask is None else mask.data_ptr(), tn, b, t, hq, d, kind, 2 * layer,
             2 * layer + 1, 1 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), workspace.nbytes)
-        _tb_cache.tb_tree_attention(a, cache._c, sh)
+        if window is None and cache.fp4 is None:
+            _tb_cache.tb_tree_attention(a, cache._c, sh)
+        else:
+            view = _tb_serve.pack_view(window or 0, sinks, 0 if depths is None else depths.data_ptr(),
+                                       0 if cache.fp4 is None else 1)
+            _tb_serve.tb_view_attention(a, view, cache._c, sh)
     return out, lse
+
+
+_PROB_TYPES = {torch.float32: _tb_serve.TB_FP32, **_ATTN_TYPES}
+
+
+class Verified(NamedTuple):
+    """What verify_drafts returns, all int32 on the device."""
+    count: torch.Tensor                                # [batch]: accepted nodes, the root among them
+    path: torch.Tensor                                 # [batch, nodes]: their numbers, then -1
+    token: torch.Tensor                                # [batch]: the next token, -1 where there is none
+    lens: Optional[torch.Tensor] = None                # with a cache: [batch], for resize()
+    append_seqs: Optional[torch.Tensor] = None         # and [batch * nodes] each, for append() of
+    append_positions: Optional[torch.Tensor] = None    # rows of which b * nodes + t is node t of
+    append_index: Optional[torch.Tensor] = None        # sequence b
+
+
+def verify_drafts_workspace(probs: torch.Tensor) -> torch.Tensor:
+    """Workspace for verify_drafts calls with probabilities of this shape.  One serves any number of calls that
+    follow each other; calls that can overlap need one each."""
+    v = _tb_serve.tb_verify(batch=probs.shape[0], vocab=probs.shape[2])
+    return torch.empty(_tb_serve.tb_verify_workspace(v), dtype=torch.uint8, device=probs.device)
+
+
+def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor,
+                  parents: Optional[torch.Tensor] = None, draft_probs: Optional[torch.Tensor] = None,
+                  nodes: Optional[torch.Tensor] = None, cache: Optional[PagedCache] = None,
+                  seqs: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> Verified:
+    """Which of the drafted tokens hold, so that they and the next one are distributed as the target's (the rule is
+    tb_verify_drafts' in include/tb_serve.h).
+
+    probs [batch, nodes, vocab]: the target's distribution of what follows each node; node 0 is the root, the last
+    token that holds already.  tokens int32 [batch, nodes]: what the nodes propose.  uniform float32 [batch, nodes]:
+    random numbers in [0, 1), a node's for its test, the root's for the next token.  parents int32 [batch, nodes], each
+    below its node (default: chains).  draft_probs as probs: row t is what node t's children were drawn from,
+    independently of each other; None: they were chosen, not drawn.  nodes int32 [batch]: how many are real.
+    Probabilities are float32, bfloat16 or float16, any strides, the vocabulary contiguous.
+
+    With cache and seqs int32 [batch], their rows in it, the result has the lengths and lists with which
+    cache.resize(seqs, r.lens) and cache.append(rows, r.append_seqs, r.append_positions, r.append_index) take the
+    accepted nodes into it."""
+    dev, kind = probs.device, _PROB_TYPES.get(probs.dtype)
+    if kind is None or probs.dim() != 3 or not probs.is_cuda or (probs.shape[2] > 1 and probs.stride(2) != 1):
+        raise ValueError("probs must be a float32, bfloat16 or float16 CUDA tensor [batch, nodes, vocab], "
+                         "the vocabulary contiguous")
+    b, t, vocab = probs.shape
+    if not (1 <= t <= 4096 and b <= 65536 and 1 <= vocab <= _tb_serve.TB_VERIFY_MAX_VOCAB):
+        raise ValueError("probs must have 1 to 4096 nodes, up to 65536 sequences and 2^24 entries of the vocabulary")
+    if draft_probs is not None and (draft_probs.dtype != probs.dtype or draft_probs.device != dev
+                                    or draft_probs.shape != probs.shape
+                                    or (vocab > 1 and draft_probs.stride(2) != 1)):
+        raise ValueError("draft_probs must have probs' type, shape and device, the vocabulary contiguous")
+    _no_gradient("verify_drafts", probs, draft_probs, uniform)
+    for x, dtype, what in ((tokens, torch.int32, "tokens"), (uniform, torch.float32, "uniform"),
+                           (parents, torch.int32, "parents")):
+        if x is not None and (x.dtype != dtype or x.device != dev or x.shape != (b, t) or not x.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {(b, t)} on {dev}")
+    tn = 0 if nodes is None else _list_arg(nodes, b, dev, "nodes")
+    if (cache is None) != (seqs is None):
+        raise ValueError("cache and seqs go together")
+    if cache is not None and cache.device != dev:
+        raise ValueError("probs must be on the cache's device")
+    sq = 0 if seqs is None else _list_arg(seqs, b, dev, "seqs")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream must be one of {dev}")
+    there = _NO_CONTEXT if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+    with there, _NO_CONTEXT if stream is None else torch.cuda.stream(stream):
+        sh = torch._C._cuda_getCurrentRawStream(dev.index)
+        if workspace is None:
+            workspace = verify_drafts_workspace(probs)
+        # one allocation, cut up
+        sizes = [b, b * t, b] + ([] if cache is None else [b, b * t, b * t, b * t])
+        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
+        ptrs = [p.data_ptr() for p in parts] + [0] * (7 - len(parts))
+        ps, ds = probs.stride(), (0, 0) if draft_probs is None else draft_probs.stride()
+        v = _tb_serve.pack_verify(
+            probs.data_ptr(), 0 if draft_probs is None else draft_probs.data_ptr(), ps[0], ps[1], ds[0], ds[1],
+            tokens.data_ptr(), 0 if parents is None else parents.data_ptr(), uniform.data_ptr(), tn, b, t, vocab, kind,
+            *ptrs[:3], sq, 0 if cache is None else cache.lens.data_ptr(), 0 if cache is None else cache.max_seqs,
+            *ptrs[3:], workspace.data_ptr(), workspace.nbytes)
+        _tb_serve.tb_verify_drafts(v, sh)
+    return Verified(parts[0], parts[1].view(b, t), *parts[2:])
