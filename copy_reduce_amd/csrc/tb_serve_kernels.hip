@@ -260,10 +260,10 @@ hipError_t launch_read(const Pools &pools, uint32_t npools, const CacheState &s,
 // rejections at one node is max(p - taken q, 0), taken the sum of the z's: where an earlier difference was cut
 // at 0, so is the later one.
 //
-// The first kernel has a workgroup for each stretch of the vocabulary.  Each walks its sequence's tree by itself (one wave; the
-// numbers of 64 nodes at once, so that a chain of any length up to that costs two latencies) up to the first sum, and
-// sums its stretch.  The second, a workgroup a sequence, goes on from there, and draws the token: the stretch in which the sums
-// pass, then the place in it.
+// The first kernel, a wave a sequence, walks the tree up to the first sum: the numbers of 64 nodes at once, so that a
+// chain of any length up to that costs two latencies.  The second has a wave for each stretch of the vocabulary, which sums
+// it; the last workgroup of a sequence to end goes on with the walk, if it is not at its end, and draws the token: the stretch in which the
+// sums pass, then the place in it.
 
 struct VerifyArgs {
     const uint8_t *probs, *draft;
@@ -275,6 +275,8 @@ struct VerifyArgs {
     uint32_t batch, nodes, vocab, max_seqs;
     uint32_t stretch, stretches;                 // elements, and how many of them the vocabulary is
     struct Walk *walks;                          // [batch] workspace
+    uint32_t groups;                             // workgroups a sequence
+    uint32_t *ended;                             // [batch] those that have ended
     double *sums;                                // [batch][stretches]
 };
 
@@ -286,11 +288,14 @@ struct Walk {
     double z, taken;
 };
 
-constexpr uint32_t kMaxStretch = 8192, kMaxStretches = 2048;
-// Elements of a stretch: enough workgroups to fill the chip, but none with less than 1,024 elements.
+constexpr uint32_t kDraw = 512, kDrawWaves = kDraw / 64;   // threads and waves of a workgroup
+constexpr uint32_t kMaxStretch = 4096, kMaxStretches = 4096;
+// Elements of a stretch: enough for two workgroups on each CU, which all run at once, but no more stretches than there is room
+// for in LDS.
 static uint32_t stretch_of(uint32_t batch, uint32_t vocab) {
     uint32_t n = kMaxStretch;
-    while (n > 1024 && (uint64_t)batch * ((vocab + n - 1) / n) < 1024)
+    while (n > 512 && (uint64_t)batch * ((vocab + n * kDrawWaves - 1) / (n * kDrawWaves)) < 512
+            && (vocab + n / 2 - 1) / (n / 2) <= kMaxStretches)
         n /= 2;
     return n;
 }
@@ -315,63 +320,85 @@ __device__ __forceinline__ uint32_t nodes_of(const VerifyArgs &g, uint32_t b) {
     const int32_t n = g.tree_nodes != nullptr ? g.tree_nodes[b] : (int32_t)g.nodes;
     return (uint32_t)min(max(n, 0), (int32_t)g.nodes);
 }
-// What node t of sequence b proposes; false where it is passed over.
+// 64 nodes of a sequence, one a lane: what each proposes and the numbers of its test.
+struct Proposals {
+    uint32_t first;      // of the 64; ~0: none yet
+    bool there;          // not passed over
+    int32_t parent, x;
+    double u, p, q;
+};
+
+// What node t of sequence b proposes; false where it is passed over.  t < nodes of the call, n: of the sequence.
 __device__ __forceinline__ bool proposal(const VerifyArgs &g, uint32_t b, uint32_t t, uint32_t n, int32_t *parent,
         int32_t *x) {
-    *parent = *x = -1;
-    if (t < 1 || t >= n)
-        return false;
     const uint64_t at = (uint64_t)b * g.nodes + t;
     *parent = g.parents != nullptr ? g.parents[at] : (int32_t)t - 1;
     *x = g.tokens[at];
-    return (uint32_t)*parent < t && (uint32_t)*x < g.vocab;
+    return t >= 1 && t < n && (uint32_t)*parent < t && (uint32_t)*x < g.vocab;
 }
 
-// Goes on with a walk, the same in all lanes of one whole wave: to its end, or (Q) to a rejection.  `write`: the path
-// is written.
 template <typename T, bool Q>
-__device__ __forceinline__ Walk go_on(const VerifyArgs &g, uint32_t b, uint32_t n, Walk w, bool write) {
+__device__ __forceinline__ void look_at(const VerifyArgs &g, uint32_t b, uint32_t n, uint32_t first, Proposals *s) {
+    const uint32_t lane = threadIdx.x & 63, t = first + lane;
+    const uint8_t *const row0 = g.probs + b * g.probs_stride[0], *const draft0 = g.draft + b * g.draft_stride[0];
+    s->first = first;
+    s->there = false;
+    s->parent = s->x = -1;
+    s->u = s->p = 0;
+    s->q = 1;
+    if (t < g.nodes) {
+        s->u = g.uniform[(uint64_t)b * g.nodes + t];
+        s->there = proposal(g, b, t, n, &s->parent, &s->x);
+    }
+    if (s->there) {
+        s->p = (double)(float)reinterpret_cast<const T *>(row0 + s->parent * g.probs_stride[1])[s->x];
+        if (Q)
+            s->q = (double)(float)reinterpret_cast<const T *>(draft0 + s->parent * g.draft_stride[1])[s->x];
+    }
+}
+
+// Whether an earlier child of `cur` than the k-th of these nodes proposes the same.
+__device__ __forceinline__ bool proposed_before(const VerifyArgs &g, uint32_t b, uint32_t n, const Proposals &s, int k,
+        int32_t cur) {
     const uint32_t lane = threadIdx.x & 63;
-    const uint64_t row0 = reinterpret_cast<uint64_t>(g.probs) + b * g.probs_stride[0];
-    const uint64_t draft0 = reinterpret_cast<uint64_t>(g.draft) + b * g.draft_stride[0];
+    const int32_t x = __builtin_amdgcn_readlane(s.x, k);
+    if (__ballot(s.there && s.parent == cur && (int)lane < k && s.x == x) != 0)
+        return true;
+    for (uint32_t first = (uint32_t)(cur + 1) & ~63u; first < s.first; first += 64) {
+        int32_t parent = -1, other = -1;
+        const bool there = proposal(g, b, first + lane, n, &parent, &other);
+        if (__ballot(there && parent == cur && other == x) != 0)
+            return true;
+    }
+    return false;
+}
+
+// Goes on with a walk, the same in all lanes of one whole wave: to its end, or (Q) to a rejection after which the current
+// node has another child.  `write`: the path is written.
+template <typename T, bool Q>
+__device__ __forceinline__ Walk go_on(const VerifyArgs &g, uint32_t b, uint32_t n, Walk w, Proposals *s, bool write) {
+    const uint32_t lane = threadIdx.x & 63;
+    bool rejected = false;
     w.waits = 0;
-    for (uint32_t g0 = (uint32_t)(w.last + 1) & ~63u; g0 < n && !w.waits; g0 += 64) {
-        const uint32_t t = g0 + lane;
-        int32_t parent, x;
-        const bool there = proposal(g, b, t, n, &parent, &x);
-        double u = 0, p = 0, q = 1;
-        if (there) {
-            u = g.uniform[(uint64_t)b * g.nodes + t];
-            p = (double)(float)reinterpret_cast<const T *>(row0 + parent * g.probs_stride[1])[x];
-            if (Q)
-                q = (double)(float)reinterpret_cast<const T *>(draft0 + parent * g.draft_stride[1])[x];
-        }
-        if (!Q && g.parents != nullptr) {
-            // a token that an earlier sibling had is gone
-            bool again = false;
-            for (uint32_t h0 = 0; h0 <= g0; h0 += 64) {
-                int32_t parent2 = parent, x2 = x;
-                bool there2 = there;
-                if (h0 != g0)
-                    there2 = proposal(g, b, h0 + lane, n, &parent2, &x2);
-                parent2 = there2 ? parent2 : -1;
-                const uint32_t end = min(64u, n - h0);
-                for (uint32_t k = 0; k < end; k++)
-                    again |= __builtin_amdgcn_readlane(parent2, k) == parent && __builtin_amdgcn_readlane(x2, k) == x
-                            && h0 + k < t;
-            }
-            if (again)
-                p = 0;
-        }
+    for (uint32_t first = (uint32_t)(w.last + 1) & ~63u; first < n; first += 64) {
+        if (s->first != first)
+            look_at<T, Q>(g, b, n, first, s);
         for (;;) {
-            const uint64_t next = __ballot(there && parent == w.cur && (int32_t)t > w.last);
+            const uint64_t next = __ballot(s->there && s->parent == w.cur && (int32_t)(first + lane) > w.last);
             if (next == 0)
                 break;
+            if (Q && rejected) {   // its test needs the sum
+                w.waits = 1;
+                return w;
+            }
             const int k = __builtin_ctzll(next);
-            const double pk = lane_double(p, k), qk = lane_double(q, k), uk = lane_double(u, k);
-            const double left = Q ? fmax(pk - w.taken * qk, 0.0) : pk;
-            w.last = (int32_t)g0 + k;
-            if (uk * qk * w.z < left) {
+            double p = lane_double(s->p, k);
+            const double q = lane_double(s->q, k), u = lane_double(s->u, k);
+            if (!Q && g.parents != nullptr && proposed_before(g, b, n, *s, k, w.cur))
+                p = 0;   // that token is gone
+            const double left = Q ? fmax(__builtin_fma(-w.taken, q, p), 0.0) : p;
+            w.last = (int32_t)first + k;
+            if (u * q * w.z < left) {
                 w.cur = w.last;
                 w.z = 1;
                 w.taken = 0;
@@ -380,10 +407,9 @@ __device__ __forceinline__ Walk go_on(const VerifyArgs &g, uint32_t b, uint32_t 
                 w.count++;
             } else if (Q) {
                 w.taken += w.z;
-                w.waits = 1;
-                break;
+                rejected = true;
             } else {
-                w.z -= pk;
+                w.z -= p;
             }
         }
     }
@@ -405,253 +431,296 @@ struct Left {
     }
     __device__ __forceinline__ double of(double p_, double q_, uint32_t x) const {
         if (Q)
-            return fmax(p_ - taken * q_, 0.0);
-        return gone != nullptr && (gone[(x - first) / 32] >> ((x - first) % 32) & 1) ? 0.0 : p_;
+            return fmax(__builtin_fma(-taken, q_, p_), 0.0);
+        return gone != nullptr && p_ > 0 && (gone[(x - first) / 32] >> ((x - first) % 32) & 1) ? 0.0 : p_;
     }
     __device__ __forceinline__ double at(uint32_t x) const {
         return of((double)(float)p[x], Q ? (double)(float)q[x] : 0.0, x);
     }
-    // The sum over this thread's part of [begin, end), of `threads`.
-    __device__ __forceinline__ double sum(uint32_t begin, uint32_t end, uint32_t thread, uint32_t threads) const {
-        constexpr uint32_t E = 16 / sizeof(T);
+    // The sums of the stretches that lie in [begin, end), by one whole wave: done(k, sum) for each.  begin is a whole number of
+    // stretches, or of runs of kRun elements, whose loads are on their way together.
+    static constexpr uint32_t E = 16 / sizeof(T), kLoads = 8, kRun = kLoads * 64 * E;
+    // ready() is called once, with the first loads on their way.
+    template <typename Done, typename Ready>
+    __device__ __forceinline__ void sums(uint32_t begin, uint32_t end, uint32_t stretch, Done done, Ready ready) const {
         typedef T Vec __attribute__((ext_vector_type(E), aligned(sizeof(T))));
+        const uint32_t lane = threadIdx.x & 63;
         double s = 0;
-        for (uint32_t x = begin + thread * E; x < end; x += threads * E) {
-            if (x + E <= end) {
-                const Vec pv = *reinterpret_cast<const Vec *>(p + x);
-                Vec qv = pv;
-                if (Q)
-                    qv = *reinterpret_cast<const Vec *>(q + x);
+#pragma unroll 1
+        for (uint32_t x0 = begin; x0 < end; x0 += kRun) {
+            Vec pv[kLoads], qv[kLoads];
+#pragma unroll
+            for (uint32_t i = 0; i < kLoads; i++) {
+                const uint32_t x = x0 + (i * 64 + lane) * E;
+                pv[i] = qv[i] = Vec{};
+                if (x + E <= end) {
+                    pv[i] = *reinterpret_cast<const Vec *>(p + x);
+                    if (Q)
+                        qv[i] = *reinterpret_cast<const Vec *>(q + x);
+                } else if (x < end) {   // the end of the vocabulary
+#pragma unroll
+                    for (uint32_t e = 0; e < E - 1; e++)
+                        if (x + e < end) {
+                            pv[i][e] = p[x + e];
+                            if (Q)
+                                qv[i][e] = q[x + e];
+                        }
+                }
+            }
+            if (x0 == begin)
+                ready();
+#pragma unroll
+            for (uint32_t i = 0; i < kLoads; i++) {
+                const uint32_t x = x0 + i * 64 * E, next = x + 64 * E;
+                if (x >= end)
+                    break;
 #pragma unroll
                 for (uint32_t e = 0; e < E; e++)
-                    s += of((double)(float)pv[e], (double)(float)qv[e], x + e);
-            } else {
-                for (uint32_t e = x; e < end; e++)
-                    s += at(e);
+                    s += of((double)(float)pv[i][e], Q ? (double)(float)qv[i][e] : 0.0, x + lane * E + e);
+                if (next % stretch == 0 || next >= end) {
+                    const double all = wave_sum(s);
+                    done(x / stretch, all);
+                    s = 0;
+                }
             }
         }
-        return s;
     }
 };
 
-// Marks what the current node's children stood for, of [first, end), in gone[]; all threads, with a barrier.
-__device__ __forceinline__ void mark_gone(const VerifyArgs &g, uint32_t b, uint32_t n, const Walk &w, uint32_t first,
-        uint32_t end, uint32_t *gone) {
-    for (uint32_t i = threadIdx.x; i < (end - first + 31) / 32; i += blockDim.x)
-        gone[i] = 0;
-    __syncthreads();
-    for (uint32_t t = threadIdx.x; t < n; t += blockDim.x) {
-        int32_t parent, x;
-        if (proposal(g, b, t, n, &parent, &x) && parent == w.cur && (uint32_t)x >= first && (uint32_t)x < end)
-            atomicOr(&gone[((uint32_t)x - first) / 32], 1u << (((uint32_t)x - first) % 32));
+// What this thread's nodes propose, the first of them read before it is known what for.
+struct Gone {
+    const VerifyArgs &g;
+    uint32_t b, n;
+    bool there;
+    int32_t parent, x;
+
+    __device__ __forceinline__ Gone(const VerifyArgs &g_, uint32_t b_, uint32_t n_) : g(g_), b(b_), n(n_), there(false),
+            parent(-1), x(-1) {
+        if (n != 0 && threadIdx.x < g.nodes)
+            there = proposal(g, b, threadIdx.x, n, &parent, &x);
     }
-    __syncthreads();
-}
+    __device__ __forceinline__ void one(bool there_, int32_t parent_, uint32_t x_, int32_t cur, uint32_t first,
+            uint32_t end, uint32_t *bits) const {
+        if (there_ && parent_ == cur && x_ >= first && x_ < end)
+            atomicOr(&bits[(x_ - first) / 32], 1u << ((x_ - first) % 32));
+    }
+    // Marks what the children of `cur` propose, of [first, end), in bits[]; all threads, with barriers.
+    __device__ __forceinline__ void mark(int32_t cur, uint32_t first, uint32_t end, uint32_t *bits) const {
+        for (uint32_t i = threadIdx.x; i < (end - first + 31) / 32; i += kDraw)
+            bits[i] = 0;
+        __syncthreads();
+        one(there, parent, (uint32_t)x, cur, first, end, bits);
+        for (uint32_t t = threadIdx.x + kDraw; t < n; t += kDraw) {
+            int32_t parent2 = -1, x2 = -1;
+            const bool there2 = proposal(g, b, t, n, &parent2, &x2);
+            one(there2, parent2, (uint32_t)x2, cur, first, end, bits);
+        }
+        __syncthreads();
+    }
+};
 
 template <typename T, bool Q>
-__global__ __launch_bounds__(256) void verify_walk_kernel(VerifyArgs g) {
-    __shared__ Walk walk;
-    __shared__ double parts[4];
-    __shared__ uint32_t gone[kMaxStretch / 32];
-    const uint32_t b = blockIdx.x / g.stretches, k = blockIdx.x % g.stretches, thread = threadIdx.x;
+__global__ __launch_bounds__(64) void verify_walk_kernel(VerifyArgs g) {
+    const uint32_t b = blockIdx.x;
+    const uint64_t row = (uint64_t)b * g.nodes;
+    Proposals s;
     const uint32_t n = nodes_of(g, b);
-    if (n == 0)
-        return;
-    if (thread < 64) {
-        const Walk to = go_on<T, Q>(g, b, n, Walk{0, 0, 1, 0, 1.0, 0.0}, k == 0);
-        if (thread == 0) {
-            walk = to;
-            if (k == 0)
-                g.path[(uint64_t)b * g.nodes] = 0;
-        }
-    }
-    __syncthreads();
-    const Walk w = walk;
-    const uint32_t begin = k * g.stretch, end = min(begin + g.stretch, g.vocab);
-    if (!Q)
-        mark_gone(g, b, n, w, begin, end, gone);
-    const double s = wave_sum(Left<T, Q>(g, b, w, gone, begin).sum(begin, end, thread, 256));
-    if (thread % 64 == 0)
-        parts[thread / 64] = s;
-    __syncthreads();
-    if (thread == 0) {
-        g.sums[(uint64_t)b * g.stretches + k] = parts[0] + parts[1] + (parts[2] + parts[3]);
-        if (k == 0)
-            g.walks[b] = w;
+    look_at<T, Q>(g, b, n, 0, &s);
+    Walk w = {0, 0, n == 0 ? 0 : 1, 0, 1.0, 0.0};
+    w = go_on<T, Q>(g, b, n, w, &s, true);
+    if (threadIdx.x == 0) {
+        if (n != 0)
+            g.path[row] = 0;
+        g.walks[b] = w;
+        g.ended[b] = 0;
     }
 }
 
-constexpr uint32_t kDraw = 1024;   // threads
-
-// The sum of v over the workgroup, the same in all threads and the same whenever it is taken.
-__device__ __forceinline__ double block_total(double v, double *lds) {
-    v = wave_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 64 == 0)
-        lds[threadIdx.x / 64] = v;
-    __syncthreads();
-    double all = 0;
-    for (uint32_t k = 0; k < kDraw / 64; k++)
-        all += lds[k];
-    return all;
-}
-// The sum of v over the threads up to and with this one.
-__device__ __forceinline__ double block_upto(double v, double *lds) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Sums of x over the lanes up to and with this one.
+__device__ __forceinline__ double wave_upto(double x) {
+    const uint32_t lane = threadIdx.x & 63;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(v, d);
+        const double y = __shfl_up(x, d);
         if (lane >= (uint32_t)d)
-            v += y;
+            x += y;
     }
-    __syncthreads();
-    if (lane == 63)
-        lds[wave] = v;
-    __syncthreads();
-    double before = 0;
-    for (uint32_t k = 0; k < wave; k++)
-        before += lds[k];
-    return before + v;
+    return x;
+}
+
+// Values that other workgroups of this kernel wrote, or another wave of this one: past the L1.
+template <typename N>
+__device__ __forceinline__ N fresh(const N *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <typename T, bool Q>
-__global__ __launch_bounds__(kDraw) void verify_draw_kernel(VerifyArgs g) {
+__global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
     __shared__ Walk walk;
-    __shared__ double sums[kMaxStretches], lds[kDraw / 64], before;
-    __shared__ uint32_t gone[kMaxStretch / 32], found, spare;
-    const uint32_t b = blockIdx.x, thread = threadIdx.x, n = nodes_of(g, b);
+    __shared__ double sums[kMaxStretches], waves[kDrawWaves];
+    __shared__ uint32_t gone[kMaxStretch * kDrawWaves / 32], found, spare, last_one;
+    const uint32_t b = blockIdx.x / g.groups, thread = threadIdx.x, lane = thread & 63, wave = thread >> 6;
     const uint64_t row = (uint64_t)b * g.nodes;
-    int32_t token = -1;
-    if (thread == 0)
-        walk = n == 0 ? Walk{0, 0, 0, 0, 1.0, 0.0} : g.walks[b];
-    if (n != 0) {
-        double s = 0;
-        for (uint32_t k = thread; k < g.stretches; k += kDraw)
-            s += sums[k] = g.sums[(uint64_t)b * g.stretches + k];
-        double total = block_total(s, lds);
-        // Takes the sums of what is left anew, a wave a stretch.
-        const auto take_sums = [&](const Left<T, Q> &left) {
-            for (uint32_t k = thread / 64; k < g.stretches; k += kDraw / 64) {
-                const double x = wave_sum(
-                        left.sum(k * g.stretch, min((k + 1) * g.stretch, g.vocab), thread % 64, 64));
-                if (thread % 64 == 0)
-                    sums[k] = x;
-            }
-            __syncthreads();
-            double y = 0;
-            for (uint32_t k = thread; k < g.stretches; k += kDraw)
-                y += sums[k];
-            total = block_total(y, lds);
+    const double u = g.uniform[row];
+    Walk w = g.walks[b];
+    const uint32_t n = nodes_of(g, b);
+    const int32_t seq = g.seqs != nullptr ? g.seqs[b] : -1;
+    const Gone whose(g, b, Q ? 0 : n);
+    int32_t token = -1, had = 0;
+    if (n != 0) {   // this wave's stretch
+        const uint32_t first = blockIdx.x % g.groups * kDrawWaves, k = first + wave;
+        const uint32_t begin = first * g.stretch, end = min(begin + kDrawWaves * g.stretch, g.vocab);
+        const auto ready = [&] {
+            if (!Q)
+                whose.mark(w.cur, begin, end, gone);
         };
-        if (Q)
-            while (walk.waits) {
-                Walk w = walk;
-                const int32_t last = w.last;
-                __syncthreads();
-                if (thread < 64) {
+        if (k < g.stretches)
+            Left<T, Q>(g, b, w, gone, begin).sums(
+                    k * g.stretch, min((k + 1) * g.stretch, g.vocab), g.stretch, [&](uint32_t j, double x) {
+                        if (lane == 0)
+                            __hip_atomic_store(&g.sums[(uint64_t)b * g.stretches + j], x, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+                    }, ready);
+        else
+            ready();
+        // The sums bypass the L2, so that the wait makes them seen by all before this workgroup is counted.  A
+        // release would do as well, and write the L2 back first.
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (thread == 0)
+            last_one = __hip_atomic_fetch_add(&g.ended[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        __syncthreads();
+        if (last_one != g.groups)
+            return;
+        for (uint32_t i = thread; i < g.stretches; i += kDraw)
+            sums[i] = fresh(&g.sums[(uint64_t)b * g.stretches + i]);
+        had = g.seqs != nullptr ? g.lens[seq] : 0;
+        __syncthreads();
+        // The same in every wave, and no barrier.
+        const auto total_of = [&] {
+            double y = 0;
+            for (uint32_t k = lane; k < g.stretches; k += 64)
+                y += sums[k];
+            return wave_sum(y);
+        };
+        // Takes the sums of what is left anew: by stretches, or by runs of several.
+        const auto take_sums = [&](const Left<T, Q> &left) {
+            const uint32_t step = max(g.stretch, Left<T, Q>::kRun);
+            __syncthreads();
+            for (uint32_t x = wave * step; x < g.vocab; x += kDrawWaves * step)
+                left.sums(x, min(x + step, g.vocab), g.stretch, [&](uint32_t j, double y) {
+                    if (lane == 0)
+                        sums[j] = y;
+                }, [] {});
+            __syncthreads();
+        };
+        double total = total_of();
+        if (Q) {
+            Proposals s;
+            s.first = ~0u;
+            while (w.waits) {
+                if (wave == 0) {
                     w.z = total;
-                    w = go_on<T, Q>(g, b, n, w, true);
-                    if (thread == 0)
+                    w = go_on<T, Q>(g, b, n, w, &s, true);
+                    if (lane == 0)
                         walk = w;
                 }
                 __syncthreads();
-                if (walk.last == last)   // it had no sibling left
-                    break;
-                take_sums(Left<T, Q>(g, b, walk, nullptr, 0));
+                w = walk;
+                take_sums(Left<T, Q>(g, b, w, nullptr, 0));
+                total = total_of();
             }
-        Walk w = walk;
+        }
+        Walk from = w;
         bool all = false;   // whether p itself is drawn from
         if (!(total > 0)) {
-            w.taken = 0;
+            from.taken = 0;
             all = true;
-            take_sums(Left<T, Q>(g, b, w, nullptr, 0));
+            take_sums(Left<T, Q>(g, b, from, nullptr, 0));
+            total = total_of();
         }
         if (total > 0 && total < INFINITY) {
-            const double target = (double)g.uniform[row] * total;
+            const double target = u * total;
             // the first stretch whose sums pass the target, or (rounding) the last with anything in it
-            if (thread == 0) {
-                found = ~0u;
-                spare = 0;
+            uint32_t stretch = 0;
+            double passed = 0, before = 0;
+            for (uint32_t k0 = 0; k0 < g.stretches; k0 += 64) {
+                const double mine = k0 + lane < g.stretches ? sums[k0 + lane] : 0;
+                const double upto = passed + wave_upto(mine);
+                const uint64_t some = __ballot(mine > 0), over = __ballot(mine > 0 && upto > target);
+                const uint64_t pick = over != 0 ? over & -over : some;
+                if (pick != 0) {
+                    const int k = 63 - __builtin_clzll(pick);
+                    stretch = k0 + k;
+                    before = lane_double(upto, k) - lane_double(mine, k);
+                }
+                if (over != 0)
+                    break;
+                passed = lane_double(upto, 63);
             }
-            double passed = 0;
-            for (uint32_t k0 = 0; k0 < g.stretches; k0 += kDraw) {
-                const uint32_t k = k0 + thread;
-                const double mine = k < g.stretches ? sums[k] : 0;
-                const double upto = passed + block_upto(mine, lds);
-                if (mine > 0 && upto > target)
-                    atomicMin(&found, k);
-                if (mine > 0)
-                    atomicMax(&spare, k);
-                passed += block_total(mine, lds);
-            }
-            __syncthreads();
-            const uint32_t k = found != ~0u ? found : spare;
-            __syncthreads();
-            double s0 = 0;
-            for (uint32_t j = thread; j < k; j += kDraw)
-                s0 += sums[j];
-            s0 = block_total(s0, lds);
-            if (thread == 0) {
-                before = s0;
-                found = ~0u;
-                spare = 0;
-            }
-            const uint32_t begin = k * g.stretch, end = min(begin + g.stretch, g.vocab);
+            // the first place in it
+            const uint32_t begin = stretch * g.stretch, end = min(begin + g.stretch, g.vocab);
             const bool any_gone = !Q && !all;
+            if (thread == 0) {
+                found = ~0u;
+                spare = begin;
+            }
             if (any_gone)
-                mark_gone(g, b, n, w, begin, end, gone);
-            const Left<T, Q> left(g, b, w, any_gone ? gone : nullptr, begin);
+                whose.mark(w.cur, begin, end, gone);
+            const Left<T, Q> left(g, b, from, any_gone ? gone : nullptr, begin);
             const uint32_t each = g.stretch / kDraw, x0 = begin + thread * each;
-            double mine = 0;
-            for (uint32_t x = x0; x < min(x0 + each, end); x++)
-                mine += left.at(x);
-            double upto = block_upto(mine, lds) + before;
+            constexpr uint32_t kEach = kMaxStretch / kDraw;
+            double v[kEach], mine = 0;
+#pragma unroll
+            for (uint32_t e = 0; e < kEach; e++) {
+                v[e] = e < each && x0 + e < end ? left.at(x0 + e) : 0;
+                mine += v[e];
+            }
+            double upto = wave_upto(mine);
+            if (lane == 63)
+                waves[wave] = upto;
+            __syncthreads();
+            for (uint32_t k = 0; k < wave; k++)
+                before += waves[k];
+            upto += before;
             if (mine > 0) {
-                // from here on by single places; this thread's end is the sum just taken
+                uint32_t hit = ~0u, last = 0;
                 double run = upto - mine;
-                uint32_t last = x0;
-                for (uint32_t x = x0; x < min(x0 + each, end); x++) {
-                    const double v = left.at(x);
-                    if (v > 0)
-                        last = x;
+#pragma unroll
+                for (uint32_t e = 0; e < kEach; e++) {
+                    run += v[e];
+                    if (v[e] > 0)
+                        last = x0 + e;
+                    if (v[e] > 0 && run > target && hit == ~0u)
+                        hit = x0 + e;
                 }
-                atomicMax(&spare, last + 1);
-                if (upto > target) {
-                    uint32_t hit = last;
-                    for (uint32_t x = x0; x < last; x++) {
-                        const double v = left.at(x);
-                        run += v;
-                        if (v > 0 && run > target) {
-                            hit = x;
-                            break;
-                        }
-                    }
-                    atomicMin(&found, hit);
-                }
+                atomicMax(&spare, last);
+                if (upto > target)   // the last place where the sum by single places falls short
+                    atomicMin(&found, hit != ~0u ? hit : last);
             }
             __syncthreads();
-            token = (int32_t)(found != ~0u ? found : (spare != 0 ? spare - 1 : begin));
+            token = (int32_t)(found != ~0u ? found : spare);
         }
+    } else if (blockIdx.x % g.groups != 0) {
+        return;   // one workgroup writes that there is nothing
+    } else if (g.seqs != nullptr && (uint32_t)seq < g.max_seqs) {
+        had = g.lens[seq];
     }
-    __syncthreads();
-    const int32_t count = walk.count;
-    const int32_t q = g.seqs != nullptr ? g.seqs[b] : -1;
-    const bool held = g.seqs != nullptr && (uint32_t)q < g.max_seqs;
-    const int32_t had = held ? g.lens[q] : 0;
     if (thread == 0) {
-        g.count[b] = count;
+        g.count[b] = w.count;
         g.token[b] = token;
         if (g.seqs != nullptr)
-            g.new_lens[b] = had + count;
+            g.new_lens[b] = had + w.count;
     }
+    if (Q)
+        __syncthreads();   // of the path's last entries, which the first wave may have written
     for (uint32_t i = thread; i < g.nodes; i += kDraw) {
-        const bool real = (int32_t)i < count;
-        // written by this kernel too: past the L1
-        const int32_t node = real ? __hip_atomic_load(&g.path[row + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : -1;
+        const bool real = (int32_t)i < w.count;
+        const int32_t node = real ? fresh(&g.path[row + i]) : -1;
         if (!real)
             g.path[row + i] = -1;
         if (g.seqs != nullptr) {
-            g.append_seqs[row + i] = real ? q : -1;
+            g.append_seqs[row + i] = real ? seq : -1;
             g.append_positions[row + i] = real ? had + (int32_t)i : 0;
             g.append_index[row + i] = real ? (int32_t)(row + node) : 0;
         }
@@ -662,19 +731,19 @@ static uint64_t round16(uint64_t n) { return (n + 15) / 16 * 16; }
 
 uint64_t verify_workspace(uint32_t batch, uint32_t vocab) {
     const uint32_t stretch = stretch_of(batch, vocab);
-    return round16(sizeof(Walk) * batch) + round16(8ull * batch * ((vocab + stretch - 1) / stretch));
+    return round16(sizeof(Walk) * batch) + round16(4ull * batch) + round16(8ull * batch * ((vocab + stretch - 1) / stretch));
 }
 
 template <typename T>
 static hipError_t launch_verify_type(const VerifyArgs &g, bool drafted, hipStream_t stream) {
     LaunchSeq seq;
     const hipError_t e = launch(drafted ? verify_walk_kernel<T, true> : verify_walk_kernel<T, false>,
-            g.batch * g.stretches, 256, stream, nullptr, g);
+            g.batch, 64, stream, nullptr, g);
     if (e != hipSuccess)
         return e;
     seq.last();
-    return launch(drafted ? verify_draw_kernel<T, true> : verify_draw_kernel<T, false>, g.batch, kDraw, stream,
-            nullptr, g);
+    return launch(drafted ? verify_draw_kernel<T, true> : verify_draw_kernel<T, false>, g.batch * g.groups, kDraw,
+            stream, nullptr, g);
 }
 
 hipError_t launch_verify(const tb_verify &v, hipStream_t stream) {
@@ -705,9 +774,11 @@ hipError_t launch_verify(const tb_verify &v, hipStream_t stream) {
     g.max_seqs = v.max_seqs;
     g.stretch = stretch_of(v.batch, v.vocab);
     g.stretches = (v.vocab + g.stretch - 1) / g.stretch;   // <= kMaxStretches
+    g.groups = (g.stretches + kDrawWaves - 1) / kDrawWaves;
     uint8_t *ws = static_cast<uint8_t *>(v.workspace);
     g.walks = reinterpret_cast<Walk *>(ws);
-    g.sums = reinterpret_cast<double *>(ws + round16(sizeof(Walk) * v.batch));
+    g.ended = reinterpret_cast<uint32_t *>(ws + round16(sizeof(Walk) * v.batch));
+    g.sums = reinterpret_cast<double *>(ws + round16(sizeof(Walk) * v.batch) + round16(4ull * v.batch));
     switch (v.dtype) {
     case TB_BF16: return launch_verify_type<__bf16>(g, v.draft_probs != nullptr, stream);
     case TB_FP16: return launch_verify_type<_Float16>(g, v.draft_probs != nullptr, stream);
