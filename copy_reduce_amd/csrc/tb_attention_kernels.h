@@ -85,6 +85,14 @@ struct Mfma<__bf16> {
     static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
+    // Of two pairs: the sum of the products and c.  One of a pair.
+    static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c) {
+        typedef __bf16 V2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(V2, a), __builtin_bit_cast(V2, b), c, false);
+    }
+    static __device__ __forceinline__ float number(uint32_t two, int i) {
+        return __uint_as_float(i == 0 ? two << 16 : two & 0xffff0000u);
+    }
     static constexpr uint32_t kExp = 0x7f80;   // exponent bits, all set where a value is not finite
     // Weights are taken times 2^kLift, numerator and denominator alike.  fp16 begins to lose bits below 2^-14 and
     // everything below 2^-25, where many small weights can still count together: seven bits are to spare above.
@@ -95,6 +103,14 @@ struct Mfma<_Float16> {
     typedef f16x8 V;
     static __device__ __forceinline__ f32x4 mul(V a, V b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c) {
+        typedef _Float16 V2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(V2, a), __builtin_bit_cast(V2, b), c, false);
+    }
+    static __device__ __forceinline__ float number(uint32_t two, int i) {
+        typedef _Float16 V2 __attribute__((ext_vector_type(2)));
+        return (float)__builtin_bit_cast(V2, two)[i];
     }
     static constexpr uint32_t kExp = 0x7c00;
     static constexpr float kLift = 7.f;
@@ -220,15 +236,18 @@ __device__ __forceinline__ typename SequenceOf<WIN>::T sequence_of(const AttnArg
 }
 
 // The batch's keys as one stream: each sequence's context and nodes, rounded up to kUnit
-// keys, and one unit more for what a sequence costs by itself, one after the other.  It is cut into equal shares,
+// keys, and some units more for what a sequence costs by itself, one after the other.  It is cut into equal shares,
 // one for each of the workgroups that a head's rows have, so that they all end together
 // however the lengths differ.  A share may cover parts of several sequences.
 // Every workgroup finds its place by itself (a few loads and a sum over the
 // batch): nothing is planned before the launch and the lengths stay on the device.
 constexpr uint32_t kUnit = 128;
-template <typename Seq>
+// What a sequence costs by itself, a dozen latencies, in units of its keys: of 4 bits they take a quarter of the time.
+// 64 sequences of up to 8,191 tokens in 4 bits with one unit 73 us, with three 65.5, five 64.5, eight 65.5.
+constexpr uint32_t own_units(bool fp4) { return fp4 ? 4 : 1; }
+template <bool FP4, typename Seq>
 __device__ __forceinline__ uint32_t weight_of(const Seq &s) {
-    return ((s.context + s.special() + kUnit - 1) / kUnit + 1) * kUnit;
+    return ((s.context + s.special() + kUnit - 1) / kUnit + own_units(FP4)) * kUnit;
 }
 
 constexpr uint64_t kWhole = 1ull << 40;   // a share longer than any sequence
@@ -239,7 +258,7 @@ struct Place {
 };
 
 // `known`: LDS for a sequence a thread; filled where the batch has no more than that.
-template <int WAVES, bool WIN>
+template <int WAVES, bool WIN, bool FP4>
 __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Place *out, uint64_t *lds,
         typename SequenceOf<WIN>::T *known) {
     if (g.budget == 0) {   // one sequence, from its first key to its last
@@ -255,7 +274,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Pla
         if (b0 + t < g.batch) {
             const auto q = sequence_of<WIN>(g, b0 + t);
             known[t] = q;
-            w = weight_of(q);
+            w = weight_of<FP4>(q);
         }
         total += w;
     }
@@ -275,7 +294,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Pla
     uint64_t before = 0;
     for (uint32_t b0 = 0; b0 < g.batch; b0 += 64 * WAVES) {
         if (g.batch > 64 * WAVES)
-            w = b0 + t < g.batch ? weight_of(sequence_of<WIN>(g, b0 + t)) : 0;
+            w = b0 + t < g.batch ? weight_of<FP4>(sequence_of<WIN>(g, b0 + t)) : 0;
         uint64_t x = w;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -304,7 +323,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &g, uint32_t mine, Pla
 // What a workgroup does of one sequence: the part [c0, c1) of its context and, if
 // `last`, its nodes.  Shares of one sequence are joined afterwards, from slot
 // (workgroup + sequence), unless there is only one.
-template <bool WIN>
+template <bool WIN, bool FP4>
 struct Part {
     typedef typename SequenceOf<WIN>::T Seq;
     Seq seq;
@@ -324,7 +343,7 @@ struct Part {
             seq.gap = uniform(s.gap);
             seq.zone = uniform(s.zone);
         }
-        end = at.start + weight_of(seq);
+        end = at.start + weight_of<FP4>(seq);
         if (at.share == kWhole) {
             c0 = slot = 0;
             c1 = seq.context;
@@ -365,7 +384,7 @@ struct Keys {
 
     // Places in a pool count pieces of 16 bytes (FP4: 4): 32 bits reach 64 GiB (16), and the address costs one
     // instruction.
-    __device__ __forceinline__ Keys(const AttnArgs &g_, const Part<WIN> &part, uint32_t head_, uint32_t *lds)
+    __device__ __forceinline__ Keys(const AttnArgs &g_, const Part<WIN, FP4> &part, uint32_t head_, uint32_t *lds)
         : g(g_), seq(part.seq), b(part.b), head(head_), count(part.seq.nodes), p1(0), list(lds) {
         row_table = g.table + (uint64_t)max(part.seq.row, 0) * g.max_pages;
         p0 = page_of(part.c0);
@@ -807,11 +826,73 @@ struct Held<T, D, true> {
     }
 };
 
-// Workgroups of the kernel for few rows that a CU holds, by the registers it is built with.
-constexpr int few_resident(int head_dim, bool) { return head_dim == 64 ? 3 : (head_dim <= 128 ? 2 : 1); }
+// The zone's keys and the drafted nodes one by one, every fourth a wave's: for the kernel over a cache in 4 bits, whose rows
+// see few of either (up to 16 nodes, and 15 tokens of the zone), and whose registers the tiles' way (both operands in 16 bits,
+// values that are not finite apart) would decide.
+// A lane has, of row n, elements q4 D / 4 on of key and values alike.
+template <typename T, int D, typename R, typename K, typename Seq>
+__device__ __forceinline__ void single_keys(const AttnArgs &g, const K &keys, const Seq &seq, R &rows, uint64_t kb,
+        uint64_t vb, uint32_t wk, uint32_t n, uint32_t q4) {
+    constexpr int KS = D / 32, DJ = D / 16;
+    // the lane's quarter of a head, in 16 bits or in the cache
+    const auto quarter = [&](bool in_zone, uint64_t row, u32x4 *x) {
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            if (in_zone) {
+                uint32_t code;
+                load_words<1>(&code, row + q4 * (D / 8) + s * 4);
+                const uint8_t p = *reinterpret_cast<const uint8_t *>(row + D / 2 + (q4 * (D / 4) + 8 * s) / 32);
+                x[s] = eight_of<T>(code, power_of(p, 0));
+            } else {
+                x[s] = *(const gu32x4 *)(row + R::lane_at(q4) + s * R::kStepBytes);
+            }
+        }
+    };
+#pragma unroll 1
+    for (uint32_t at = wk; at < seq.zone + keys.count; at += kWaves) {
+        const bool in_zone = at < seq.zone;
+        const uint32_t u = in_zone ? at : at - seq.zone;
+        uint64_t key = kb + u * g.k_stride[1], values = vb + u * g.v_stride[1];
+        if (in_zone) {
+            const uint64_t offset = keys.offset_in_zone(u);
+            key = reinterpret_cast<uint64_t>(g.k_cache) + offset;
+            values = reinterpret_cast<uint64_t>(g.v_cache) + offset;
+        }
+        u32x4 k[KS], v[KS];
+        quarter(in_zone, key, k);
+        quarter(in_zone, values, v);
+        const uint32_t bits = in_zone ? keys.seen_in_zone(n, u & ~31u) : keys.seen(n, u & ~31u);
+        const bool sees = bits >> (u & 31) & 1;
+        float score = 0;
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            const u32x4 q = __builtin_bit_cast(u32x4, rows.q[0][s]);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                score = Mfma<T>::dot(q[e], k[s][e], score);
+        }
+        score = lanes_sum(score);
+        const float top = sees ? score : -INFINITY;
+        if (__any(top * g.scale2 > __builtin_fmaf(rows.m[0], g.scale2, kSlack)))
+            rows.raise_maxima(g, &top);
+        const float weight = sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(score, g.scale2, -rows.base[0])) : 0.f;
+        rows.l[0] += q4 == 0 ? weight : 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 4; e++) {   // not seen: 0 times 0
+            const uint32_t two = sees ? v[e / 8][e % 8 / 2] : 0;
+            rows.o[0][e % DJ][e / DJ] =
+                __builtin_fmaf(weight, Mfma<T>::number(two, e % 2), rows.o[0][e % DJ][e / DJ]);
+        }
+    }
+}
+
+// Workgroups of the kernel for few rows that a CU holds, by the registers it is built with.  In 4 bits three of 128
+// elements, or two of 256, fit with spills in the loop, and take 68 us against 67, and 168 against 136 (64 sequences of up
+// to 8,191 tokens).
+constexpr int few_resident(int head_dim) { return head_dim == 64 ? 3 : (head_dim <= 128 ? 2 : 1); }
 
 template <typename T, int D, bool WIN, bool FP4>
-__global__ __launch_bounds__(64 * kWaves, few_resident(D, FP4)) void tree_attention_kernel(AttnArgs g) {
+__global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_kernel(AttnArgs g) {
     constexpr int NT = 1;
     typedef Rows<T, D, NT, FP4> R;
     typedef typename R::V8 V8;
@@ -822,39 +903,70 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, FP4)) void tree_attent
     __shared__ uint64_t sums[kWaves];
     __shared__ uint32_t list[kListPages];
     __shared__ float merge[kWaves / 2 * R::kMergeFloats];
+    __shared__ __attribute__((aligned(16))) uint32_t spots[kWaves][WIN || FP4 ? kTile : 4];   // of a wave's next tile
 
-    const uint32_t wk = uniform(threadIdx.x >> 6), mine = blockIdx.x / g.heads, head = blockIdx.x % g.heads;
-    find_place<kWaves, WIN>(g, mine, &place, sums, known);
+    const uint32_t wk = uniform(threadIdx.x >> 6);
+    uint32_t mine = blockIdx.x / g.heads, head = blockIdx.x % g.heads;
+    if constexpr (FP4) {
+        // Pages by token: all heads of a share run on one XCD at about the same time, as their rows are neighbours of
+        // less than a line each.  64 sequences of up to 8,191 tokens 124 us to 87; pages by head 67, this way 70.
+        if (g.head_step < g.token_step) {
+            head = blockIdx.x / 8 % g.heads;
+            mine = blockIdx.x / 8 / g.heads * 8 + blockIdx.x % 8;
+        }
+        if (mine >= (g.budget != 0 ? g.budget : g.batch))
+            return;
+    }
+    find_place<kWaves, WIN, FP4>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
     for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end;
             at.batch++) {
         const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-        const Part<WIN> w(g, at, mine, known, 64 * kWaves);
+        const Part<WIN, FP4> w(g, at, mine, known, 64 * kWaves);
         at.start = w.end;
         note_splits(g, w, head, 0);
+        R rows;
+        if constexpr (FP4)   // on its way while the pages are read
+            rows.open(g, w.b, head, 0, lane);
         const Keys<kWaves, WIN, FP4> keys(g, w, head, list);
         const uint32_t c0 = w.c0, c1 = w.c1;
-        R rows;
-        rows.open(g, keys.b, head, 0, lane);
+        if constexpr (!FP4)
+            rows.open(g, keys.b, head, 0, lane);
         __syncthreads();
 
         const uint64_t k_pool = reinterpret_cast<uint64_t>(g.k_cache), v_pool = reinterpret_cast<uint64_t>(g.v_cache);
-        Held<T, D, FP4> held;
-        // tokens first .. first + 31, those past the chunk its last one
-        const auto load_ctx_k = [&](uint32_t first) {
-            held.load_k(k_pool + keys.offset_of(min(first + n, c1 - 1)),
-                    k_pool + keys.offset_of(min(first + 16 + n, c1 - 1)), q4);
+        // 4 bits: two tiles are on their way, as a tile is a quarter of the bytes
+        constexpr int kAhead = 1;
+        Held<T, D, FP4> waiting[kAhead];
+        Held<T, D, FP4> &held = waiting[0];
+        // Tokens first .. first + 31, those past the chunk its last one.  Where finding a place counts, each lane finds
+        // that of token first + lane % 32, and all have them from LDS: ten times some 15 instructions of a tile become once.
+        constexpr bool kShare = WIN || FP4;
+        const auto find = [&](uint32_t first) {
+            if constexpr (kShare)
+                spots[wk][lane & 31] = keys.place_of(min(first + (lane & 31), c1 - 1));
         };
-        const auto load_ctx_v = [&](uint32_t first) {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                held.load_v(i, v_pool + keys.offset_of(min(first + key_of(q4, i), c1 - 1)), n);
+        const auto load_ctx_k = [&](Held<T, D, FP4> &h, uint32_t first) {
+            if constexpr (kShare)
+                h.load_k(k_pool + (uint64_t)spots[wk][n] * keys.kPiece,
+                        k_pool + (uint64_t)spots[wk][16 + n] * keys.kPiece, q4);
+            else
+                h.load_k(k_pool + keys.offset_of(min(first + n, c1 - 1)),
+                        k_pool + keys.offset_of(min(first + 16 + n, c1 - 1)), q4);
         };
-        const auto key = [&](int k, V8 *x) {
+        const auto load_ctx_v = [&](Held<T, D, FP4> &h, uint32_t first) {
+            if constexpr (kShare) {
+                const u32x4 at0 = *reinterpret_cast<const u32x4 *>(&spots[wk][key_of(q4, 0)]),
+                            at1 = *reinterpret_cast<const u32x4 *>(&spots[wk][key_of(q4, 4)]);
 #pragma unroll
-            for (int i = 0; i < 4 && k + i / 2 < KS; i++)
-                x[i] = __builtin_bit_cast(V8, held.key(i % 2, k + i / 2, q4));
+                for (int i = 0; i < 8; i++)
+                    h.load_v(i, v_pool + (uint64_t)(i < 4 ? at0[i] : at1[i - 4]) * keys.kPiece, n);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    h.load_v(i, v_pool + keys.offset_of(min(first + key_of(q4, i), c1 - 1)), n);
+            }
         };
         // element j + e of the lane's D/16 elements of keys 2i and 2i + 1 side by side
         const auto pair_up = [&](int j, V8 *x, auto value) {
@@ -868,102 +980,114 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, FP4)) void tree_attent
                 x[e] = __builtin_bit_cast(V8, y);
             }
         };
-        const auto values = [&](int j, V8 *x) {
-            pair_up(j, x, [&](int i, int p) { return held.value(i, p, n); });
-        };
 
         // the chunk of the context
-        if (c1 > c0 + wk * kTile) {
-            load_ctx_k(c0 + wk * kTile);
-            load_ctx_v(c0 + wk * kTile);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const uint32_t first = c0 + (i * kWaves + wk) * kTile;
+            if (first < c1) {
+                find(first);
+                load_ctx_k(waiting[i], first);
+                load_ctx_v(waiting[i], first);
+            }
         }
+        if constexpr (FP4)   // while the first tiles are on their way
+            if (w.last)
+                single_keys<T, D, R>(g, keys, w.seq, rows,
+                        reinterpret_cast<uint64_t>(g.k) + w.b * g.k_stride[0] + head * g.k_stride[2],
+                        reinterpret_cast<uint64_t>(g.v) + w.b * g.v_stride[0] + head * g.v_stride[2], wk, n, q4);
         f32x4 score[NT][2];
         float tops[NT];
 #pragma unroll 1
-        for (uint32_t first = c0 + wk * kTile; first < c1; first += kWaves * kTile) {
-            const uint32_t next = first + kWaves * kTile;
-            const bool some = first + kTile > c1;
-            const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
-                    score, tops);
-            if (next < c1)
-                load_ctx_k(next);
-            if (some) {
-                // values of keys past the end meet weights of 0 and have to be finite: 0
+        for (uint32_t first0 = c0 + wk * kTile; first0 < c1; first0 += kAhead * kWaves * kTile) {
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    held.clear_v(i, key_of(q4, i) < c1 - first);
+            for (int a = 0; a < kAhead; a++) {
+                const uint32_t first = first0 + a * kWaves * kTile, next = first + kAhead * kWaves * kTile;
+                if (a > 0 && first >= c1)
+                    break;
+                Held<T, D, FP4> &h = waiting[a];
+                const auto key = [&](int k, V8 *x) {
+#pragma unroll
+                    for (int i = 0; i < 4 && k + i / 2 < KS; i++)
+                        x[i] = __builtin_bit_cast(V8, h.key(i % 2, k + i / 2, q4));
+                };
+                const auto values = [&](int j, V8 *x) {
+                    pair_up(j, x, [&](int i, int p) { return h.value(i, p, n); });
+                };
+                const bool some = first + kTile > c1;
+                const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
+                        score, tops);
+                // Past the end the last key once more: with a branch here, or below, the compiler no longer knows how many loads
+                // are on their way after the keys', and waits for the values as well before the first product.
+                if (kShare || next < c1) {
+                    find(next);
+                    load_ctx_k(h, next);
+                }
+                if (some) {
+                    // values of keys past the end meet weights of 0 and have to be finite: 0
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        h.clear_v(i, key_of(q4, i) < c1 - first);
+                }
+                if (raise)
+                    rows.raise_maxima(g, tops);
+                rows.apply(g, score, values);
+                if (kShare || next < c1)
+                    load_ctx_v(h, next);
             }
-            if (raise)
-                rows.raise_maxima(g, tops);
-            rows.apply(g, score, values);
-            if (next < c1)
-                load_ctx_v(next);
         }
 
         // the drafted nodes, and before them the zone, with the sequence's last chunk
-        if (w.last) {
-            const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
-            const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
-            const uint32_t count = keys.count, special = w.seq.special(), room = special - count;
-            // in 16 bits, whatever the cache holds; h: the registers that the context's tiles had, where those are alike
-            const auto special_keys = [&](Held<T, D, false> &h) {
+        if constexpr (!FP4)
+            if (w.last) {
+                const uint64_t kb = reinterpret_cast<uint64_t>(g.k) + keys.b * g.k_stride[0] + head * g.k_stride[2];
+                const uint64_t vb = reinterpret_cast<uint64_t>(g.v) + keys.b * g.v_stride[0] + head * g.v_stride[2];
+                const uint32_t count = keys.count, special = w.seq.special(), room = special - count;
                 for (uint32_t first = wk * kTile; first < special; first += kWaves * kTile) {
                     const bool in_zone = WIN && first < room;   // room is whole tiles
-                    const uint32_t begin = in_zone ? first : first - room;
+                    const uint32_t begin = in_zone ? first : first - room, end = in_zone ? zone_of(w.seq) : count;
+                    // Of key u, and of its values.
+                    const auto key_row = [&](uint32_t u) {
+                        if constexpr (WIN)
+                            if (in_zone)
+                                return k_pool + keys.offset_in_zone(min(u, end - 1));
+                        return kb + min(u, end - 1) * g.k_stride[1];
+                    };
+                    const auto value_row = [&](uint32_t u) {
+                        if constexpr (WIN)
+                            if (in_zone)
+                                return v_pool + keys.offset_in_zone(min(u, end - 1));
+                        return vb + min(u, end - 1) * g.v_stride[1];
+                    };
+                    held.load_k(key_row(begin + n), key_row(begin + 16 + n), q4);
                     // A value that is not finite would turn a weight of 0 into NaN: here it counts
                     // as 0, and the rows that do see it get it added afterwards.
-                    uint32_t wild = 0, bits[NT];
-                    if (in_zone) {
-                        if constexpr (WIN) {
-                            const uint32_t zone = w.seq.zone;
-                            held.load_k(k_pool + keys.offset_in_zone(min(begin + n, zone - 1)),
-                                    k_pool + keys.offset_in_zone(min(begin + 16 + n, zone - 1)), q4);
+                    uint32_t wild = 0;
 #pragma unroll
-                            for (int s = 0; s < KS; s++)
+                    for (int i = 0; i < 8; i++) {
+                        const uint32_t u = begin + key_of(q4, i);
+                        held.load_v(i, value_row(u), n);
 #pragma unroll
-                                for (int z = 0; z < 2; z++) {
-                                    const u32x4 x = held.key(z, s, q4);
-                                    h.kr[z][s][0] = x.x, h.kr[z][s][1] = x.y, h.kr[z][s][2] = x.z, h.kr[z][s][3] = x.w;
-                                }
+                        for (int j = 0; j < DJ / 2; j++)
+                            held.vr[i][j] = tamed<T>(u < end ? held.vr[i][j] : 0, &wild);
+                    }
+                    uint32_t bits[NT];
 #pragma unroll
-                            for (int i = 0; i < 8; i++) {
-                                const uint32_t u = begin + key_of(q4, i);
-                                held.load_v(i, v_pool + keys.offset_in_zone(min(u, zone - 1)), n);
-#pragma unroll
-                                for (int j = 0; j < DJ / 2; j++)
-                                    h.vr[i][j] = tamed<T>(u < zone ? held.value(i, j, n) : 0, &wild);
-                            }
-#pragma unroll
-                            for (int t = 0; t < NT; t++)
+                    for (int t = 0; t < NT; t++) {
+                        bits[t] = 0;
+                        if constexpr (WIN)
+                            if (in_zone)
                                 bits[t] = keys.seen_in_zone(t * 16 + n, begin);
-                        }
-                    } else {
-                        const uint64_t at0 = kb + min(begin + n, count - 1) * g.k_stride[1] + R::lane_at(q4),
-                                       at1 = kb + min(begin + 16 + n, count - 1) * g.k_stride[1] + R::lane_at(q4);
-#pragma unroll
-                        for (int s = 0; s < KS; s++) {
-                            load_dwords<4>(h.kr[0][s], at0 + s * R::kStepBytes);
-                            load_dwords<4>(h.kr[1][s], at1 + s * R::kStepBytes);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const uint32_t u = begin + key_of(q4, i);
-                            load_dwords<DJ / 2>(h.vr[i], vb + min(u, count - 1) * g.v_stride[1] + n * (2 * DJ));
-#pragma unroll
-                            for (int j = 0; j < DJ / 2; j++)
-                                h.vr[i][j] = tamed<T>(u < count ? h.vr[i][j] : 0, &wild);
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; t++)
+                        if (!in_zone)
                             bits[t] = keys.seen(t * 16 + n, begin);
                     }
                     const auto key16 = [&](int k, V8 *x) {
 #pragma unroll
                         for (int i = 0; i < 4 && k + i / 2 < KS; i++)
-                            x[i] = __builtin_bit_cast(V8, h.key(i % 2, k + i / 2, q4));
+                            x[i] = __builtin_bit_cast(V8, held.key(i % 2, k + i / 2, q4));
                     };
                     const auto values16 = [&](int j, V8 *x) {
-                        pair_up(j, x, [&](int i, int p) { return h.value(i, p, n); });
+                        pair_up(j, x, [&](int i, int p) { return held.value(i, p, n); });
                     };
                     if (rows.scores(g, true, key16, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
                             score, tops))
@@ -971,27 +1095,10 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D, FP4)) void tree_attent
                     rows.apply(g, score, values16);
                     if (__any(wild))
                         rows.add_wild(
-                            [&](uint32_t u, uint32_t e) {
-                                uint64_t row = vb + u * g.v_stride[1];
-                                if constexpr (WIN)
-                                    if (in_zone) {
-                                        row = v_pool + keys.offset_in_zone(u);
-                                        if constexpr (FP4)
-                                            return fp4_number<D>(row, e);
-                                    }
-                                return (float)reinterpret_cast<const T *>(row)[e];
-                            },
-                            begin, min(begin + kTile, in_zone ? zone_of(w.seq) : count), bits,
-                            [&](int j, int r) { return (4 * q4 + r) * DJ + j; });
+                            [&](uint32_t u, uint32_t e) { return (float)reinterpret_cast<const T *>(value_row(u))[e]; },
+                            begin, min(begin + kTile, end), bits, [&](int j, int r) { return (4 * q4 + r) * DJ + j; });
                 }
-            };
-            if constexpr (FP4) {
-                Held<T, D, false> own;
-                special_keys(own);
-            } else {
-                special_keys(held);
             }
-        }
 
         rows.template join<1, kWaves>(g, merge, wk, lane);
         if (wk == 0)
@@ -1074,13 +1181,13 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
     const uint32_t mine = unit / g.heads, head = unit % g.heads;
     if (mine >= (g.budget != 0 ? g.budget : g.batch))
         return;
-    find_place<kSharedWaves, WIN>(g, mine, &place, sums, known);
+    find_place<kSharedWaves, WIN, FP4>(g, mine, &place, sums, known);
     Place at = {uniform(place.start), uniform(place.share), uniform(place.batch)};
 #pragma unroll 1
     for (uint64_t end = at.share == kWhole ? kWhole : (mine + 1) * at.share; at.batch < g.batch && at.start < end;
             at.batch++) {
         const uint32_t thread = anew(threadIdx.x), lane = thread & 63, n = lane & 15, q4 = lane >> 4;
-        const Part<WIN> w(g, at, mine, known, kThreads);
+        const Part<WIN, FP4> w(g, at, mine, known, kThreads);
         at.start = w.end;
         note_splits(g, w, head, block);
         const Keys<kSharedWaves, WIN, FP4> keys(g, w, head, list);

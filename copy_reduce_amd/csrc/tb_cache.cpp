@@ -289,7 +289,7 @@ static bool attn_sizes_ok(const tb_tree_attn *a, const tb_cache *c) {
            (a->head_dim == 64 || a->head_dim == 96 || a->head_dim == 128 || a->head_dim == 256);
 }
 
-static int attention_workspace(const tb_tree_attn *a, bool fp4, const tb_cache *c, uint64_t *bytes_out) {
+static int attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64_t *bytes_out) {
     if (bytes_out == nullptr || !attn_sizes_ok(a, c))
         return TB_ERR_INVALID;
     *bytes_out = 0;
@@ -298,7 +298,7 @@ static int attention_workspace(const tb_tree_attn *a, bool fp4, const tb_cache *
     int cus = 0;
     const int rc = tbh::cu_count_of_device(&cus);
     if (rc == TB_OK)
-        *bytes_out = tbk::tree_attention_workspace(*a, c->heads, fp4, cus);
+        *bytes_out = tbk::tree_attention_workspace(*a, c->heads, cus);
     return rc;
 }
 
@@ -336,14 +336,14 @@ static int attention(const tb_tree_attn *a, const tb_attn_view &view, const tb_c
     const int rc = tbh::cu_count_of_device(&cus);
     if (rc != TB_OK)
         return rc;
-    if (a->workspace_bytes < tbk::tree_attention_workspace(args, c->heads, fp4, cus))
+    if (a->workspace_bytes < tbk::tree_attention_workspace(args, c->heads, cus))
         return TB_ERR_INVALID;
     const hipError_t e = tbk::launch_tree_attention(args, view, *c, cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? TB_OK : hip_fail(e, "tree attention launch");
 }
 
 int tb_tree_attention_workspace(const tb_tree_attn *a, const tb_cache *c, uint64_t *bytes_out) {
-    return attention_workspace(a, false, c, bytes_out);
+    return attention_workspace(a, c, bytes_out);
 }
 
 int tb_tree_attention(const tb_tree_attn *a, const tb_cache *c, void *stream) {
@@ -354,7 +354,7 @@ int tb_view_attention_workspace(const tb_tree_attn *a, const tb_attn_view *view,
                                 uint64_t *bytes_out) {
     if (view == nullptr || view->fp4 > 1)
         return TB_ERR_INVALID;
-    return attention_workspace(a, view->fp4 != 0, c, bytes_out);
+    return attention_workspace(a, c, bytes_out);
 }
 
 int tb_view_attention(const tb_tree_attn *a, const tb_attn_view *view, const tb_cache *c, void *stream) {

@@ -135,7 +135,7 @@ __host__ __device__ inline uint64_t units_of_share(uint64_t units, uint32_t budg
 
 hipError_t launch_tree_attention(const tb_tree_attn &a, const tb_attn_view &view, const tb_cache &c, int cu_count,
                                  hipStream_t stream);
-uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, bool fp4, int cu_count);
+uint64_t tree_attention_workspace(const tb_tree_attn &a, uint32_t heads, int cu_count);
 
 // Tokens in 4 bits: rows of dim elements a head, rounded to the cache's or read from it.
 struct Fp4Args {

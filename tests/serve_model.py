@@ -12,27 +12,25 @@ def head_bytes(dim):
 
 
 def encode(x):
-    """x [..., dim] of 16 bits -> uint8 [..., head_bytes(dim)], element by element."""
+    """x [..., dim] of 16 bits -> uint8 [..., head_bytes(dim)]: the smallest power with max < 7 * 2^e, the nearest of the
+    eight steps by distance, of two the even code."""
     dim, (low, high) = x.shape[-1], LIMITS[x.dtype]
-    rows = x.reshape(-1, dim).double().tolist()
-    out = torch.zeros(len(rows), head_bytes(dim), dtype=torch.uint8)
-    for r, row in enumerate(rows):
-        for b in range(dim // 32):
-            block = row[32 * b:32 * b + 32]
-            if not all(math.isfinite(v) for v in block):
-                out[r, dim // 2 + b] = 255
-                continue
-            top = max(abs(v) for v in block)
-            e = low
-            while e < high and top >= 7 * 2.0 ** e:
-                e += 1
-            out[r, dim // 2 + b] = e + 127
-            for i, v in enumerate(block):
-                a = abs(v) / 2.0 ** e
-                best = min(range(8), key=lambda c: (abs(STEPS[c] - a), c % 2))
-                code = best + (8 if math.copysign(1, v) < 0 else 0)
-                out[r, 16 * b + i // 2] |= code << (4 * (i % 2))
-    return out.view(*x.shape[:-1], -1)
+    y = x.reshape(-1, dim // 32, 32).double()
+    wild = ~torch.isfinite(y).all(2)
+    y = torch.where(wild[:, :, None], 0.0, y)
+    top = y.abs().amax(2)
+    e = torch.full(top.shape, low)
+    for _ in range(low, high):
+        e += (top >= 7 * torch.exp2(e.double())) & (e < high)
+    a = y.abs() / torch.exp2(e.double())[:, :, None]
+    off = (a[..., None] - torch.tensor(STEPS, dtype=torch.float64)).abs()
+    near = off == off.amin(3, keepdim=True)
+    best = torch.where(near & (torch.arange(8) % 2 == 0), 2, near.int()).argmax(3)   # the even one of two
+    code = (best + 8 * torch.signbit(y)).flatten(1).to(torch.uint8)
+    code = torch.where(wild.repeat_interleave(32, 1), 0, code)
+    powers = torch.where(wild, 255, e + 127).to(torch.uint8)
+    pad = torch.zeros(len(code), head_bytes(dim) - dim // 2 - dim // 32, dtype=torch.uint8)
+    return torch.cat([code[:, 0::2] | code[:, 1::2] << 4, powers, pad], 1).view(*x.shape[:-1], -1)
 
 
 def decode(raw, dim):
