@@ -78,73 +78,98 @@ __device__ __forceinline__ uint32_t power_byte(uint32_t top) {
     return (uint32_t)min(max(e, Type16<T>::kLow), Type16<T>::kHigh);
 }
 
-// A thread has 8 elements of one token in kFp4Pools pools, four threads a block of 32.  The conversion to 4 bits is the
-// hardware's: to the nearest, of two the even code, larger ones to 6.
-constexpr int kFp4Pools = 4;
+// A thread has 8 elements of one token, four threads a block of 32, and goes over pools, kFp4Pools at a time, those
+// blockIdx.y * kFp4Pools on, while the next ones' elements are on their way; the first are asked for while the page is found, four
+// loads one after the other.  The conversion to 4 bits is the hardware's: to the nearest, of two the even code,
+// larger ones to 6.
+constexpr uint32_t kFp4Pools = 4, kTokenBlocks = 4096;
+// Workgroups that go over the same tokens, in y: so many that the chip has work for some rounds.
+static dim3 token_grid(uint32_t n, uint32_t parts, uint32_t npools) {
+    const uint64_t blocks = ((uint64_t)n * parts + 255) / 256, most = 1u << 22;
+    const uint32_t x = (uint32_t)(blocks < most ? blocks : most), each = (npools + kFp4Pools - 1) / kFp4Pools;
+    const uint32_t y = (kTokenBlocks + x - 1) / x;
+    return dim3(x, y < each ? y : each, 1);
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void fp4_append_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
         uint32_t npools) {
     constexpr uint32_t U = kFp4Pools;
     const uint64_t all = (uint64_t)a.n * parts;
-    const uint32_t pool = blockIdx.y * U, of_head = a.dim / 8;
+    const uint32_t of_head = a.dim / 8;
     const bool whole = 64 % of_head == 0;   // no head lies in two waves
     for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
         const int32_t q = a.seqs[i];
+        const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
         if (q < 0)
             continue;
-        const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
+        const uint64_t src = a.rows + row * a.row_stride + part * 16ull;
+        const bool there = row < a.nrows;
+        const auto load = [&](uint32_t pool, u32x4 *x) {
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++)
+                if (there && pool + u < npools)
+                    x[u] = __builtin_nontemporal_load((const gu32x4_at2 *)(src + (pool + u) * a.pool_stride));
+        };
+        u32x4 x[U], next[U];
+        uint32_t pool = blockIdx.y * U;
+        load(pool, x);
         TokenPlace to = place_of_token(s, q, a.positions[i], a.page_stride, a.token_step, true);
-        if (row >= a.nrows)
+        if (!there)
             to.flag = TB_CACHE_RANGE;
         if (to.flag != 0) {
             if (part == 0 && blockIdx.y == 0)
                 atomicOr(&s.counts[1], to.flag);
             continue;
         }
-        const uint64_t src = a.rows + pool * a.pool_stride + row * a.row_stride + part * 16ull;
         const uint64_t dst = to.at + head * a.head_step;
-        u32x4 x[U];
+        for (;;) {
+            const uint32_t after = pool + gridDim.y * U;
+            load(after, next);   // past the last: none
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++)
-            if (pool + u < npools)
-                x[u] = *(const gu32x4_at2 *)(src + u * a.pool_stride);
+            for (uint32_t u = 0; u < U; u++) {
+                if (pool + u >= npools)
+                    break;
+                u16x2 m = {0, 0};
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            if (pool + u >= npools)
-                break;
-            u16x2 m = {0, 0};
+                for (int e = 0; e < 4; e++)
+                    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[u][e] & 0x7fff7fffu));
+                uint32_t top = max((uint32_t)m.x, (uint32_t)m.y);
+                top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+                top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+                const uint32_t byte = power_byte<T>(top);
+                const float power = __uint_as_float(byte << 23);
+                uint32_t code = Type16<T>::template round<0>(0, x[u][0], power);
+                code = Type16<T>::template round<1>(code, x[u][1], power);
+                code = Type16<T>::template round<2>(code, x[u][2], power);
+                code = Type16<T>::template round<3>(code, x[u][3], power);
+                const uint64_t place = pools.dst[pool + u] + dst;
+                *(gu32 *)(place + in_head * 4) = byte == 255 ? 0 : code;
+                const uint32_t block = in_head / 4, blocks = of_head / 4;
+                if (whole) {   // a word of powers, from the first of its blocks' threads
+                    uint32_t word = byte;
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[u][e] & 0x7fff7fffu));
-            uint32_t top = max((uint32_t)m.x, (uint32_t)m.y);
-            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-            const uint32_t byte = power_byte<T>(top);
-            const float power = __uint_as_float(byte << 23);
-            uint32_t code = Type16<T>::template round<0>(0, x[u][0], power);
-            code = Type16<T>::template round<1>(code, x[u][1], power);
-            code = Type16<T>::template round<2>(code, x[u][2], power);
-            code = Type16<T>::template round<3>(code, x[u][3], power);
-            const uint64_t there = pools.dst[pool + u] + dst;
-            *(gu32 *)(there + in_head * 4) = byte == 255 ? 0 : code;
-            const uint32_t block = in_head / 4, blocks = of_head / 4;
-            if (whole) {   // a word of powers, from the first of its blocks' threads
-                uint32_t word = byte;
-#pragma unroll
-                for (int k = 1; k < 4; k++) {
-                    const uint32_t other = (uint32_t)__shfl_down((int)byte, 4 * k);
-                    word |= block + k < blocks ? other << (8 * k) : 0;
+                    for (int k = 1; k < 4; k++) {
+                        const uint32_t other = (uint32_t)__shfl_down((int)byte, 4 * k);
+                        word |= block + k < blocks ? other << (8 * k) : 0;
+                    }
+                    if (in_head % 16 == 0)
+                        *(gu32 *)(place + a.dim / 2 + block) = word;
+                } else if (in_head % 4 == 0) {
+                    *(gu8 *)(place + a.dim / 2 + block) = (uint8_t)byte;
+                    if (block + 1 == blocks)
+                        for (uint32_t k = blocks; k % 4 != 0; k++)
+                            *(gu8 *)(place + a.dim / 2 + k) = 0;
                 }
-                if (in_head % 16 == 0)
-                    *(gu32 *)(there + a.dim / 2 + block) = word;
-            } else if (in_head % 4 == 0) {
-                *(gu8 *)(there + a.dim / 2 + block) = (uint8_t)byte;
-                if (block + 1 == blocks)
-                    for (uint32_t k = blocks; k % 4 != 0; k++)
-                        *(gu8 *)(there + a.dim / 2 + k) = 0;
             }
+            if (after >= npools)
+                break;
+            pool = after;
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++)
+                x[u] = next[u];
         }
     }
 }
@@ -152,9 +177,8 @@ __global__ __launch_bounds__(256) void fp4_append_kernel(Pools pools, CacheState
 hipError_t launch_fp4_append(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
                              uint32_t dtype, hipStream_t stream) {
     const uint32_t parts = a.heads * (a.dim / 8);
-    const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
-    const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kFp4Pools - 1) / kFp4Pools, 1);
-    return launch(dtype == TB_BF16 ? fp4_append_kernel<__bf16> : fp4_append_kernel<_Float16>, grid, 256, stream,
+    return launch(dtype == TB_BF16 ? fp4_append_kernel<__bf16> : fp4_append_kernel<_Float16>,
+                  token_grid(a.n, parts, npools), 256, stream,
                   nullptr, pools, s, a, parts, npools);
 }
 
@@ -163,7 +187,7 @@ __global__ __launch_bounds__(256) void fp4_read_kernel(Pools pools, CacheState s
         uint32_t npools) {
     constexpr uint32_t U = kFp4Pools;
     const uint64_t all = (uint64_t)a.n * parts;
-    const uint32_t pool = blockIdx.y * U, of_head = a.dim / 8;
+    const uint32_t of_head = a.dim / 8;
     for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
@@ -171,30 +195,45 @@ __global__ __launch_bounds__(256) void fp4_read_kernel(Pools pools, CacheState s
         if (from.flag > 0 && part == 0 && blockIdx.y == 0)
             atomicOr(&s.counts[1], from.flag);
         const uint64_t src = from.at + head * a.head_step;
-        const uint64_t dst = a.rows + pool * a.pool_stride + i * a.row_stride + part * 16ull;
-        uint32_t code[U], byte[U];
+        const uint64_t dst = a.rows + i * a.row_stride + part * 16ull;
+        const auto load = [&](uint32_t pool, uint32_t *code, uint32_t *byte) {
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            code[u] = byte[u] = 0;
-            if (pool + u < npools && from.flag == 0) {
-                code[u] = *(const gu32 *)(pools.dst[pool + u] + src + in_head * 4);
-                byte[u] = *(const gu8 *)(pools.dst[pool + u] + src + a.dim / 2 + in_head / 4);
+            for (uint32_t u = 0; u < U; u++) {
+                code[u] = byte[u] = 0;
+                if (pool + u < npools && from.flag == 0) {
+                    code[u] = *(const gu32 *)(pools.dst[pool + u] + src + in_head * 4);
+                    byte[u] = *(const gu8 *)(pools.dst[pool + u] + src + a.dim / 2 + in_head / 4);
+                }
+            }
+        };
+        uint32_t code[U], byte[U], code2[U], byte2[U];
+        uint32_t pool = blockIdx.y * U;
+        load(pool, code, byte);
+        for (;;) {
+            const uint32_t after = pool + gridDim.y * U;
+            load(after, code2, byte2);
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++)
+                if (pool + u < npools)
+                    __builtin_nontemporal_store(eight_of<T>(code[u], power_of(byte[u], 0)),
+                            (gu32x4_at2 *)(dst + (pool + u) * a.pool_stride));
+            if (after >= npools)
+                break;
+            pool = after;
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                code[u] = code2[u];
+                byte[u] = byte2[u];
             }
         }
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++)
-            if (pool + u < npools)
-                *(gu32x4_at2 *)(dst + u * a.pool_stride) = eight_of<T>(code[u], power_of(byte[u], 0));
     }
 }
 
 hipError_t launch_fp4_read(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
                            uint32_t dtype, hipStream_t stream) {
     const uint32_t parts = a.heads * (a.dim / 8);
-    const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
-    const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kFp4Pools - 1) / kFp4Pools, 1);
-    return launch(dtype == TB_BF16 ? fp4_read_kernel<__bf16> : fp4_read_kernel<_Float16>, grid, 256, stream, nullptr,
-                  pools, s, a, parts, npools);
+    return launch(dtype == TB_BF16 ? fp4_read_kernel<__bf16> : fp4_read_kernel<_Float16>,
+                  token_grid(a.n, parts, npools), 256, stream, nullptr, pools, s, a, parts, npools);
 }
 
 // The bytes of tokens out of their pages: E bytes of one token in kFp4Pools pools a thread.
