@@ -1127,8 +1127,11 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
 // rows' worth of registers in the kernel for few.
 constexpr int kSharedWaves = 8;
 constexpr int shared_nt(int head_dim) { return head_dim <= 128 ? 2 : 1; }
-// Keys of a step: a tile at least for each wave that divides them, whole pieces for each thread.
-constexpr int shared_step(int head_dim, int wm) { return head_dim < 128 || wm == 2 ? 128 : 64; }
+// Keys of a step: a tile at least for each wave that divides them, whole pieces for each thread.  In 4 bits, where a
+// step ends with its unpacking, 128 where LDS has room: the trees 220 us against 227.
+constexpr int shared_step(int head_dim, int wm, bool fp4) {
+    return head_dim < 128 || wm == 2 || (fp4 && head_dim == 128) ? 128 : 64;
+}
 
 // Place of a piece in its key's row of D / 8. The first product reads one piece of sixteen keys at
 // once (of keys 0 to 3 and 12 to 15 together with the neighbouring piece of 4 to 11), the second two
@@ -1155,7 +1158,7 @@ __device__ __forceinline__ uint32_t piece_at_place(uint32_t key, uint32_t place)
 
 template <typename T, int D, int WM, bool WIN, bool FP4>
 __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_kernel(AttnArgs g) {
-    constexpr int NT = shared_nt(D), kStep = shared_step(D, WM), WK = kSharedWaves / WM;
+    constexpr int NT = shared_nt(D), kStep = shared_step(D, WM, FP4), WK = kSharedWaves / WM;
     constexpr int kThreads = 64 * kSharedWaves, kPieces = D / 8, kEach = kStep * kPieces / kThreads;
     static_assert(kStep * kPieces % kThreads == 0 && kStep % (WK * kTile) == 0, "step");
     typedef Rows<T, D, NT, false> R;

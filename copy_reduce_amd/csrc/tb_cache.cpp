@@ -85,7 +85,7 @@ bool pages_aligned(const tb_cache *c, uint64_t bytes) {
     return true;
 }
 
-// Calls launch_one(pools, npools, shape, fit, last) for the pools of both caches, kPoolsPerLaunch at a time (once,
+// Calls launch_one(pools, npools, shape, piece, last) for the pools of both caches, kPoolsPerLaunch at a time (once,
 // with none, for caches without pools).  `parts`: the used tokens of a head-major page are a stretch a head.
 template <typename Launch>
 hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launch launch_one) {
@@ -99,12 +99,14 @@ hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launc
     parts = parts && dst->layout == TB_CACHE_HEAD_MAJOR;
     g.runs = parts ? dst->heads : 1;
     g.token_bytes = (uint32_t)(parts ? dst->head_bytes : token_bytes(dst));
-    const bool fit = (whole ? page_bytes(dst) : g.token_bytes) % 16 == 0 && pages_aligned(dst, 16)
-            && pages_aligned(src, 16);
+    uint32_t piece = 1;
+    for (uint32_t w : {4u, 16u})
+        if ((whole ? page_bytes(dst) : g.token_bytes) % w == 0 && pages_aligned(dst, w) && pages_aligned(src, w))
+            piece = w;
     if (dst->npools == 0) {   // what rides along with the copy has to run all the same; no page is in range
         g.src_pages = g.dst_pages = 0;
         const tbk::Pools none = {};
-        return launch_one(none, 1, g, true, true);
+        return launch_one(none, 1, g, 16u, true);
     }
     uint32_t p0 = 0;
     do {
@@ -115,7 +117,7 @@ hipError_t for_pools(const tb_cache *dst, const tb_cache *src, bool parts, Launc
             pools.dst[p] = reinterpret_cast<uintptr_t>(dst->pools[p0 + p]);
         }
         p0 += n;
-        const hipError_t e = launch_one(pools, n, g, fit, p0 == dst->npools);
+        const hipError_t e = launch_one(pools, n, g, piece, p0 == dst->npools);
         if (e != hipSuccess)
             return e;
     } while (p0 < dst->npools);
@@ -153,10 +155,10 @@ int tb_page_copy(const tb_cache *dst, const tb_cache *src, const int32_t *dst_pa
     tbk::PagePairs pairs = {src_pages, dst_pages, nullptr, nullptr, n};
     tbk::LaunchSeq seq;
     const hipError_t e = for_pools(dst, src, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g,
-            bool fit, bool last) {
+            uint32_t piece, bool last) {
         if (last)
             seq.last();
-        return tbk::launch_page_copy(pools, np, g, pairs, fit, static_cast<hipStream_t>(stream));
+        return tbk::launch_page_copy(pools, np, g, pairs, piece, static_cast<hipStream_t>(stream));
     });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page copy launch");
 }
@@ -224,11 +226,11 @@ int tb_page_fork(const tb_cache *cache, const int32_t *parents, const int32_t *c
     hipError_t e = tbk::launch_fork_plan(s, parents, children, n, st);
     const tbk::PagePairs pairs = {s.w.from, s.w.to, s.w.aux, nullptr, n};
     if (e == hipSuccess)
-        e = for_pools(cache, cache, true, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g, bool fit,
-                bool last) {
+        e = for_pools(cache, cache, true, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g,
+                uint32_t piece, bool last) {
             if (last)
                 seq.last();
-            return tbk::launch_fork_copy(pools, np, g, pairs, fit, s, parents, children, n, last, st);
+            return tbk::launch_fork_copy(pools, np, g, pairs, piece, s, parents, children, n, last, st);
         });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page fork launch");
 }
@@ -254,10 +256,10 @@ int tb_page_compact(const tb_cache *cache, void *stream) {
     const tbk::PagePairs pairs = {s.w.from, s.w.to, nullptr, s.w.pairs, cache->num_pages / 2};
     if (e == hipSuccess)
         e = for_pools(cache, cache, false, [&](const tbk::Pools &pools, uint32_t np, const tbk::PageShape &g,
-                bool fit, bool last) {
+                uint32_t piece, bool last) {
             if (last)
                 seq.last();
-            return tbk::launch_compact_copy(pools, np, g, pairs, fit, s, last, st);
+            return tbk::launch_compact_copy(pools, np, g, pairs, piece, s, last, st);
         });
     return e == hipSuccess ? TB_OK : hip_fail(e, "page compact launch");
 }

@@ -108,8 +108,9 @@ struct AppendArgs {
 };
 
 hipError_t launch_cache_init(const CacheState &s, hipStream_t stream);
+// piece of a copy: 16, 4 or 1 bytes, what every address and every run's tokens (or whole pages) are multiples of.
 hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
-                            bool aligned16, hipStream_t stream);
+                            uint32_t piece, hipStream_t stream);
 // piece: 16, 4 or 1 bytes, what every address and a head are multiples of.
 hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a,
                          uint32_t piece, hipStream_t stream);
@@ -117,14 +118,14 @@ hipError_t launch_append(const Pools &pools, uint32_t npools, const CacheState &
 hipError_t launch_fork_plan(const CacheState &s, const int32_t *parents, const int32_t *children, uint32_t n,
                             hipStream_t stream);
 hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
-                            bool aligned16, const CacheState &s, const int32_t *parents, const int32_t *children,
+                            uint32_t piece, const CacheState &s, const int32_t *parents, const int32_t *children,
                             uint32_t n, bool rows, hipStream_t stream);
 hipError_t launch_resize(const CacheState &s, const int32_t *seqs, const int32_t *lens, uint32_t n,
                          hipStream_t stream);
 // A compaction: its plan, then its pages and, with the launch that has `apply`, its tables.
 hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream);
 hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &shape, const PagePairs &pairs,
-                               bool aligned16, const CacheState &s, bool apply, hipStream_t stream);
+                               uint32_t piece, const CacheState &s, bool apply, hipStream_t stream);
 
 // The attention's share of a stream of `units`: a `budget`-th, rounded up.  A division of 32 bits where that is enough,
 // as it nearly always is.

@@ -111,8 +111,8 @@ __device__ void compact_apply(const Rider &r, uint32_t block, uint32_t blocks);
 // end only) go in small workgroups, of which those behind the end do nothing, and are loaded
 // through the caches, several children reading one page: 192 such pages of 32 KiB in 32 pools in 24 us;
 // nt loads 46 us for the whole call against 34.
-// E is 16, or 1 where pages (a fork's heads) are no multiple of 16 bytes or do not begin at one: pages of 8,190 bytes
-// take 470 us where those of 8,192 take 163.
+// E is what pages (a fork's heads) are a multiple of and begin at: 16, 4 as in a cache held in 4 bits, where a load of 16
+// bytes is one all the same, or 1: pages of 8,190 bytes take 470 us where those of 8,192 take 163.
 template <int E, int TH, int U, int LD, int ST, int WITH>
 __global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g, PagePairs pairs, uint32_t blocks,
         Rider rider) {
@@ -155,6 +155,15 @@ __global__ __launch_bounds__(TH) void page_copy_kernel(Pools pools, PageShape g,
 #pragma unroll
             for (int u = 0; u < U; u++)
                 __builtin_amdgcn_raw_buffer_store_b128(v[u], out, threadIdx.x * 16, u * TH * 16, ST);
+        } else if constexpr (E == 4) {
+            typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+            typedef __attribute__((address_space(1))) u32x4_at4 gu32x4_at4;
+            typedef __attribute__((address_space(1))) uint32_t gu32;
+            const uint32_t whole = left / 16 * 16;
+            for (uint32_t k = threadIdx.x * 16; k < whole; k += TH * 16)
+                *(gu32x4_at4 *)(dst + k) = *(const gu32x4_at4 *)(src + k);
+            for (uint32_t k = whole + threadIdx.x * 4; k < left; k += TH * 4)
+                *(gu32 *)(dst + k) = *(const gu32 *)(src + k);
         } else {
             for (uint32_t k = threadIdx.x; k < left; k += TH)
                 *(gu8 *)(dst + k) = *(const gu8 *)(src + k);
@@ -186,8 +195,10 @@ static hipError_t launch_copy(const Pools &pools, uint32_t npools, const PageSha
 // and 168, 434 and 188.  (64 threads with one load: 152 to 177 and 182 to 190; 128: 150 to 167, 172 to 197.)
 template <int WITH>
 static hipError_t launch_whole(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
-                               const Rider &rider, bool aligned16, hipStream_t stream) {
-    if (!aligned16)
+                               const Rider &rider, uint32_t piece, hipStream_t stream) {
+    if (piece == 4)
+        return launch_copy<4, 256, 1, 0, 0, WITH>(pools, npools, g, pairs, rider, stream);
+    if (piece != 16)
         return launch_copy<1, 256, 4, 0, 0, WITH>(pools, npools, g, pairs, rider, stream);
     if ((uint64_t)g.page_tokens * g.token_bytes < 16 * 512)
         return launch_copy<16, 64, 2, 2, 19, WITH>(pools, npools, g, pairs, rider, stream);
@@ -195,8 +206,8 @@ static hipError_t launch_whole(const Pools &pools, uint32_t npools, const PageSh
 }
 
 hipError_t launch_page_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
-                            bool aligned16, hipStream_t stream) {
-    return launch_whole<kAlone>(pools, npools, g, pairs, Rider(), aligned16, stream);
+                            uint32_t piece, hipStream_t stream) {
+    return launch_whole<kAlone>(pools, npools, g, pairs, Rider(), piece, stream);
 }
 
 // ---- append --------------------------------------------------------------------
@@ -376,11 +387,12 @@ hipError_t launch_fork_plan(const CacheState &s, const int32_t *parents, const i
 }
 
 hipError_t launch_fork_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
-                            bool aligned16, const CacheState &s, const int32_t *parents, const int32_t *children,
+                            uint32_t piece, const CacheState &s, const int32_t *parents, const int32_t *children,
                             uint32_t n, bool rows, hipStream_t stream) {
     const Rider rider = {s, parents, children, rows ? n : 0};
-    return aligned16 ? launch_copy<16, 64, 4, 0, 2, kWithFork>(pools, npools, g, pairs, rider, stream)
-                     : launch_copy<1, 256, 4, 0, 0, kWithFork>(pools, npools, g, pairs, rider, stream);
+    return piece == 16  ? launch_copy<16, 64, 4, 0, 2, kWithFork>(pools, npools, g, pairs, rider, stream)
+           : piece == 4 ? launch_copy<4, 64, 4, 0, 0, kWithFork>(pools, npools, g, pairs, rider, stream)
+                        : launch_copy<1, 256, 4, 0, 0, kWithFork>(pools, npools, g, pairs, rider, stream);
 }
 
 // ---- resize --------------------------------------------------------------------
@@ -747,9 +759,9 @@ hipError_t launch_compact_plan(const CacheState &s, hipStream_t stream) {
 }
 
 hipError_t launch_compact_copy(const Pools &pools, uint32_t npools, const PageShape &g, const PagePairs &pairs,
-                               bool aligned16, const CacheState &s, bool apply, hipStream_t stream) {
+                               uint32_t piece, const CacheState &s, bool apply, hipStream_t stream) {
     const Rider rider = {s, nullptr, nullptr, apply ? 1u : 0u};
-    return launch_whole<kWithCompact>(pools, npools, g, pairs, rider, aligned16, stream);
+    return launch_whole<kWithCompact>(pools, npools, g, pairs, rider, piece, stream);
 }
 
 }  // namespace tbk

@@ -156,7 +156,7 @@ _NO_CONTEXT = nullcontext()
 def _list_arg(t: torch.Tensor, n: Optional[int], device: torch.device, what: str) -> int:
     """Address of an int32 index list on the cache's device."""
     if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != 1
-            or not t.is_contiguous() or (n is not None and len(t) != n)):
+            or not t.is_contiguous() or (n is not None and t.shape[0] != n)):
         raise ValueError(f"{what} must be a contiguous one-dimensional int32 tensor on {device}"
                          + ("" if n is None else f" of {n} entries"))
     return t.data_ptr()
@@ -339,8 +339,9 @@ class PagedCache:
         """What position positions[i] of sequence seqs[i] holds: [npools, n, heads, head_dim], or with `layer` the two
         pools of that layer.  append()'s way back; a cache held in 4 bits gives the numbers that it holds.
         A negative sequence reads as zeros, and so does what is out of range, with TB_CACHE_RANGE."""
-        n = len(seqs)
-        q, p = _list_arg(seqs, None, self.device, "seqs"), _list_arg(positions, n, self.device, "positions")
+        q = _list_arg(seqs, None, self.device, "seqs")
+        n = seqs.shape[0]
+        p = _list_arg(positions, n, self.device, "positions")
         if layer is None:
             first, count = 0, len(self.pools)
         elif 0 <= layer < len(self.pools) // 2:
@@ -569,8 +570,13 @@ def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tens
             workspace = verify_drafts_workspace(probs)
         # one allocation, cut up
         sizes = [b, b * t, b] + ([] if cache is None else [b, b * t, b * t, b * t])
-        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
-        ptrs = [p.data_ptr() for p in parts] + [0] * (7 - len(parts))
+        whole = torch.empty(sum(sizes), dtype=torch.int32, device=dev)
+        parts = whole.split_with_sizes(sizes)
+        ptrs = [0] * 7
+        at = whole.data_ptr()
+        for i, size in enumerate(sizes):
+            ptrs[i] = at
+            at += 4 * size
         ps, ds = probs.stride(), (0, 0) if draft_probs is None else draft_probs.stride()
         v = _tb_serve.pack_verify(
             probs.data_ptr(), 0 if draft_probs is None else draft_probs.data_ptr(), ps[0], ps[1], ds[0], ds[1],
