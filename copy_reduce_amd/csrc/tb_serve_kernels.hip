@@ -327,13 +327,14 @@ struct Walk {
     double z, taken;
 };
 
-constexpr uint32_t kDraw = 512, kDrawWaves = kDraw / 64;   // threads and waves of a workgroup
-constexpr uint32_t kMaxStretch = 4096, kMaxStretches = 4096;
-// Elements of a stretch: enough for two workgroups on each CU, which all run at once, but no more stretches than there is room
-// for in LDS.
+constexpr uint32_t kDraw = 1024, kDrawWaves = kDraw / 64;   // threads and waves of a workgroup
+constexpr uint32_t kMaxStretch = 8192, kMaxStretches = 4096;
+// Elements of a stretch: enough for a workgroup on each CU, which all run at once, but no more stretches than there is room
+// for in LDS.  Stretches of 1,024 at least instead of 512: 16 chains over 131,072 tokens 23.2 us against 19.5; workgroups of 512
+// threads, two on a CU: 25.5, and 64 such chains 29.6 against 30.3.
 static uint32_t stretch_of(uint32_t batch, uint32_t vocab) {
     uint32_t n = kMaxStretch;
-    while (n > 512 && (uint64_t)batch * ((vocab + n * kDrawWaves - 1) / (n * kDrawWaves)) < 512
+    while (n > 512 && (uint64_t)batch * ((vocab + n * kDrawWaves - 1) / (n * kDrawWaves)) < 256
             && (vocab + n / 2 - 1) / (n / 2) <= kMaxStretches)
         n /= 2;
     return n;
@@ -594,7 +595,7 @@ __device__ __forceinline__ N fresh(const N *p) {
 }
 
 template <typename T, bool Q>
-__global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
+__global__ __launch_bounds__(kDraw) void verify_draw_kernel(VerifyArgs g) {
     __shared__ Walk walk;
     __shared__ double sums[kMaxStretches], waves[kDrawWaves];
     __shared__ uint32_t gone[kMaxStretch * kDrawWaves / 32], found, spare, last_one;
@@ -605,7 +606,7 @@ __global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
     const uint32_t n = nodes_of(g, b);
     const int32_t seq = g.seqs != nullptr ? g.seqs[b] : -1;
     const Gone whose(g, b, Q ? 0 : n);
-    int32_t token = -1, had = 0;
+    int32_t token = -1, had = 0, node = -1, walked = 0;
     if (n != 0) {   // this wave's stretch
         const uint32_t first = blockIdx.x % g.groups * kDrawWaves, k = first + wave;
         const uint32_t begin = first * g.stretch, end = min(begin + kDrawWaves * g.stretch, g.vocab);
@@ -634,6 +635,8 @@ __global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
         for (uint32_t i = thread; i < g.stretches; i += kDraw)
             sums[i] = fresh(&g.sums[(uint64_t)b * g.stretches + i]);
         had = g.seqs != nullptr ? g.lens[seq] : 0;
+        node = (int32_t)thread < w.count ? g.path[row + thread] : -1;   // of the first kernel
+        walked = w.count;
         __syncthreads();
         // The same in every wave, and no barrier.
         const auto total_of = [&] {
@@ -707,7 +710,7 @@ __global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
             if (any_gone)
                 whose.mark(w.cur, begin, end, gone);
             const Left<T, Q> left(g, b, from, any_gone ? gone : nullptr, begin);
-            const uint32_t each = g.stretch / kDraw, x0 = begin + thread * each;
+            const uint32_t each = max(g.stretch / kDraw, 1u), x0 = begin + thread * each;
             constexpr uint32_t kEach = kMaxStretch / kDraw;
             double v[kEach], mine = 0;
 #pragma unroll
@@ -755,7 +758,8 @@ __global__ __launch_bounds__(kDraw, 4) void verify_draw_kernel(VerifyArgs g) {
         __syncthreads();   // of the path's last entries, which the first wave may have written
     for (uint32_t i = thread; i < g.nodes; i += kDraw) {
         const bool real = (int32_t)i < w.count;
-        const int32_t node = real ? fresh(&g.path[row + i]) : -1;
+        if (i >= kDraw || (int32_t)i >= walked)   // not had yet
+            node = real ? fresh(&g.path[row + i]) : -1;
         if (!real)
             g.path[row + i] = -1;
         if (g.seqs != nullptr) {
