@@ -944,8 +944,11 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
         // that of token first + lane % 32, and all have them from LDS: ten times some 15 instructions of a tile become once.
         constexpr bool kShare = WIN || FP4;
         const auto find = [&](uint32_t first) {
-            if constexpr (kShare)
+            if constexpr (kShare) {
                 spots[wk][lane & 31] = keys.place_of(min(first + (lane & 31), c1 - 1));
+                // the wave's own, in order: only the compiler has to be told
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            }
         };
         const auto load_ctx_k = [&](Held<T, D, FP4> &h, uint32_t first) {
             if constexpr (kShare)

@@ -311,7 +311,7 @@ class PagedCache:
                index: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Write rows[:, index[i]] ([npools, n, heads, head_dim]) to position positions[i] of sequence seqs[i].
         A cache held in 4 bits takes rows of its type and rounds them: each 32 elements of a head to a common power
-        of two times 0, 0.5, 1, 1.5, 2, 3, 4 or 6, either sign."""
+        of two times 0, 0.5, 1, 1.5, 2, 3, 4 or 6, either sign.  A position listed twice holds a mixture there."""
         shape, stride = rows.shape, rows.stride()
         if (rows.dtype != self.dtype or rows.device != self.device or len(shape) != 4 or shape[0] != len(self.pools)
                 or shape[2] != self.heads or shape[3] != self.head_dim or stride[3] != 1

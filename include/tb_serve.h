@@ -108,8 +108,11 @@ int tb_verify_workspace(const tb_verify *v, uint64_t *bytes_out);
 #define TB_FP4_BLOCK 32
 #define TB_FP4_HEAD_BYTES(head_dim) ((head_dim) / 2 + ((head_dim) / TB_FP4_BLOCK + 3) / 4 * 4)
 
-/* tb_page_append of rows of `dtype` (TB_BF16 or TB_FP16), heads * head_dim elements each, row_stride and
- * pool_stride in bytes, to a cache held in 4 bits: they are rounded on the way.  rows is aligned to 2 bytes. */
+/*
+ * tb_page_append of rows of `dtype` (TB_BF16 or TB_FP16), heads * head_dim elements each, row_stride and
+ * pool_stride in bytes and multiples of 2, to a cache held in 4 bits: they are rounded on the way.  The same position
+ * twice leaves codes and powers of either row, and so numbers that may be of neither.
+ */
 int tb_fp4_append(const tb_cache *cache, uint32_t dtype, uint32_t head_dim, const void *rows, uint64_t nrows,
                   uint64_t row_stride, uint64_t pool_stride, const int32_t *seqs, const int32_t *positions,
                   const int32_t *index, uint32_t n, void *stream);

@@ -247,3 +247,60 @@ def test_long_context():
     for t in (1, 20):
         q, k, v = inputs(g, 2, t, 2, 1, 64, torch.bfloat16)
         run(c, m, q, k, v, [0, 1], what=f"{t} nodes")
+
+
+@pytest.mark.parametrize("heads,pt", [(1, 1), (3, 1), (1, 5), (3, 7)])
+@pytest.mark.parametrize("layout", ["token", "head"])
+@pytest.mark.parametrize("pad", [0, 4])
+def test_pages_that_are_no_multiple_of_16_bytes(heads, pt, layout, pad):
+    """Whole pages and tails are moved by 16 bytes at 4-byte alignment; what lies between pages stays as it was."""
+    note(f"pages of {pt * heads * 36} bytes and {pad} between, {layout}")
+    c, m, g = make([3 * pt + 2, pt, 2 * pt + 1], heads=heads, dim=64, pt=pt, layout=layout, layers=2, rows=6, spare=20, pad=pad)
+    lens = [3 * pt + 2, pt, 2 * pt + 1]
+    seqs, at = [q for q, n in enumerate(lens) for _ in range(n)], [p for n in lens for p in range(n)]
+    held = c.read(ints(seqs), ints(at))
+    c.fork(ints([0, 2, 0]), ints([3, 4, 5]))
+    for child, parent in ((3, 0), (4, 2), (5, 0)):
+        own = [i for i, q in enumerate(seqs) if q == parent]
+        assert torch.equal(c.read(ints([child] * lens[parent]), ints(list(range(lens[parent])))), held[:, own])
+    c.resize(ints([0, 3]), ints([0, 0]))
+    c.compact()
+    kept = [i for i, q in enumerate(seqs) if q != 0]
+    assert torch.equal(c.read(ints([seqs[i] for i in kept]), ints([at[i] for i in kept])), held[:, kept])
+    assert torch.equal(c.read(ints([5] * lens[0]), ints(list(range(lens[0])))), held[:, :lens[0]])
+    last = int(c.free_list[0])
+    c.copy_pages(ints([last]), c.table[1, :1].clone())
+    assert all(torch.equal(p[last], p[int(c.table[1, 0])]) for p in c.pools) and c.flags() == 0
+    if pad:
+        between = torch.as_strided(c.pools[0], (c.num_pages, pad), (c.pools[0].stride(0), 1), c.pools[0].storage_offset() + pt * heads * 36)
+        assert bool((between == 255).all())
+
+
+def test_pages_past_4_gib():
+    """Pages 1.2 GiB apart: places, and what append, read, fork and attention make of them, past 32 bits of bytes."""
+    note("4 bits: pools of 6 GiB, pages 1.2 GiB apart")
+    require_gpu()
+    from copy_reduce_amd.torch_api import PagedCache, fp4_head_bytes
+    g = torch.Generator().manual_seed(3)
+    pages, pt, heads, dim, apart = 5, 16, 2, 64, (1 << 30) + (200 << 20) + 4
+    hb = fp4_head_bytes(dim)
+    room = [torch.empty((pages - 1) * apart + pt * heads * hb, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pools = [r.as_strided((pages, pt, heads, hb), (apart, heads * hb, hb, 1)) for r in room]
+    c = PagedCache(pools, pt, 3, 5, fp4=torch.bfloat16)
+    m = Model(pages, pt, 3, 5, torch.zeros(2, pages, pt, heads, dim, dtype=torch.bfloat16), "token")
+    m.stack = list(range(pages - 1, -1, -1))
+    n = 50
+    c.resize(ints([1]), ints([n]))
+    m.resize([1], [n])
+    new = torch.randn(2, n, heads, dim, generator=g).to(torch.bfloat16)
+    c.append(new.cuda(), ints([1] * n), ints(list(range(n))))
+    want = decode(encode(new), dim).to(torch.bfloat16)
+    assert torch.equal(c.read(ints([1] * n), ints(list(range(n)))).cpu(), want)
+    for p in range(n):
+        m.by_token()[:, m.table[1][p // pt], p % pt] = want[:, p]
+    for t, hq in ((1, 4), (20, 4)):
+        q, k, v = inputs(g, 1, t, hq, heads, dim, torch.bfloat16)
+        run(c, m, q, k, v, [1], what=f"{t} nodes")
+        run(c, m, q, k, v, [1], window=18, sinks=3, what=f"{t} nodes, window")
+    c.fork(ints([1]), ints([0]))
+    assert torch.equal(c.read(ints([0] * n), ints(list(range(n)))).cpu(), want) and c.flags() == 0

@@ -212,3 +212,63 @@ def test_the_tokens_are_distributed_as_the_target_s():
         first = torch.where(second > 0, tokens.gather(1, second.clamp(min=0)[:, None]).squeeze(1), r.token.cpu().long())
         share = torch.bincount(first, minlength=vocab) / n
         assert float((share - p[0]).abs().max()) < 5 * 0.0036
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turns over new inputs, with an eager call of the same workspace in between."""
+    note("verify: two captured graphs with one workspace")
+    require_gpu()
+    from copy_reduce_amd.torch_api import verify_drafts, verify_drafts_workspace
+    g = torch.Generator().manual_seed(12)
+    shapes = [(3, 6, 70000, 2, True), (3, 9, 70000, 3, False)]
+    held = []
+    for b, t, vocab, kids, drafted in shapes:
+        probs, draft, parents, tokens, u = case(g, b, t, vocab, kids, drafted)
+        held.append([probs.cuda(), None if draft is None else draft.cuda(), ints(parents), ints(tokens), u.cuda()])
+    ws = verify_drafts_workspace(held[0][0])
+
+    def call(x):
+        return verify_drafts(x[0], x[3], x[4], parents=x[2], draft_probs=x[1], workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for x in held:
+            call(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for x in held:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(x))
+        graphs.append(graph)
+    for turn in range(4):
+        for i, (b, t, vocab, kids, drafted) in enumerate(shapes):
+            new = case(g, b, t, vocab, kids, drafted)
+            for a, n in zip(held[i], new[:1] + (new[1],) + tuple(z.to(torch.int32) for z in new[2:4]) + new[4:]):
+                if a is not None:
+                    a.copy_(n)
+            graphs[i].replay()
+            want = verify(new[0], new[3], new[4], new[2], new[1])
+            for j, (count, path, token) in enumerate(want):
+                assert (int(outs[i].count[j]), outs[i].path[j].tolist(), int(outs[i].token[j])) == (count, path + [-1] * (t - count), token), f"turn {turn}"
+            eager = call(held[i])
+            assert all(torch.equal(p, q) for p, q in zip(eager[:3], outs[i][:3]))
+
+
+def test_two_streams_at_once():
+    note("verify on two streams")
+    require_gpu()
+    from copy_reduce_amd.torch_api import verify_drafts
+    g = torch.Generator().manual_seed(13)
+    sets = [case(g, 5, 7, 60000, 2, True) for _ in range(2)]
+    on = [[x[0].cuda(), ints(x[3]), x[4].cuda(), ints(x[2]), x[1].cuda()] for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[verify_drafts(*x, stream=s) for x, s in zip(on, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for i, x in enumerate(sets):
+        want = verify(x[0], x[3], x[4], x[2], x[1])
+        for r in got:
+            for j, (count, path, token) in enumerate(want):
+                assert (int(r[i].count[j]), r[i].path[j].tolist(), int(r[i].token[j])) == (count, path + [-1] * (7 - count), token)
