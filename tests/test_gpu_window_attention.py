@@ -142,3 +142,19 @@ def test_scale_and_strides():
     got = tree_attention(qs, k.cuda(), v.cuda(), c, 0, ints([0, 1]), scale=-0.3, out=out, window=25, sinks=2)
     compare(got, window_attention(m, 0, q, k, v, [0, 1], scale=-0.3, window=25, sinks=2), 110, 64, q.dtype, "strided")
     assert not bool(wide[:, :, :, 0].any())
+
+
+@pytest.mark.parametrize("batch,t,group", [(16, 64, 4), (64, 1, 4)], ids=["rows divided", "whole sequences"])
+def test_batches_that_fill_the_chip(batch, t, group):
+    """So many sequences with windows of 800 that no keys are shared out: many rows are divided instead, few go with a
+    workgroup a sequence."""
+    note(f"{batch} sequences of {t} nodes, windows of 800")
+    lens = [1 + (i * 397) % 1100 for i in range(batch)]
+    c, m, g = setup(lens, heads=8, dim=128, pt=32, seed=batch, room=8192)
+    q, k, v = inputs(g, batch, t, 8 * group, 8, 128, torch.bfloat16)
+    order = torch.randperm(batch, generator=g).tolist()
+    if t == 1:
+        run(c, m, q, k, v, order, 800, 4, what="single tokens")
+    else:
+        mask = tree_mask(g, batch, t)
+        run(c, m, q, k, v, order, 800, 4, mask, [t - (i % 3) * 20 for i in range(batch)], depths_of(mask), what="trees")
