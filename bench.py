@@ -1273,10 +1273,13 @@ def paged_study(args, torch, tb, wl):
     """A paged key/value cache as a decoding engine uses it (include/tb_cache.h): 32 sequences whose prompts'
     pages of 32 KiB arrive by the batched copy, as transferred from a prefill, in pools of 8 layers; then the calls
     of a step, each timed by its launches' own events: one token attending to its context, trees of 16 and
-    of 64 drafted tokens, accepted tokens appended, sequences forked, freed and the cache compacted.
-    One layer's attention is checked against its definition in 64 bits."""
+    of 64 drafted tokens, the same over windows of 1,024, chains of 8 drafted tokens verified over a vocabulary of
+    131,072, accepted tokens appended, the context of one layer rounded to 4 bits, read back and attended to, sequences
+    forked, freed and the cache compacted.  One layer's attention is checked against its definition in 64 bits, and that over 4
+    bits against the attention over the numbers it holds (include/tb_serve.h)."""
     import numpy as np
-    from copy_reduce_amd.torch_api import PagedCache, batched_copy, make_desc, tree_attention, tree_attention_workspace
+    from copy_reduce_amd.torch_api import (PagedCache, batched_copy, fp4_head_bytes, make_desc, tree_attention,
+                                           tree_attention_workspace, verify_drafts, verify_drafts_workspace)
 
     layers, pages, pt, heads, dim, seqs, group = 8, 16384, 16, 8, 128, 32, 4
     gen = torch.Generator(device="cuda").manual_seed(7)
@@ -1346,6 +1349,52 @@ def paged_study(args, torch, tb, wl):
             worst = max(worst, float((got - want).norm() / want.norm()))
         if not worst < 1e-2:
             raise RuntimeError(f"attention of {nodes} nodes is {worst} off its definition")
+
+        window, sinks = 1024, 4
+        seen = sum(min(n, window + sinks - 1) for n in lens) + seqs * nodes
+        timed(f"attention of {nodes} drafted tokens over windows of {window} (tb_view_attention)",
+              lambda: tree_attention(q, k, v, cache, 1, rows, workspace=ws, window=window, sinks=sinks),
+              2 * seen * token + 2 * q.nbytes, 4 * dim * heads * group * nodes * seen)
+
+    # one layer's context in 4 bits: pages of the same tokens, attention over the numbers that they hold
+    hb = fp4_head_bytes(dim)
+    small = PagedCache(torch.zeros(2, sum(-(-n // pt) for n in lens) + 1, heads, pt, hb, dtype=torch.uint8, device="cuda"),
+                       pt, seqs, 600, layout="head", fp4=torch.bfloat16)
+    small.resize(rows, ints(lens))
+    who = ints(b for b in range(seqs) for _ in range(lens[b]))
+    where = ints(p for b in range(seqs) for p in range(lens[b]))
+    context = cache.read(who, where, layer=1)
+    tokens = len(who)
+    timed(f"{tokens} tokens of a layer rounded to 4 bits (tb_fp4_append)", lambda: small.append(context, who, where),
+          2 * tokens * (token + heads * hb))
+    held = small.read(who, where)
+    timed("and read back (tb_fp4_read)", lambda: small.read(who, where, out=held), 2 * tokens * (token + heads * hb))
+    cache.append(torch.cat([torch.zeros_like(held), held] + [torch.zeros_like(held)] * (layers - 2)), who, where)
+    q = torch.empty(seqs, 1, heads * group, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    k, v = [torch.empty(seqs, 1, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2)]
+    ws = tree_attention_workspace(q, small)
+    timed("attention of single tokens over 4 bits (tb_view_attention)",
+          lambda: tree_attention(q, k, v, small, 0, rows, workspace=ws),
+          2 * tokens * heads * hb + 2 * seqs * token + 2 * q.nbytes, 4 * dim * heads * group * (tokens + seqs))
+    got = tree_attention(q, k, v, small, 0, rows, workspace=ws)[0].double()
+    want = tree_attention(q, k, v, cache, 1, rows)[0].double()
+    worst = float((got - want).norm() / want.norm())
+    if not worst < 1e-2:
+        raise RuntimeError(f"attention over 4 bits is {worst} off that over the same numbers in 16")
+    del context, held, small
+
+    vocab, nodes = 131072, 8
+    logits = 3 * torch.empty(seqs, nodes, vocab, device="cuda").normal_(generator=gen)
+    probs = torch.softmax(logits, 2)
+    draft = torch.softmax(logits + 0.5 * torch.empty_like(logits).normal_(generator=gen), 2)
+    drafted = torch.multinomial(draft[:, :-1].reshape(-1, vocab), 1, generator=gen).view(seqs, nodes - 1).to(torch.int32)
+    drafted = torch.cat([torch.zeros_like(drafted[:, :1]), drafted], 1)
+    uniform = torch.rand(seqs, nodes, device="cuda", generator=gen)
+    vws = verify_drafts_workspace(probs)
+    timed(f"chains of {nodes} tokens verified (tb_verify_drafts)",
+          lambda: verify_drafts(probs, drafted, uniform, draft_probs=draft, cache=cache, seqs=rows, workspace=vws),
+          2 * 4 * seqs * vocab)
+    del logits, probs, draft
 
     new = torch.empty(2 * layers, 4 * seqs, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
     who = ints(q for q in range(seqs) for _ in range(4))
