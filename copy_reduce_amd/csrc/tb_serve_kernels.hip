@@ -30,10 +30,10 @@ __device__ __forceinline__ TokenPlace place_of_token(const CacheState &s, int32_
     if ((uint32_t)q >= s.max_seqs)
         return {q < 0 ? -1 : (int32_t)TB_CACHE_RANGE, 0};
     const int32_t most = (int32_t)(s.max_pages * s.page_tokens), n = s.lens[q];
+    const uint32_t j = (uint32_t)pos / s.page_tokens, in_page = (uint32_t)pos % s.page_tokens;
+    const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + min(j, s.max_pages - 1)];   // beside the length
     if (pos < 0 || pos >= min(n, most))
         return {TB_CACHE_RANGE, 0};
-    const uint32_t j = (uint32_t)pos / s.page_tokens, in_page = (uint32_t)pos % s.page_tokens;
-    const uint32_t page = (uint32_t)s.table[(uint64_t)q * s.max_pages + j];
     if (page >= s.num_pages)
         return {TB_CACHE_RANGE, 0};
     if (to_write && s.refs[page] > 1)
@@ -78,30 +78,41 @@ __device__ __forceinline__ uint32_t power_byte(uint32_t top) {
     return (uint32_t)min(max(e, Type16<T>::kLow), Type16<T>::kHigh);
 }
 
-// A thread has 8 elements of one token, four threads a block of 32, and goes over pools, kFp4Pools at a time, those
-// blockIdx.y * kFp4Pools on, while the next ones' elements are on their way; the first are asked for while the page is found, four
-// loads one after the other.  The conversion to 4 bits is the hardware's: to the nearest, of two the even code,
-// larger ones to 6.
-constexpr uint32_t kFp4Pools = 4, kTokenBlocks = 4096;
-// Workgroups that go over the same tokens, in y: so many that the chip has work for some rounds.
-static dim3 token_grid(uint32_t n, uint32_t parts, uint32_t npools) {
+// A thread has 8 elements of one token, four threads a block of 32, and goes over the pools, a few at a time, while the next
+// ones' elements are on their way; the first are asked for while the page is found, three loads one after the other.  The
+// conversion to 4 bits is the hardware's: to the nearest, of two the even code, larger ones to 6.
+//
+// Bound by HBM in the large: 3,500 tokens of 64 pools, 8 heads of 128, in 107 us by token and 116 by head, back out in 86 (a copy's
+// rate would be 89 either way); in random order 108 and 123, and 88 and 113.  With few pools the search for the page
+// is what costs: 131,072 tokens of 2 pools in 168 us, back out in 101 (104 at a copy's rate).  Two pools at a time into
+// the cache and four out of it: four into it 172 us against 164 at 2 pools, and 105 against 107 at 64.  Registers for 8
+// waves instead of 6: 104 us against 114.
+constexpr uint32_t kInPools = 2, kOutPools = 4, kTokenBlocks = 4096;
+// Workgroups in x go over the tokens, those in y over the pools: so many that the chip has work for some rounds.  In x
+// each of the 8 XCDs has tokens that follow each other, since heads of 68 bytes share lines with their neighbours: 131,072
+// tokens of 2 pools, by head, are read in 104 us so, and in 115 one after the other.
+constexpr uint32_t kXcds = 8;
+static dim3 token_grid(uint32_t n, uint32_t parts, uint32_t npools, uint32_t pools) {
     const uint64_t blocks = ((uint64_t)n * parts + 255) / 256, most = 1u << 22;
-    const uint32_t x = (uint32_t)(blocks < most ? blocks : most), each = (npools + kFp4Pools - 1) / kFp4Pools;
-    const uint32_t y = (kTokenBlocks + x - 1) / x;
+    const uint32_t x = ((uint32_t)(blocks < most ? blocks : most) + kXcds - 1) / kXcds * kXcds;
+    const uint32_t each = (npools + pools - 1) / pools, y = (kTokenBlocks + x - 1) / x;
     return dim3(x, y < each ? y : each, 1);
+}
+__device__ __forceinline__ uint32_t token_block() {
+    return blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void fp4_append_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
+__global__ __launch_bounds__(256, 8) void fp4_append_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
         uint32_t npools) {
-    constexpr uint32_t U = kFp4Pools;
+    constexpr uint32_t U = kInPools;
     const uint64_t all = (uint64_t)a.n * parts;
     const uint32_t of_head = a.dim / 8;
     const bool whole = 64 % of_head == 0;   // no head lies in two waves
-    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
+    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
-        const int32_t q = a.seqs[i];
+        const int32_t q = a.seqs[i], position = a.positions[i];
         const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
         if (q < 0)
             continue;
@@ -116,7 +127,7 @@ __global__ __launch_bounds__(256) void fp4_append_kernel(Pools pools, CacheState
         u32x4 x[U], next[U];
         uint32_t pool = blockIdx.y * U;
         load(pool, x);
-        TokenPlace to = place_of_token(s, q, a.positions[i], a.page_stride, a.token_step, true);
+        TokenPlace to = place_of_token(s, q, position, a.page_stride, a.token_step, true);
         if (!there)
             to.flag = TB_CACHE_RANGE;
         if (to.flag != 0) {
@@ -178,17 +189,17 @@ hipError_t launch_fp4_append(const Pools &pools, uint32_t npools, const CacheSta
                              uint32_t dtype, hipStream_t stream) {
     const uint32_t parts = a.heads * (a.dim / 8);
     return launch(dtype == TB_BF16 ? fp4_append_kernel<__bf16> : fp4_append_kernel<_Float16>,
-                  token_grid(a.n, parts, npools), 256, stream,
+                  token_grid(a.n, parts, npools, kInPools), 256, stream,
                   nullptr, pools, s, a, parts, npools);
 }
 
 template <typename T>
 __global__ __launch_bounds__(256) void fp4_read_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
         uint32_t npools) {
-    constexpr uint32_t U = kFp4Pools;
+    constexpr uint32_t U = kOutPools;
     const uint64_t all = (uint64_t)a.n * parts;
     const uint32_t of_head = a.dim / 8;
-    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
+    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
         const TokenPlace from = place_of_token(s, a.seqs[i], a.positions[i], a.page_stride, a.token_step, false);
@@ -233,10 +244,10 @@ hipError_t launch_fp4_read(const Pools &pools, uint32_t npools, const CacheState
                            uint32_t dtype, hipStream_t stream) {
     const uint32_t parts = a.heads * (a.dim / 8);
     return launch(dtype == TB_BF16 ? fp4_read_kernel<__bf16> : fp4_read_kernel<_Float16>,
-                  token_grid(a.n, parts, npools), 256, stream, nullptr, pools, s, a, parts, npools);
+                  token_grid(a.n, parts, npools, kOutPools), 256, stream, nullptr, pools, s, a, parts, npools);
 }
 
-// The bytes of tokens out of their pages: E bytes of one token in kFp4Pools pools a thread.
+// The bytes of tokens out of their pages: E bytes of one token in kOutPools pools a thread.
 template <int E>
 struct Bytes;
 template <>
@@ -257,10 +268,10 @@ __global__ __launch_bounds__(256) void read_kernel(Pools pools, CacheState s, Ap
         uint32_t npools) {
     typedef typename Bytes<E>::T piece;
     typedef __attribute__((address_space(1))) piece gpiece;
-    constexpr uint32_t U = kFp4Pools;
+    constexpr uint32_t U = kOutPools;
     const uint64_t all = (uint64_t)a.n * parts;
     const uint32_t pool = blockIdx.y * U;
-    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
+    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t off = (uint32_t)(at - (uint64_t)i * parts) * E;
         const TokenPlace from = place_of_token(s, a.seqs[i], a.positions[i], a.page_stride, a.token_step, false);
@@ -285,8 +296,8 @@ __global__ __launch_bounds__(256) void read_kernel(Pools pools, CacheState s, Ap
 hipError_t launch_read(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a, uint32_t piece,
                        hipStream_t stream) {
     const uint32_t parts = a.heads * a.head_bytes / piece;
-    const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
-    const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kFp4Pools - 1) / kFp4Pools, 1);
+    dim3 grid = token_grid(a.n, parts, npools, kOutPools);
+    grid.y = (npools + kOutPools - 1) / kOutPools;
     return launch(piece == 16 ? read_kernel<16> : (piece == 4 ? read_kernel<4> : read_kernel<1>), grid, 256, stream,
                   nullptr, pools, s, a, parts, npools);
 }
