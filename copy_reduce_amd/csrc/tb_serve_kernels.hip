@@ -78,96 +78,160 @@ __device__ __forceinline__ uint32_t power_byte(uint32_t top) {
     return (uint32_t)min(max(e, Type16<T>::kLow), Type16<T>::kHigh);
 }
 
-// A thread has 8 elements of one token, four threads a block of 32, and goes over the pools, a few at a time, while the next
-// ones' elements are on their way; the first are asked for while the page is found, three loads one after the other.  The
-// conversion to 4 bits is the hardware's: to the nearest, of two the even code, larger ones to 6.
+// A workgroup has a few tokens of one pool: it finds their places, one a thread, and then goes over their elements, 8 a
+// thread and four threads a block of 32, kAtOnce such pieces on their way at once and as many behind them.  The conversion to 4
+// bits is the hardware's: to the nearest, of two the even code, larger ones to 6.
 //
-// Bound by HBM in the large: 3,500 tokens of 64 pools, 8 heads of 128, in 107 us by token and 116 by head, back out in 86 (a copy's
-// rate would be 89 either way); in random order 108 and 123, and 88 and 113.  With few pools the search for the page
-// is what costs: 131,072 tokens of 2 pools in 168 us, back out in 101 (104 at a copy's rate).  Two pools at a time into
-// the cache and four out of it: four into it 172 us against 164 at 2 pools, and 105 against 107 at 64.  Registers for 8
-// waves instead of 6: 104 us against 114.
-constexpr uint32_t kInPools = 2, kOutPools = 4, kTokenBlocks = 4096;
-// Workgroups in x go over the tokens, those in y over the pools: so many that the chip has work for some rounds.  In x
-// each of the 8 XCDs has tokens that follow each other, since heads of 68 bytes share lines with their neighbours: 131,072
-// tokens of 2 pools, by head, are read in 104 us so, and in 115 one after the other.
-constexpr uint32_t kXcds = 8;
-static dim3 token_grid(uint32_t n, uint32_t parts, uint32_t npools, uint32_t pools) {
-    const uint64_t blocks = ((uint64_t)n * parts + 255) / 256, most = 1u << 22;
-    const uint32_t x = ((uint32_t)(blocks < most ? blocks : most) + kXcds - 1) / kXcds * kXcds;
-    const uint32_t each = (npools + pools - 1) / pools, y = (kTokenBlocks + x - 1) / x;
-    return dim3(x, y < each ? y : each, 1);
+// Each of the 8 XCDs has an eighth of the work, pool by pool.  Heads of 68 bytes share lines with their neighbours, which so
+// meet in one L2, in whatever order the tokens are listed.
+//
+// Bound by HBM in the large: 3,500 tokens of 64 pools, 8 heads of 128, in 109 us by token and 111 by head, back out in 81 (a
+// copy's rate would be 89 either way); in random order 111 and 114, and 82; 131,072 tokens of 2 pools in 133, back out
+// in 95 (104).  With a token's pools in one thread instead, which finds its place by itself: 106 and 115, 86; 107 and 122, 88
+// and 113; 163, 100; 16,384 tokens of 8 pools, 4 heads of 256, which partly stay in the caches, 61 against 71 here, where
+// instructions count.  Registers for 8 waves spill: 143 and 104 instead of 111 and 81.
+constexpr uint32_t kXcds = 8, kAtOnce = 4, kTokens = 64, kPieces = 2048;
+struct TokenWork {
+    uint32_t heads, of_head, parts;    // of a token; pieces of a head and of a token
+    uint32_t tokens, groups;           // of a workgroup; workgroups a pool
+    uint32_t step_token, step_head, step_in;   // 256 pieces on
+    uint64_t share;                    // (pool, group) pairs an XCD
+    uint32_t npools;
+};
+static TokenWork token_work(const Fp4Args &a, uint32_t npools) {
+    TokenWork w;
+    w.heads = a.heads;
+    w.of_head = a.dim / 8;
+    w.parts = a.heads * w.of_head;
+    w.tokens = 1;
+    while (w.tokens < kTokens && w.tokens * 2 * (uint64_t)w.parts <= kPieces)
+        w.tokens *= 2;
+    while (w.tokens > 1 && w.tokens * (uint64_t)w.parts > 256 && ((uint64_t)a.n + w.tokens - 1) / w.tokens * npools < 1024)
+        w.tokens /= 2;
+    w.groups = (uint32_t)(((uint64_t)a.n + w.tokens - 1) / w.tokens);
+    w.share = ((uint64_t)w.groups * npools + kXcds - 1) / kXcds;
+    const uint32_t heads = 256 / w.of_head;
+    w.step_token = heads / w.heads;
+    w.step_head = heads % w.heads;
+    w.step_in = 256 % w.of_head;
+    w.npools = npools;
+    return w;
 }
-__device__ __forceinline__ uint32_t token_block() {
-    return blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+static uint32_t token_grid(const TokenWork &w) {
+    return kXcds * (uint32_t)(w.share < (1u << 19) ? w.share : 1u << 19);
 }
 
-template <typename T>
-__global__ __launch_bounds__(256, 8) void fp4_append_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
-        uint32_t npools) {
-    constexpr uint32_t U = kInPools;
-    const uint64_t all = (uint64_t)a.n * parts;
-    const uint32_t of_head = a.dim / 8;
-    const bool whole = 64 % of_head == 0;   // no head lies in two waves
-    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
-        const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
-        const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
-        const int32_t q = a.seqs[i], position = a.positions[i];
-        const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
-        if (q < 0)
-            continue;
-        const uint64_t src = a.rows + row * a.row_stride + part * 16ull;
-        const bool there = row < a.nrows;
-        const auto load = [&](uint32_t pool, u32x4 *x) {
-#pragma unroll
-            for (uint32_t u = 0; u < U; u++)
-                if (there && pool + u < npools)
-                    x[u] = __builtin_nontemporal_load((const gu32x4_at2 *)(src + (pool + u) * a.pool_stride));
-        };
-        u32x4 x[U], next[U];
-        uint32_t pool = blockIdx.y * U;
-        load(pool, x);
-        TokenPlace to = place_of_token(s, q, position, a.page_stride, a.token_step, true);
-        if (!there)
-            to.flag = TB_CACHE_RANGE;
-        if (to.flag != 0) {
-            if (part == 0 && blockIdx.y == 0)
-                atomicOr(&s.counts[1], to.flag);
-            continue;
+// A thread's place among the pieces of its workgroup's tokens.
+struct Piece {
+    uint32_t token, head, in_head;
+
+    __device__ __forceinline__ explicit Piece(const TokenWork &w) {
+        const uint32_t h = threadIdx.x / w.of_head;
+        in_head = threadIdx.x % w.of_head;
+        token = h / w.heads;
+        head = h % w.heads;
+    }
+    __device__ __forceinline__ void next(const TokenWork &w) {
+        in_head += w.step_in;
+        head += w.step_head;
+        token += w.step_token;
+        if (in_head >= w.of_head) {
+            in_head -= w.of_head;
+            head++;
         }
-        const uint64_t dst = to.at + head * a.head_step;
-        for (;;) {
-            const uint32_t after = pool + gridDim.y * U;
-            load(after, next);   // past the last: none
+        if (head >= w.heads) {
+            head -= w.heads;
+            token++;
+        }
+    }
+};
+
+// f(pool, first token, tokens) for each share of this workgroup's; f has barriers.
+template <typename F>
+__device__ __forceinline__ void over_tokens(const TokenWork &w, uint32_t n, F f) {
+    const uint64_t end = min((uint64_t)(blockIdx.x % kXcds + 1) * w.share, (uint64_t)w.groups * w.npools);
+    for (uint64_t k = blockIdx.x % kXcds * w.share + blockIdx.x / kXcds; k < end; k += gridDim.x / kXcds) {
+        const uint32_t pool = k <= 0xffffffffu ? (uint32_t)k / w.groups : (uint32_t)(k / w.groups);
+        const uint32_t first = (uint32_t)(k - (uint64_t)pool * w.groups) * w.tokens;
+        f(pool, first, min(w.tokens, n - first));
+    }
+}
+
+constexpr uint64_t kNowhere = ~0ull;
+
+// The lane's value of `x` C says, in its row of 16; 0 past the row's end.
+template <int C>
+__device__ __forceinline__ uint32_t of_lane(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, C, 0xf, 0xf, true);
+}
+constexpr int kPairs = 0xb1, kTwos = 0x4e, kAhead4 = 0x104;   // 1 0 3 2; 2 3 0 1; four lanes on
+
+// WHOLE: no head lies in two waves, and a thread's place in a head is the same for all of its pieces.
+template <typename T, bool WHOLE>
+__global__ __launch_bounds__(256, 6) void fp4_append_kernel(Pools pools, CacheState s, Fp4Args a, TokenWork w) {
+    __shared__ uint64_t rows[kTokens], places[kTokens];
+    constexpr uint32_t U = kAtOnce;
+    const uint32_t blocks = w.of_head / 4, mine = threadIdx.x % w.of_head;
+    const uint32_t powers = ~0u >> (8 * max(4 - (int)(blocks - min(mine / 4, blocks)), 0));   // of a word
+    over_tokens(w, a.n, [&](uint32_t pool, uint32_t first, uint32_t tokens) {
+        if (threadIdx.x < tokens) {
+            const uint32_t i = first + threadIdx.x;
+            const int32_t q = a.seqs[i], position = a.positions[i];
+            const uint64_t row = a.index != nullptr ? (uint64_t)(int64_t)a.index[i] : i;
+            TokenPlace to = place_of_token(s, q, position, a.page_stride, a.token_step, true);
+            if (q >= 0 && row >= a.nrows)
+                to.flag = TB_CACHE_RANGE;
+            if (to.flag > 0 && pool == 0)
+                atomicOr(&s.counts[1], to.flag);
+            rows[threadIdx.x] = a.rows + row * a.row_stride + pool * a.pool_stride;
+            places[threadIdx.x] = to.flag == 0 ? pools.dst[pool] + to.at : kNowhere;
+        }
+        __syncthreads();
+        const uint32_t pieces = tokens * w.parts;
+        Piece ahead(w), here(w);
+        const auto load = [&](uint32_t at, u32x4 *x) {
 #pragma unroll
             for (uint32_t u = 0; u < U; u++) {
-                if (pool + u >= npools)
+                if (at + u * 256 < pieces && places[ahead.token] != kNowhere)
+                    x[u] = __builtin_nontemporal_load(
+                            (const gu32x4_at2 *)(rows[ahead.token] + (ahead.head * w.of_head + (WHOLE ? mine : ahead.in_head)) * 16ull));
+                ahead.next(w);
+            }
+        };
+        u32x4 x[U], after[U];
+        load(threadIdx.x, x);
+        for (uint32_t at = threadIdx.x; at < pieces; at += U * 256) {
+            load(at + U * 256, after);   // past the last: none
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                const Piece piece = here;
+                here.next(w);
+                if (at + u * 256 >= pieces)
                     break;
+                const uint64_t token = places[piece.token];
+                if (token == kNowhere)
+                    continue;
+                const uint64_t place = token + piece.head * (uint32_t)a.head_step;
                 u16x2 m = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[u][e] & 0x7fff7fffu));
                 uint32_t top = max((uint32_t)m.x, (uint32_t)m.y);
-                top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-                top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+                top = max(top, of_lane<kPairs>(top));
+                top = max(top, of_lane<kTwos>(top));
                 const uint32_t byte = power_byte<T>(top);
                 const float power = __uint_as_float(byte << 23);
                 uint32_t code = Type16<T>::template round<0>(0, x[u][0], power);
                 code = Type16<T>::template round<1>(code, x[u][1], power);
                 code = Type16<T>::template round<2>(code, x[u][2], power);
                 code = Type16<T>::template round<3>(code, x[u][3], power);
-                const uint64_t place = pools.dst[pool + u] + dst;
+                const uint32_t in_head = WHOLE ? mine : piece.in_head, block = in_head / 4;
                 *(gu32 *)(place + in_head * 4) = byte == 255 ? 0 : code;
-                const uint32_t block = in_head / 4, blocks = of_head / 4;
-                if (whole) {   // a word of powers, from the first of its blocks' threads
-                    uint32_t word = byte;
-#pragma unroll
-                    for (int k = 1; k < 4; k++) {
-                        const uint32_t other = (uint32_t)__shfl_down((int)byte, 4 * k);
-                        word |= block + k < blocks ? other << (8 * k) : 0;
-                    }
+                if (WHOLE) {   // a word of powers, from the first of its blocks' threads
+                    const uint32_t word = byte | of_lane<kAhead4>(byte) << 8 | of_lane<kAhead4 + 4>(byte) << 16 |
+                                          of_lane<kAhead4 + 8>(byte) << 24;
                     if (in_head % 16 == 0)
-                        *(gu32 *)(place + a.dim / 2 + block) = word;
+                        *(gu32 *)(place + a.dim / 2 + block) = word & powers;
                 } else if (in_head % 4 == 0) {
                     *(gu8 *)(place + a.dim / 2 + block) = (uint8_t)byte;
                     if (block + 1 == blocks)
@@ -175,79 +239,79 @@ __global__ __launch_bounds__(256, 8) void fp4_append_kernel(Pools pools, CacheSt
                             *(gu8 *)(place + a.dim / 2 + k) = 0;
                 }
             }
-            if (after >= npools)
-                break;
-            pool = after;
 #pragma unroll
             for (uint32_t u = 0; u < U; u++)
-                x[u] = next[u];
+                x[u] = after[u];
         }
-    }
+        __syncthreads();
+    });
 }
 
 hipError_t launch_fp4_append(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
                              uint32_t dtype, hipStream_t stream) {
-    const uint32_t parts = a.heads * (a.dim / 8);
-    return launch(dtype == TB_BF16 ? fp4_append_kernel<__bf16> : fp4_append_kernel<_Float16>,
-                  token_grid(a.n, parts, npools, kInPools), 256, stream,
-                  nullptr, pools, s, a, parts, npools);
+    const TokenWork w = token_work(a, npools);
+    const bool whole = 64 % w.of_head == 0;
+    return launch(dtype == TB_BF16 ? (whole ? fp4_append_kernel<__bf16, true> : fp4_append_kernel<__bf16, false>)
+                                   : (whole ? fp4_append_kernel<_Float16, true> : fp4_append_kernel<_Float16, false>),
+                  token_grid(w), 256, stream, nullptr, pools, s, a, w);
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void fp4_read_kernel(Pools pools, CacheState s, Fp4Args a, uint32_t parts,
-        uint32_t npools) {
-    constexpr uint32_t U = kOutPools;
-    const uint64_t all = (uint64_t)a.n * parts;
-    const uint32_t of_head = a.dim / 8;
-    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
-        const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
-        const uint32_t part = (uint32_t)(at - (uint64_t)i * parts), head = part / of_head, in_head = part % of_head;
-        const TokenPlace from = place_of_token(s, a.seqs[i], a.positions[i], a.page_stride, a.token_step, false);
-        if (from.flag > 0 && part == 0 && blockIdx.y == 0)
-            atomicOr(&s.counts[1], from.flag);
-        const uint64_t src = from.at + head * a.head_step;
-        const uint64_t dst = a.rows + i * a.row_stride + part * 16ull;
-        const auto load = [&](uint32_t pool, uint32_t *code, uint32_t *byte) {
+__global__ __launch_bounds__(256, 6) void fp4_read_kernel(Pools pools, CacheState s, Fp4Args a, TokenWork w) {
+    __shared__ uint64_t places[kTokens];
+    constexpr uint32_t U = kAtOnce;
+    over_tokens(w, a.n, [&](uint32_t pool, uint32_t first, uint32_t tokens) {
+        if (threadIdx.x < tokens) {
+            const uint32_t i = first + threadIdx.x;
+            const TokenPlace from = place_of_token(s, a.seqs[i], a.positions[i], a.page_stride, a.token_step, false);
+            if (from.flag > 0 && pool == 0)
+                atomicOr(&s.counts[1], from.flag);
+            places[threadIdx.x] = from.flag == 0 ? pools.dst[pool] + from.at : kNowhere;
+        }
+        __syncthreads();
+        const uint32_t pieces = tokens * w.parts;
+        const uint64_t out = a.rows + pool * a.pool_stride + first * a.row_stride;
+        Piece ahead(w), here(w);
+        const auto load = [&](uint32_t at, uint32_t *code, uint32_t *byte) {
 #pragma unroll
             for (uint32_t u = 0; u < U; u++) {
                 code[u] = byte[u] = 0;
-                if (pool + u < npools && from.flag == 0) {
-                    code[u] = *(const gu32 *)(pools.dst[pool + u] + src + in_head * 4);
-                    byte[u] = *(const gu8 *)(pools.dst[pool + u] + src + a.dim / 2 + in_head / 4);
+                const uint64_t token = at + u * 256 < pieces ? places[ahead.token] : kNowhere;
+                if (token != kNowhere) {
+                    const uint64_t place = token + ahead.head * (uint32_t)a.head_step;
+                    code[u] = *(const gu32 *)(place + ahead.in_head * 4);
+                    byte[u] = *(const gu8 *)(place + a.dim / 2 + ahead.in_head / 4);
                 }
+                ahead.next(w);
             }
         };
         uint32_t code[U], byte[U], code2[U], byte2[U];
-        uint32_t pool = blockIdx.y * U;
-        load(pool, code, byte);
-        for (;;) {
-            const uint32_t after = pool + gridDim.y * U;
-            load(after, code2, byte2);
-#pragma unroll
-            for (uint32_t u = 0; u < U; u++)
-                if (pool + u < npools)
-                    __builtin_nontemporal_store(eight_of<T>(code[u], power_of(byte[u], 0)),
-                            (gu32x4_at2 *)(dst + (pool + u) * a.pool_stride));
-            if (after >= npools)
-                break;
-            pool = after;
+        load(threadIdx.x, code, byte);
+        for (uint32_t at = threadIdx.x; at < pieces; at += U * 256) {
+            load(at + U * 256, code2, byte2);
 #pragma unroll
             for (uint32_t u = 0; u < U; u++) {
+                if (at + u * 256 < pieces)
+                    __builtin_nontemporal_store(eight_of<T>(code[u], power_of(byte[u], 0)),
+                            (gu32x4_at2 *)(out + here.token * a.row_stride + (here.head * w.of_head + here.in_head) * 16ull));
+                here.next(w);
                 code[u] = code2[u];
                 byte[u] = byte2[u];
             }
         }
-    }
+        __syncthreads();
+    });
 }
 
 hipError_t launch_fp4_read(const Pools &pools, uint32_t npools, const CacheState &s, const Fp4Args &a,
                            uint32_t dtype, hipStream_t stream) {
-    const uint32_t parts = a.heads * (a.dim / 8);
-    return launch(dtype == TB_BF16 ? fp4_read_kernel<__bf16> : fp4_read_kernel<_Float16>,
-                  token_grid(a.n, parts, npools, kOutPools), 256, stream, nullptr, pools, s, a, parts, npools);
+    const TokenWork w = token_work(a, npools);
+    return launch(dtype == TB_BF16 ? fp4_read_kernel<__bf16> : fp4_read_kernel<_Float16>, token_grid(w), 256, stream,
+                  nullptr, pools, s, a, w);
 }
 
-// The bytes of tokens out of their pages: E bytes of one token in kOutPools pools a thread.
+// The bytes of tokens out of their pages: E bytes of one token in kReadPools pools a thread.
+constexpr uint32_t kReadPools = 4;
 template <int E>
 struct Bytes;
 template <>
@@ -268,10 +332,10 @@ __global__ __launch_bounds__(256) void read_kernel(Pools pools, CacheState s, Ap
         uint32_t npools) {
     typedef typename Bytes<E>::T piece;
     typedef __attribute__((address_space(1))) piece gpiece;
-    constexpr uint32_t U = kOutPools;
+    constexpr uint32_t U = kReadPools;
     const uint64_t all = (uint64_t)a.n * parts;
     const uint32_t pool = blockIdx.y * U;
-    for (uint64_t at = (uint64_t)token_block() * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
+    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (uint64_t)gridDim.x * 256) {
         const uint32_t i = at <= 0xffffffffu ? (uint32_t)at / parts : (uint32_t)(at / parts);
         const uint32_t off = (uint32_t)(at - (uint64_t)i * parts) * E;
         const TokenPlace from = place_of_token(s, a.seqs[i], a.positions[i], a.page_stride, a.token_step, false);
@@ -296,8 +360,8 @@ __global__ __launch_bounds__(256) void read_kernel(Pools pools, CacheState s, Ap
 hipError_t launch_read(const Pools &pools, uint32_t npools, const CacheState &s, const AppendArgs &a, uint32_t piece,
                        hipStream_t stream) {
     const uint32_t parts = a.heads * a.head_bytes / piece;
-    dim3 grid = token_grid(a.n, parts, npools, kOutPools);
-    grid.y = (npools + kOutPools - 1) / kOutPools;
+    const uint64_t blocks = ((uint64_t)a.n * parts + 255) / 256, most = 1u << 22;
+    const dim3 grid((uint32_t)(blocks < most ? blocks : most), (npools + kReadPools - 1) / kReadPools, 1);
     return launch(piece == 16 ? read_kernel<16> : (piece == 4 ? read_kernel<4> : read_kernel<1>), grid, 256, stream,
                   nullptr, pools, s, a, parts, npools);
 }
