@@ -110,6 +110,38 @@ def test_append_rounds_as_defined(dim, dtype, layout, pt, pad):
         assert torch.equal(got[:, i].double().nan_to_num(1e30), exp.nan_to_num(1e30))
 
 
+@pytest.mark.parametrize("layout", ["token", "head"])
+@pytest.mark.parametrize("dim,heads,n", [(32, 1, 1000), (32, 70, 40), (64, 2, 900), (96, 5, 333), (128, 9, 301), (192, 11, 64),
+                                         (512, 1, 129), (2080, 1, 13), (4096, 3, 7)])
+def test_lists_of_many_tokens_and_wide_heads(dim, heads, n, layout):
+    """More tokens than a workgroup has, in any order with padding between them, and heads that many waves share."""
+    note(f"{n} tokens in 4 bits: {heads} heads of {dim} {layout}")
+    g = torch.Generator().manual_seed(dim + n)
+    lens = [n, n // 3 + 1]
+    c, m, _ = make(lens, heads=heads, dim=dim, pt=7, layout=layout, layers=2)
+    before = [p.clone() for p in c.pools]
+    order = torch.randperm(sum(lens), generator=g).tolist()
+    where = [(0, p) if p < n else (1, p - n) for p in order]
+    where = [(-1, 5) if i % 10 == 3 else w for i, w in enumerate(where)]
+    new = torch.randn(4, len(where) + 5, heads, dim, generator=g).to(torch.bfloat16)
+    index = torch.randperm(len(where) + 5, generator=g).tolist()[:len(where)]
+    seqs, at = ints([q for q, _ in where]), ints([p for _, p in where])
+    c.append(new.cuda(), seqs, at, ints(index))
+    want = encode(new)
+    for p in range(4):
+        exp = before[p].cpu()
+        by = exp if layout == "token" else exp.transpose(1, 2)
+        for (q, pos), x in zip(where, index):
+            if q >= 0:
+                by[m.table[q][pos // 7], pos % 7] = want[p, x]
+        assert torch.equal(c.pools[p].cpu(), exp)
+    assert c.flags() == 0
+    got = c.read(seqs, at).cpu()
+    exp = decode(want[:, index], dim).to(torch.bfloat16)
+    exp[:, [i for i, (q, _) in enumerate(where) if q < 0]] = 0
+    assert torch.equal(got, exp)
+
+
 def test_every_value_of_both_types():
     """Each of the 65,536 bit patterns as an element beside a largest one that sets the power."""
     for dtype in DTYPES:
