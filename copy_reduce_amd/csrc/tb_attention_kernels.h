@@ -564,6 +564,10 @@ struct Rows {
                     for (int t = 0; t < NT; t++)
                         s[t][z] = Mfma<T>::mul(x[2 * e + z], q[t][k + e], s[t][z]);
         }
+        // The results may be read 8 states after the last product.  The compiler counts them on the way through the branch below
+        // and not on the way past it, where two to three were left, too few: now and then what the registers had before came out.
+        if constexpr (NT == 1)
+            asm volatile("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
         if (some) {
 #pragma unroll
             for (int t = 0; t < NT; t++)
@@ -936,10 +940,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
         __syncthreads();
 
         const uint64_t k_pool = reinterpret_cast<uint64_t>(g.k_cache), v_pool = reinterpret_cast<uint64_t>(g.v_cache);
-        // 4 bits: two tiles are on their way, as a tile is a quarter of the bytes
-        constexpr int kAhead = 1;
-        Held<T, D, FP4> waiting[kAhead];
-        Held<T, D, FP4> &held = waiting[0];
+        Held<T, D, FP4> held;
         // Tokens first .. first + 31, those past the chunk its last one.  Where finding a place counts, each lane finds
         // that of token first + lane % 32, and all have them from LDS: ten times some 15 instructions of a tile become once.
         constexpr bool kShare = WIN || FP4;
@@ -950,25 +951,25 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
         };
-        const auto load_ctx_k = [&](Held<T, D, FP4> &h, uint32_t first) {
+        const auto load_ctx_k = [&](uint32_t first) {
             if constexpr (kShare)
-                h.load_k(k_pool + (uint64_t)spots[wk][n] * keys.kPiece,
+                held.load_k(k_pool + (uint64_t)spots[wk][n] * keys.kPiece,
                         k_pool + (uint64_t)spots[wk][16 + n] * keys.kPiece, q4);
             else
-                h.load_k(k_pool + keys.offset_of(min(first + n, c1 - 1)),
+                held.load_k(k_pool + keys.offset_of(min(first + n, c1 - 1)),
                         k_pool + keys.offset_of(min(first + 16 + n, c1 - 1)), q4);
         };
-        const auto load_ctx_v = [&](Held<T, D, FP4> &h, uint32_t first) {
+        const auto load_ctx_v = [&](uint32_t first) {
             if constexpr (kShare) {
                 const u32x4 at0 = *reinterpret_cast<const u32x4 *>(&spots[wk][key_of(q4, 0)]),
                             at1 = *reinterpret_cast<const u32x4 *>(&spots[wk][key_of(q4, 4)]);
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    h.load_v(i, v_pool + (uint64_t)(i < 4 ? at0[i] : at1[i - 4]) * keys.kPiece, n);
+                    held.load_v(i, v_pool + (uint64_t)(i < 4 ? at0[i] : at1[i - 4]) * keys.kPiece, n);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    h.load_v(i, v_pool + keys.offset_of(min(first + key_of(q4, i), c1 - 1)), n);
+                    held.load_v(i, v_pool + keys.offset_of(min(first + key_of(q4, i), c1 - 1)), n);
             }
         };
         // element j + e of the lane's D/16 elements of keys 2i and 2i + 1 side by side
@@ -985,14 +986,10 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
         };
 
         // the chunk of the context
-#pragma unroll
-        for (int i = 0; i < kAhead; i++) {
-            const uint32_t first = c0 + (i * kWaves + wk) * kTile;
-            if (first < c1) {
-                find(first);
-                load_ctx_k(waiting[i], first);
-                load_ctx_v(waiting[i], first);
-            }
+        if (c0 + wk * kTile < c1) {
+            find(c0 + wk * kTile);
+            load_ctx_k(c0 + wk * kTile);
+            load_ctx_v(c0 + wk * kTile);
         }
         if constexpr (FP4)   // while the first tiles are on their way
             if (w.last)
@@ -1002,42 +999,36 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
         f32x4 score[NT][2];
         float tops[NT];
 #pragma unroll 1
-        for (uint32_t first0 = c0 + wk * kTile; first0 < c1; first0 += kAhead * kWaves * kTile) {
+        for (uint32_t first = c0 + wk * kTile; first < c1; first += kWaves * kTile) {
+            const uint32_t next = first + kWaves * kTile;
+            const auto key = [&](int k, V8 *x) {
 #pragma unroll
-            for (int a = 0; a < kAhead; a++) {
-                const uint32_t first = first0 + a * kWaves * kTile, next = first + kAhead * kWaves * kTile;
-                if (a > 0 && first >= c1)
-                    break;
-                Held<T, D, FP4> &h = waiting[a];
-                const auto key = [&](int k, V8 *x) {
-#pragma unroll
-                    for (int i = 0; i < 4 && k + i / 2 < KS; i++)
-                        x[i] = __builtin_bit_cast(V8, h.key(i % 2, k + i / 2, q4));
-                };
-                const auto values = [&](int j, V8 *x) {
-                    pair_up(j, x, [&](int i, int p) { return h.value(i, p, n); });
-                };
-                const bool some = first + kTile > c1;
-                const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
-                        score, tops);
-                // Past the end the last key once more: with a branch here, or below, the compiler no longer knows how many loads
-                // are on their way after the keys', and waits for the values as well before the first product.
-                if (kShare || next < c1) {
-                    find(next);
-                    load_ctx_k(h, next);
-                }
-                if (some) {
-                    // values of keys past the end meet weights of 0 and have to be finite: 0
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        h.clear_v(i, key_of(q4, i) < c1 - first);
-                }
-                if (raise)
-                    rows.raise_maxima(g, tops);
-                rows.apply(g, score, values);
-                if (kShare || next < c1)
-                    load_ctx_v(h, next);
+                for (int i = 0; i < 4 && k + i / 2 < KS; i++)
+                    x[i] = __builtin_bit_cast(V8, held.key(i % 2, k + i / 2, q4));
+            };
+            const auto values = [&](int j, V8 *x) {
+                pair_up(j, x, [&](int i, int p) { return held.value(i, p, n); });
+            };
+            const bool some = first + kTile > c1;
+            const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
+                    score, tops);
+            // Past the end the last key once more: with a branch here, or below, the compiler no longer knows how many loads
+            // are on their way after the keys', and waits for the values as well before the first product.
+            if (kShare || next < c1) {
+                find(next);
+                load_ctx_k(next);
             }
+            if (some) {
+                // values of keys past the end meet weights of 0 and have to be finite: 0
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    held.clear_v(i, key_of(q4, i) < c1 - first);
+            }
+            if (raise)
+                rows.raise_maxima(g, tops);
+            rows.apply(g, score, values);
+            if (kShare || next < c1)
+                load_ctx_v(next);
         }
 
         // the drafted nodes, and before them the zone, with the sequence's last chunk

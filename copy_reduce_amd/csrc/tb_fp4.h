@@ -10,9 +10,6 @@ namespace tbk {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Bytes of a head of D elements in 4 bits: codes, then a power of two for each 32 of them, see tb_serve.h.
-constexpr uint32_t fp4_bytes(int head_dim) { return TB_FP4_HEAD_BYTES(head_dim); }
-
 // The i-th byte of x as what a block's elements are multiplied by.
 __device__ __forceinline__ float power_of(uint32_t x, uint32_t i) {
     return __uint_as_float((x >> (8 * i) & 0xff) << 23);

@@ -142,6 +142,21 @@ def test_lists_of_many_tokens_and_wide_heads(dim, heads, n, layout):
     assert torch.equal(got, exp)
 
 
+def test_more_work_than_a_grid_has_room_for():
+    """4.4 million listed tokens of 9 heads of 1,024, a workgroup each: all but a few are padding."""
+    note("a list of 4.4 million tokens in 4 bits")
+    n, real = 4_400_000, [0, 1, 999_999, 2_097_152, 4_194_304, 4_399_999]
+    c, m, g = make([len(real)], heads=9, dim=1024, pt=4)
+    new = torch.randn(2, 3, 9, 1024, generator=g).to(torch.bfloat16)
+    seqs, at, index = [torch.full((n,), x, dtype=torch.int32) for x in (-1, 0, 1)]
+    for i, r in enumerate(real):
+        seqs[r], at[r], index[r] = 0, i, i % 3
+    c.append(new.cuda(), seqs.cuda(), at.cuda(), index.cuda())
+    got = c.read(ints([0] * len(real)), ints(list(range(len(real))))).cpu()
+    assert c.flags() == 0
+    assert torch.equal(got, decode(encode(new), 1024).to(torch.bfloat16)[:, [i % 3 for i in range(len(real))]])
+
+
 def test_every_value_of_both_types():
     """Each of the 65,536 bit patterns as an element beside a largest one that sets the power."""
     for dtype in DTYPES:

@@ -158,3 +158,29 @@ def test_batches_that_fill_the_chip(batch, t, group):
     else:
         mask = tree_mask(g, batch, t)
         run(c, m, q, k, v, order, 800, 4, mask, [t - (i % 3) * 20 for i in range(batch)], depths_of(mask), what="trees")
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["16 bits", "4 bits"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_the_same_call_gives_the_same_result(dim, dtype, fp4):
+    """Many calls in a row, each form after another one whose values are still in registers and LDS."""
+    from copy_reduce_amd.torch_api import PagedCache, fp4_head_bytes, tree_attention
+    note(f"the same calls again and again, dim {dim} {dtype} 4 bits: {fp4}")
+    c, m, g = setup([3, 97, 260, 301], heads=2, dim=dim, pt=16, layout="token", dtype=dtype, seed=dim, room=0)
+    if fp4:
+        kv = torch.zeros(2, c.num_pages, 16, 2, fp4_head_bytes(dim), dtype=torch.uint8, device="cuda")
+        small = PagedCache(kv, 16, c.max_seqs, c.max_pages, fp4=dtype)
+        seqs, lens = ints([0, 1, 2, 3]), ints([3, 97, 260, 301])
+        small.resize(seqs, lens)
+        who = ints([q for q, n in enumerate([3, 97, 260, 301]) for _ in range(n)])
+        at = ints([p for n in [3, 97, 260, 301] for p in range(n)])
+        small.append(c.read(who, at), who, at)
+        c = small
+    s = ints([2, 0, 3, 1])
+    for t, hq in ((1, 2), (3, 8), (1, 8), (4, 4)):
+        q, k, v = [x.cuda() for x in inputs(g, 4, t, hq, 2, dim, dtype)]
+        for window in (50, None, 90):
+            got = [tree_attention(q, k, v, c, 0, s, window=window, sinks=6 if window else 0) for _ in range(150)]
+            out, lse = torch.stack([o for o, _ in got]), torch.stack([x for _, x in got])
+            assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse)), (t, hq, window)
