@@ -565,9 +565,14 @@ struct Rows {
                         s[t][z] = Mfma<T>::mul(x[2 * e + z], q[t][k + e], s[t][z]);
         }
         // The results may be read 8 states after the last product.  The compiler counts them on the way through the branch below
-        // and not on the way past it, where two to three were left, too few: now and then what the registers had before came out.
+        // and not on the way past it.  With NT 1 it left 2 to 6 there, and now and then what the registers had before came out;
+        // with NT 2 it leaves enough only by the order of its reads.  So all results are tied to the wait: trees of 64
+        // nodes take 1 % longer over 4 bits and over windows, and what they took in 16 bits.
         if constexpr (NT == 1)
             asm volatile("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
+        else
+            asm volatile("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+        static_assert(NT <= 2, "the wait names each result");
         if (some) {
 #pragma unroll
             for (int t = 0; t < NT; t++)
