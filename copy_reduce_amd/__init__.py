@@ -24,4 +24,6 @@ from ._tb import (  # noqa: F401
 from ._tb_cache import (  # noqa: F401
     TB_CACHE_BUSY, TB_CACHE_RANGE, TB_CACHE_SHARED, TB_CACHE_SHORT, TB_CACHE_TWICE, TB_MAX_POOLS,
 )
-from ._tb_serve import TB_FP4_BLOCK, TB_FP4_HEAD_BYTES, TB_VERIFY_MAX_VOCAB  # noqa: F401
+from ._tb_serve import (  # noqa: F401
+    TB_FP4_BLOCK, TB_FP4_HEAD_BYTES, TB_VERIFY_MAX_ENTRIES, TB_VERIFY_MAX_VOCAB,
+)

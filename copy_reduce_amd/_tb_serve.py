@@ -9,6 +9,7 @@ from ._tb_cache import _check, tb_cache, tb_tree_attn
 
 TB_FP32 = 2   # beside TB_BF16 and TB_FP16
 TB_VERIFY_MAX_VOCAB = 1 << 24
+TB_VERIFY_MAX_ENTRIES = 1 << 38
 TB_FP4_BLOCK = 32
 
 # Every symbol include/tb_serve.h declares.

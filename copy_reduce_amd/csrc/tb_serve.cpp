@@ -178,7 +178,9 @@ int tb_verify_workspace(const tb_verify *v, uint64_t *bytes_out) {
 }
 
 int tb_verify_drafts(const tb_verify *v, void *stream) {
-    if (!verify_sizes_ok(v) || v->nodes < 1 || v->nodes > (1u << 12) || v->dtype > TB_FP32)
+    // more entries and the second kernel's grid would pass 2^32 threads, after the first one has run
+    if (!verify_sizes_ok(v) || v->nodes < 1 || v->nodes > (1u << 12) || v->dtype > TB_FP32 ||
+        (uint64_t)v->batch * v->vocab > TB_VERIFY_MAX_ENTRIES)
         return TB_ERR_INVALID;
     if (v->batch == 0)
         return TB_OK;

@@ -542,8 +542,10 @@ def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tens
         raise ValueError("probs must be a float32, bfloat16 or float16 CUDA tensor [batch, nodes, vocab], "
                          "the vocabulary contiguous")
     b, t, vocab = probs.shape
-    if not (1 <= t <= 4096 and b <= 65536 and 1 <= vocab <= _tb_serve.TB_VERIFY_MAX_VOCAB):
-        raise ValueError("probs must have 1 to 4096 nodes, up to 65536 sequences and 2^24 entries of the vocabulary")
+    if not (1 <= t <= 4096 and b <= 65536 and 1 <= vocab <= _tb_serve.TB_VERIFY_MAX_VOCAB
+            and b * vocab <= _tb_serve.TB_VERIFY_MAX_ENTRIES):
+        raise ValueError("probs must have 1 to 4096 nodes, up to 65536 sequences and 2^24 entries of the vocabulary, "
+                         "2^38 of all sequences together")
     if draft_probs is not None and (draft_probs.dtype != probs.dtype or draft_probs.device != dev
                                     or draft_probs.shape != probs.shape
                                     or (vocab > 1 and draft_probs.stride(2) != 1)):

@@ -25,6 +25,8 @@ enum { TB_FP32 = 2 };
 
 /* Most entries of the vocabulary. */
 #define TB_VERIFY_MAX_VOCAB (1u << 24)
+/* Most entries of all sequences' vocabularies together, batch * vocab. */
+#define TB_VERIFY_MAX_ENTRIES (1ull << 38)
 
 /*
  * For each sequence b a tree of drafted tokens, node 0 its root: the last token
@@ -61,7 +63,8 @@ typedef struct tb_verify {
     const int32_t *parents;       /* device, [batch][nodes], or NULL: chains, parent t - 1         */
     const float *uniform;         /* device, [batch][nodes]                                        */
     const int32_t *tree_nodes;    /* device, [batch]: how many of the nodes are real; NULL: all    */
-    uint32_t batch, nodes, vocab; /* batch <= 2^16, nodes <= 2^12, vocab <= TB_VERIFY_MAX_VOCAB    */
+    uint32_t batch, nodes, vocab; /* batch <= 2^16, nodes <= 2^12, vocab <= TB_VERIFY_MAX_VOCAB,
+                                     batch * vocab <= TB_VERIFY_MAX_ENTRIES                        */
     uint32_t dtype;               /* TB_BF16, TB_FP16 or TB_FP32, of both distributions            */
     int32_t *count;               /* device, [batch]: accepted nodes, the root among them          */
     int32_t *path;                /* device, [batch][nodes]: their numbers, then -1                */
