@@ -312,6 +312,9 @@ static int attention(const tb_tree_attn *a, const tb_attn_view &view, const tb_c
         return TB_ERR_INVALID;
     if (a->batch == 0 || a->nodes == 0)
         return TB_OK;
+    // few rows deal sequences to the 8 XCDs, a workgroup of 256 threads a head and sequence
+    if (fp4 && ((uint64_t)a->batch + 7) / 8 * 8 * c->heads >= (1u << 24))
+        return TB_ERR_INVALID;
     const uint64_t piece = fp4 ? 4 : 16;
     if (!aligned(c->pools[a->k_pool], piece) || !aligned(c->pools[a->v_pool], piece) || c->page_stride % piece != 0 ||
         c->page_stride * c->num_pages > (fp4 ? TB_ATTN_MAX_POOL_FP4 : TB_ATTN_MAX_POOL) || a->q == nullptr

@@ -153,7 +153,8 @@ typedef struct tb_attn_view {
     uint32_t sinks;
     const int32_t *depths;        /* device, [batch][nodes], each taken within 0 .. the tree's nodes - 1;
                                      NULL: node t's is t, for chains (a mask with a window needs them) */
-    uint32_t fp4;                 /* 1: the cache is held in 4 bits (TB_FP4_HEAD_BYTES(head_dim))   */
+    uint32_t fp4;                 /* 1: the cache is held in 4 bits (TB_FP4_HEAD_BYTES(head_dim)); the batch
+                                     rounded up to a multiple of 8, times cache->heads is < 2^24   */
 } tb_attn_view;
 
 /* Largest pool held in 4 bits that tb_view_attention reads: page_stride * num_pages. */
