@@ -151,20 +151,19 @@ static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count, uint64_
     return p;
 }
 
-// With a window, whose keys are counted beforehand, many rows of few keys can be divided instead of the keys, so that
-// every workgroup has a whole sequence and nothing is joined: 16 trees of 64 nodes, windows of 2,000 tokens, 84 us with halves of
-// the keys, 62.5 with halves of the rows.
-// Few rows: where the table has room for contexts of four windows and more, most sequences show a whole one, and if
-// these fill the chip's rounds to nine tenths a workgroup takes one: 64 sequences of up to 32,767 tokens, windows of
-// 4,096, 190 us against 198 with shares.
+// With a window the table says nothing about how many keys a sequence shows, and what the lengths are is not known here.
+//
+// Many rows of few keys are divided instead of the keys, so that every workgroup has a whole sequence and nothing is joined.
+// 16 trees of 64 nodes by rows and by shares, of up to 16,383 tokens and one of 16,000 among 15 of some 100: windows of 2,000
+// 62.5 us and 83, 60 and 49; of 4,000 103 and 107, 98 and 37, where the gain is no longer worth it.
+//
+// Few rows are shared out as without a window.  64 sequences, windows of 4,096, by shares and by a workgroup a sequence
+// and head: of up to 32,767 tokens 192 us and 186, in 4 bits 81 and 71; of up to 8,192 tokens 161 and 173, 54 and 50;
+// 60 of up to 300 tokens and 4 of 32,000 42 and 143, 27 and 48.
+constexpr uint64_t kShortWindow = 2048;
 static Plan plan_of_window(const tb_tree_attn &a, uint32_t heads, int cu_count, uint64_t longest, uint64_t table) {
-    Plan p = plan_of(a, heads, cu_count, longest);
-    if (!p.shape.shared && table >= 4 * longest) {
-        const uint64_t units = (uint64_t)a.batch * heads, room = (uint64_t)cu_count * resident(p.shape, a.head_dim);
-        if (10 * units >= 9 * ((units + room - 1) / room * room))
-            p.budget = 0;
-    }
-    if (!p.shape.shared || p.budget == 0 || longest > kShortMany)
+    Plan p = plan_of(a, heads, cu_count, longest <= kShortWindow ? longest : table);
+    if (!p.shape.shared || p.budget == 0 || longest > kShortWindow)
         return p;
     for (int wm = p.shape.wm; wm >= (a.head_dim <= 128 ? 2 : 4); wm /= 2) {
         const uint32_t rows = wm * 16 * shared_nt((int)a.head_dim), blocks = (p.rows + rows - 1) / rows;
