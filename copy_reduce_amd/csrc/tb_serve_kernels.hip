@@ -409,13 +409,18 @@ struct Walk {
 
 constexpr uint32_t kDraw = 1024, kDrawWaves = kDraw / 64;   // threads and waves of a workgroup
 constexpr uint32_t kMaxStretch = 8192, kMaxStretches = 4096;
-// Elements of a stretch: enough for a workgroup on each CU, which all run at once, but no more stretches than there is room
-// for in LDS.  Stretches of 1,024 at least instead of 512: 16 chains over 131,072 tokens 23.2 us against 19.5; workgroups of 512
+// Elements of a stretch: small enough that a workgroup's waves all have one, where that takes no more workgroups, and that
+// there are up to as many workgroups as CUs, which all run at once; but no more stretches than there is room for in LDS.
+// Halved until there are at least as many workgroups as CUs, whatever their waves have, 16 bits: 255 chains over 32,000 tokens
+// 34 us against 22, 256 of them 26 against 22, 130 over 131,072 tokens 44 against 35.
+// Stretches of 1,024 at least instead of 512: 16 chains over 131,072 tokens 23.2 us against 19.5; workgroups of 512
 // threads, two on a CU: 25.5, and 64 such chains 29.6 against 30.3.
+constexpr uint32_t kDrawGroups = 256;
 static uint32_t stretch_of(uint32_t batch, uint32_t vocab) {
+    const auto groups = [&](uint32_t n) { return (vocab + n * kDrawWaves - 1) / (n * kDrawWaves); };
     uint32_t n = kMaxStretch;
-    while (n > 512 && (uint64_t)batch * ((vocab + n * kDrawWaves - 1) / (n * kDrawWaves)) < 256
-            && (vocab + n / 2 - 1) / (n / 2) <= kMaxStretches)
+    while (n > 512 && (vocab + n / 2 - 1) / (n / 2) <= kMaxStretches
+            && (groups(n / 2) == groups(n) || (uint64_t)batch * groups(n / 2) <= kDrawGroups))
         n /= 2;
     return n;
 }
