@@ -545,8 +545,8 @@ struct Rows {
     // maxima have to be raised in between, which is rare.
     //
     // keys(k, x): x[2 e + z] becomes step k + e's operand for keys 16 z .. 16 z + 15, e and z 0 and 1;
-    // keep(t, i): whether row t * 16 + n sees the lane's i-th key, asked only if `some` row may not see all.
-    template <typename Keys2, typename Keep>
+    // keep(t, i): whether row t * 16 + n sees the lane's i-th key, asked only if `some` row may not see all (MASKED: always).
+    template <bool MASKED, typename Keys2, typename Keep>
     __device__ __forceinline__ bool scores(const AttnArgs &g, bool some, Keys2 keys, Keep keep, f32x4 (&s)[NT][2],
             float (&tops)[NT]) {
 #pragma unroll
@@ -567,8 +567,11 @@ struct Rows {
         // The results may be read 8 states after the last product.  The compiler counts them on the way through the branch below
         // and not on the way past it.  With NT 1 it left 2 to 6 there, and now and then what the registers had before came out;
         // with NT 2 it leaves enough only by the order of its reads.  So all results are tied to the wait: trees of 64
-        // nodes take 1 % longer over 4 bits and over windows, and what they took in 16 bits.
-        if constexpr (NT == 1)
+        // nodes take 1 % longer over 4 bits, those of 8 nodes 1 % less, a chain of 1,024 over a window of 256 3 % longer, the
+        // others what they took.  MASKED has no branch (trees over windows 61.3 us against 61.9 with the wait there as well).
+        if constexpr (MASKED)
+            some = true;
+        else if constexpr (NT == 1)
             asm volatile("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
         else
             asm volatile("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
@@ -1015,7 +1018,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
                 pair_up(j, x, [&](int i, int p) { return held.value(i, p, n); });
             };
             const bool some = first + kTile > c1;
-            const bool raise = rows.scores(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
+            const bool raise = rows.template scores<false>(g, some, key, [&](int, int i) { return key_of(q4, i) < c1 - first; },
                     score, tops);
             // Past the end the last key once more: with a branch here, or below, the compiler no longer knows how many loads
             // are on their way after the keys', and waits for the values as well before the first product.
@@ -1088,7 +1091,7 @@ __global__ __launch_bounds__(64 * kWaves, few_resident(D)) void tree_attention_k
                     const auto values16 = [&](int j, V8 *x) {
                         pair_up(j, x, [&](int i, int p) { return held.value(i, p, n); });
                     };
-                    if (rows.scores(g, true, key16, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
+                    if (rows.template scores<true>(g, true, key16, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
                             score, tops))
                         rows.raise_maxima(g, tops);
                     rows.apply(g, score, values16);
@@ -1391,7 +1394,7 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
             const auto look = [&] {
                 tile_at = uniform(data_at + buffer * 2 * kBuffer + (turn * WK + wk) * kTileBytes);
                 const uint32_t t0 = first + (turn * WK + wk) * kTile;
-                return rows.scores(g, t0 + kTile > c1, key, [&](int, int i) { return t0 + key_of(q4, i) < c1; },
+                return rows.template scores<false>(g, t0 + kTile > c1, key, [&](int, int i) { return t0 + key_of(q4, i) < c1; },
                         score, tops);
             };
             bool raise = look();
@@ -1489,7 +1492,7 @@ __global__ __launch_bounds__(64 * kSharedWaves, 2) void tree_attention_shared_ke
                     if (!in_zone)
                         bits[t] = keys.seen(row0 + t * 16 + n, begin);
                 }
-                if (rows.scores(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
+                if (rows.template scores<true>(g, true, key, [&](int t, int i) { return (bits[t] >> key_of(q4, i) & 1) != 0; },
                         score, tops))
                     rows.raise_maxima(g, tops);
                 rows.apply(g, score, values);
