@@ -155,7 +155,7 @@ static Plan plan_of(const tb_tree_attn &a, uint32_t heads, int cu_count, uint64_
 //
 // Many rows of few keys are divided instead of the keys, so that every workgroup has a whole sequence and nothing is joined.
 // 16 trees of 64 nodes by rows and by shares, of up to 16,383 tokens and one of 16,000 among 15 of some 100: windows of 2,000
-// 62.5 us and 83, 60 and 49; of 4,000 103 and 107, 98 and 37, where the gain is no longer worth it.
+// 61.5 us and 83, 59 and 49; of 4,000 103 and 107, 98 and 37, where the gain is no longer worth it.
 //
 // Few rows are shared out as without a window.  64 sequences, windows of 4,096, by shares and by a workgroup a sequence
 // and head: of up to 32,767 tokens 192 us and 186, in 4 bits 81 and 71; of up to 8,192 tokens 161 and 173, 54 and 50;
